@@ -93,6 +93,10 @@ enum {
   INTLORA_AUX_STUDENT_T2 = 3 /* Student-t with 2 degrees of freedom                            */
 };
 
+/* Floating-point element types of the 8-bit floating-point and grouped layers and of the
+ * gradient calls below. */
+enum { INTLORA_BF16 = 0, INTLORA_FP16 = 1, INTLORA_FP32 = 2 };
+
 /* One pretrained layer.  r is the LoRA rank (1..128); w_bits the base code width
  * (4 or 8); (seed, layer_id) select the auxiliary-matrix stream and aux_dist its law. */
 typedef struct intlora_desc {
@@ -363,6 +367,76 @@ int intlora_linear_fwd(int64_t M, int64_t d, int64_t n, const int8_t* xq, const 
 int intlora_linear_fwd_codes(int64_t M, int64_t d, int64_t n, const int8_t* xq, const float* s_x,
                              const uint8_t* u_code, const uint8_t* w_round, const int32_t* z, const int32_t* z_bar,
                              const float* s_bar, uint16_t* Y_bf16, int32_t* acc_dbg, void* stream);
+
+/* ---------------------------------------------------------------------------- */
+/* 8-bit floating-point linear layer, one scale per block of 128, beside the integer one:
+ * for layers whose weights or activations have outliers that one scale per row cannot hold.
+ * Codes are OCP e4m3 (largest magnitude 448).  A block's scale is the power of two 2^e with
+ * the least e >= -127 for which its largest magnitude times 2^-e is at most 448 (e = 0 for a
+ * block of zeros), kept as the byte e + 127; a code is the e4m3 value nearest to x 2^-e
+ * (half to even).  Powers of two lose no relative precision in a floating-point code, and
+ * the matrix cores apply them inside the product.  A block that holds a NaN or an infinity
+ * gets the byte 255 and NaN codes, which make the outputs that use it NaN.
+ * Scale rows have 4 ceil(n / 512) bytes; the bytes past ceil(n / 128) are written 127.
+ *
+ * Activations: blocks of 1 x 128 along each row.  X: M x n (dtype), xq: M x n codes, sx:
+ * M x 4 ceil(n / 512).  n a multiple of 16; n, d <= 2^20, M < 2^31.  M = 0 is a no-op. */
+int intlora_fp8_quant_act(int64_t M, int64_t n, int dtype, const void* X, uint8_t* xq, uint8_t* sx, void* stream);
+
+/* Weights: blocks of 128 x 128 of each of the E matrices d x n (E = 1 for one layer).
+ * wq: E x d x n codes; sw: E x ceil(d / 128) x 4 ceil(n / 512).  wq_t, sw_t (both or
+ * neither; d a multiple of 16): the same codes transposed, E x n x d, with scale rows
+ * E x ceil(n / 128) x 4 ceil(d / 512) -- the weight of the input gradient dX = dY W, which is
+ * this layer's product on them.  n a multiple of 16.  E <= 4096. */
+int intlora_fp8_quant_weight(int64_t E, int64_t d, int64_t n, int dtype, const void* W, uint8_t* wq, uint8_t* sw,
+                             uint8_t* wq_t, uint8_t* sw_t, void* stream);
+
+/* Y[t, i] = bf16( sum over blocks b of 2^(sx[t, b] + sw[i / 128, b] - 254) sum_{k in b}
+ * xq[t, k] wq[i, k] ), accumulated in binary32 in an order fixed by the sizes.  n a multiple
+ * of 16, any d and M (few tokens, M <= 32, take a weight-streaming kernel). */
+int intlora_fp8_linear_fwd(int64_t M, int64_t d, int64_t n, const uint8_t* xq, const uint8_t* sx, const uint8_t* wq,
+                           const uint8_t* sw, uint16_t* Y_bf16, void* stream);
+
+/* Products grouped by expert.  M token rows are sorted by expert; expert e of E owns the rows
+ * offsets[e] .. offsets[e + 1] - 1 (offsets: E + 1 ascending int64 on the device; a group may
+ * be empty).  Rows outside every group are neither read nor written.  An entry outside [0, M]
+ * counts as the nearer end and one below its predecessor as that predecessor, so no call
+ * touches memory outside its tensors.  offsets = NULL with E = 1: one group of all M rows.
+ * E <= 4096.  The 8-bit form, with X and W as quantized above: */
+int intlora_fp8_grouped_linear_fwd(int64_t M, int64_t E, int64_t d, int64_t n, const uint8_t* xq, const uint8_t* sx,
+                                   const int64_t* offsets, const uint8_t* wq, const uint8_t* sw, uint16_t* Y_bf16,
+                                   void* stream);
+
+/* The same in bf16 / fp16 (dtype; inputs and outputs; binary32 accumulation in an order fixed
+ * by the sizes, one rounding at the end), d and n multiples of 8:
+ *   forward  Y[t, :] = W_e X[t, :]          X: M x n, W: E x d x n, Y: M x d;
+ *   dx       dX[t, :] = W_e^T dY[t, :]      dY: M x d, dX: M x n;
+ *   dw       dW_e = sum_{t in e} dY[t, :] X[t, :]^T, zeros for an empty group: E x d x n, in
+ *            dtype or (out_dtype) INTLORA_FP32.  With E = 1 and fp32 this is the G that
+ *            intlora_ste_backward takes. */
+int intlora_grouped_linear_fwd(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, const void* X,
+                               const int64_t* offsets, const void* W, void* Y, void* stream);
+int intlora_grouped_linear_dx(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, const void* dY,
+                              const int64_t* offsets, const void* W, void* dX, void* stream);
+int intlora_grouped_linear_dw(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype, const void* dY,
+                              const void* X, const int64_t* offsets, void* dW, void* stream);
+
+/* Global gradient norm and clipping over a list of tensors (the next call after
+ * intlora_ste_backward has filled dA and dB of every layer).  grads, out, numel and dtype are
+ * HOST arrays of `count` entries (device pointers, 16-byte aligned; element counts >= 0;
+ * INTLORA_BF16 / _FP16 / _FP32 each), read before the call returns; count <= 65536.
+ *   sumsq[0] = sum of g^2 over all tensors, in binary64 in a fixed order.  (Ranks that hold
+ *   parts of the gradients add their sums before the second call.)
+ *   out_i = RN(g c), c = RN32(min(1, max_norm / (sqrt(sumsq) + 1e-6))) -- a NaN sum gives NaN
+ *   outputs and an infinite one zeros (NaN for infinite gradients); norm_out[0] =
+ *   RN32(sqrt(sumsq)), or NULL.  out_i may be grads_i (in place); outputs must not otherwise
+ *   overlap inputs or each other: INTLORA_EINVAL.  max_norm >= 0.
+ * Workspace of the sum: intlora_grad_ws_bytes (8 bytes per 16384 elements or part). */
+size_t intlora_grad_ws_bytes(int64_t count, const int64_t* numel);
+int intlora_grad_sumsq(int64_t count, const void* const* grads, const int64_t* numel, const int32_t* dtype,
+                       double* sumsq, void* ws, size_t ws_bytes, void* stream);
+int intlora_grad_clip(int64_t count, const void* const* grads, void* const* out, const int64_t* numel,
+                      const int32_t* dtype, const double* sumsq, double max_norm, float* norm_out, void* stream);
 
 /* Diagnostic: the binary32 natural log used by intlora_gen_r, on g = G * 2^-23 for
  * odd G in [1, 2^23) (the only values it is ever given): out[t] = RN32(ln(G[t] 2^-23)).

@@ -20,6 +20,7 @@ INTLORA_W_INT4, INTLORA_W_INT8, INTLORA_W_INT16, INTLORA_W_INT16_PLANES = 4, 8, 
 INTLORA_AUX_LAPLACE, INTLORA_AUX_GAUSS, INTLORA_AUX_CAUCHY, INTLORA_AUX_STUDENT_T2 = 0, 1, 2, 3
 INTLORA_OP_STATS_UMINMAX, INTLORA_OP_MERGE_MUL, INTLORA_OP_MERGE_SHIFT, INTLORA_OP_LINEAR, INTLORA_OP_BASE_QUANT = 1, 2, 3, 4, 5
 INTLORA_OP_MERGE_PTQ, INTLORA_OP_STE_BACKWARD = 6, 7
+INTLORA_BF16, INTLORA_FP16, INTLORA_FP32 = 0, 1, 2
 
 
 class IntLoraError(RuntimeError):
@@ -76,6 +77,16 @@ _SIG = {
     "intlora_quant_act": (_INT, [_I64, _I64, _P, _P, _P, _P, _P]),
     "intlora_linear_fwd": (_INT, [_I64, _I64, _I64, _P, _P, _P, _INT, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "intlora_linear_fwd_codes": (_INT, [_I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "intlora_fp8_quant_act": (_INT, [_I64, _I64, _INT, _P, _P, _P, _P]),
+    "intlora_fp8_quant_weight": (_INT, [_I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _P]),
+    "intlora_fp8_linear_fwd": (_INT, [_I64, _I64, _I64, _P, _P, _P, _P, _P, _P]),
+    "intlora_fp8_grouped_linear_fwd": (_INT, [_I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P]),
+    "intlora_grouped_linear_fwd": (_INT, [_I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P]),
+    "intlora_grouped_linear_dx": (_INT, [_I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P]),
+    "intlora_grouped_linear_dw": (_INT, [_I64, _I64, _I64, _I64, _INT, _INT, _P, _P, _P, _P, _P]),
+    "intlora_grad_ws_bytes": (ctypes.c_size_t, [_I64, _P]),
+    "intlora_grad_sumsq": (_INT, [_I64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "intlora_grad_clip": (_INT, [_I64, _P, _P, _P, _P, _P, ctypes.c_double, _P, _P]),
     "intlora_debug_ln": (_INT, [_I64, _P, _P, _P]),
     "intlora_debug_aux": (_INT, [_I64, _P, ctypes.c_uint32, _P, _P]),
     "intlora_debug_mfma_chain": (_INT, [_INT, _I64, _I64, _INT, _P, _P, _P, _P]),
@@ -248,6 +259,60 @@ def intlora_linear_fwd_codes(M: int, d: int, n: int, xq, s_x, u_code, w_round, z
     _check(lib().intlora_linear_fwd_codes(M, d, n, _ptr(xq), _ptr(s_x), _ptr(u_code), _ptr(w_round), _ptr(z),
                                           _ptr(z_bar), _ptr(s_bar), _ptr(Y_bf16), _ptr(acc_dbg), _stream(stream)),
            "intlora_linear_fwd_codes")
+
+
+def intlora_fp8_quant_act(M: int, n: int, dtype: int, X, xq, sx, stream=None):
+    _check(lib().intlora_fp8_quant_act(M, n, dtype, _ptr(X), _ptr(xq), _ptr(sx), _stream(stream)),
+           "intlora_fp8_quant_act")
+
+
+def intlora_fp8_quant_weight(E: int, d: int, n: int, dtype: int, W, wq, sw, wq_t=None, sw_t=None, stream=None):
+    _check(lib().intlora_fp8_quant_weight(E, d, n, dtype, _ptr(W), _ptr(wq), _ptr(sw), _ptr(wq_t), _ptr(sw_t),
+                                          _stream(stream)), "intlora_fp8_quant_weight")
+
+
+def intlora_fp8_linear_fwd(M: int, d: int, n: int, xq, sx, wq, sw, Y_bf16, stream=None):
+    _check(lib().intlora_fp8_linear_fwd(M, d, n, _ptr(xq), _ptr(sx), _ptr(wq), _ptr(sw), _ptr(Y_bf16),
+                                        _stream(stream)), "intlora_fp8_linear_fwd")
+
+
+def intlora_fp8_grouped_linear_fwd(M: int, E: int, d: int, n: int, xq, sx, offsets, wq, sw, Y_bf16, stream=None):
+    _check(lib().intlora_fp8_grouped_linear_fwd(M, E, d, n, _ptr(xq), _ptr(sx), _ptr(offsets), _ptr(wq), _ptr(sw),
+                                                _ptr(Y_bf16), _stream(stream)), "intlora_fp8_grouped_linear_fwd")
+
+
+def intlora_grouped_linear_fwd(M: int, E: int, d: int, n: int, dtype: int, X, offsets, W, Y, stream=None):
+    _check(lib().intlora_grouped_linear_fwd(M, E, d, n, dtype, _ptr(X), _ptr(offsets), _ptr(W), _ptr(Y),
+                                            _stream(stream)), "intlora_grouped_linear_fwd")
+
+
+def intlora_grouped_linear_dx(M: int, E: int, d: int, n: int, dtype: int, dY, offsets, W, dX, stream=None):
+    _check(lib().intlora_grouped_linear_dx(M, E, d, n, dtype, _ptr(dY), _ptr(offsets), _ptr(W), _ptr(dX),
+                                           _stream(stream)), "intlora_grouped_linear_dx")
+
+
+def intlora_grouped_linear_dw(M: int, E: int, d: int, n: int, dtype: int, out_dtype: int, dY, X, offsets, dW,
+                              stream=None):
+    _check(lib().intlora_grouped_linear_dw(M, E, d, n, dtype, out_dtype, _ptr(dY), _ptr(X), _ptr(offsets), _ptr(dW),
+                                           _stream(stream)), "intlora_grouped_linear_dw")
+
+
+def intlora_grad_ws_bytes(numel) -> int:
+    """numel: a ctypes int64 array (host)."""
+    return int(lib().intlora_grad_ws_bytes(len(numel), numel))
+
+
+def intlora_grad_sumsq(grads, numel, dtype, sumsq, ws, stream=None):
+    """grads, numel, dtype: ctypes arrays of pointers, int64 and int32 (host)."""
+    wsb = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().intlora_grad_sumsq(len(numel), grads, numel, dtype, _ptr(sumsq), _ptr(ws), wsb, _stream(stream)),
+           "intlora_grad_sumsq")
+
+
+def intlora_grad_clip(grads, out, numel, dtype, sumsq, max_norm: float, norm_out=None, stream=None):
+    """grads, out, numel, dtype: ctypes arrays of pointers, pointers, int64 and int32 (host)."""
+    _check(lib().intlora_grad_clip(len(numel), grads, out, numel, dtype, _ptr(sumsq), float(max_norm),
+                                   _ptr(norm_out), _stream(stream)), "intlora_grad_clip")
 
 
 def intlora_debug_ln(count: int, G, out, stream=None):

@@ -1,9 +1,12 @@
 // C ABI of libintlora.so (declared in include/intlora.h): host-side validation,
 // workspace layout and kernel dispatch.  No allocation, no state across calls.
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "../../include/intlora.h"
 #include "intlora_internal.h"
@@ -258,6 +261,128 @@ int64_t noalloc_rows(int64_t d, int64_t n) {
   return rows;
 }
 
+// ---- floating-point layers and gradients
+constexpr int64_t kMaxFeatures = int64_t(1) << 20;  // d, n: 256 rows of a tile stay below 2^31 bytes
+constexpr int64_t kMaxExperts = 4096;
+constexpr int64_t kMaxGrads = 65536;
+constexpr int64_t kMaxNumel = int64_t(1) << 40;
+
+int check_dtype(int dtype, bool fp32, const char* what) {
+  if (dtype == INTLORA_BF16 || dtype == INTLORA_FP16 || (fp32 && dtype == INTLORA_FP32)) return INTLORA_OK;
+  return fail(INTLORA_EINVAL, "%s: dtype must be INTLORA_BF16, _FP16%s (got %d)", what, fp32 ? " or _FP32" : "", dtype);
+}
+
+int check_layer(int64_t M, int64_t E, int64_t d, int64_t n, const char* what) {
+  if (M < 0 || M >= kMaxDim - 256 || d < 0 || d > kMaxFeatures || n < 1 || n > kMaxFeatures)
+    return fail(INTLORA_ESHAPE, "%s: bad shape M=%lld d=%lld n=%lld (d, n <= 2^20)", what, (long long)M, (long long)d,
+                (long long)n);
+  if (E < 1 || E > kMaxExperts) return fail(INTLORA_ESHAPE, "%s: E must be in [1, 4096] (got %lld)", what, (long long)E);
+  // blocks of the largest grid any of these calls makes (tiles of 64 x 64)
+  const int64_t row_tiles = (M + 63) / 64 + E, dt = (d + 63) / 64, nt = (n + 63) / 64;
+  if (row_tiles * (dt > nt ? dt : nt) >= kMaxDim - 256 || E * dt * nt >= kMaxDim - 256)
+    return fail(INTLORA_ESHAPE, "%s: too many tiles", what);
+  return INTLORA_OK;
+}
+
+int check_offsets(int64_t E, const int64_t* offsets, const char* what) {
+  if (!offsets && E != 1) return fail(INTLORA_EINVAL, "%s: offsets may be NULL with E = 1 only", what);
+  return check_opt(offsets, "offsets");
+}
+
+int check_grouped(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype, const int64_t* offsets,
+                  const char* what) {
+  int s = check_dtype(dtype, false, what);
+  if (s) return s;
+  if (out_dtype != dtype && out_dtype != INTLORA_FP32)
+    return fail(INTLORA_EINVAL, "%s: out_dtype must be dtype or INTLORA_FP32 (got %d)", what, out_dtype);
+  if ((s = check_layer(M, E, d, n, what))) return s;
+  if (d % 8 != 0 || n % 8 != 0)
+    return fail(INTLORA_ESHAPE, "%s needs d and n multiples of 8 (got %lld, %lld)", what, (long long)d, (long long)n);
+  return check_offsets(E, offsets, what);
+}
+
+int run_grouped(const char* what, int direction, int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype,
+                const void* tokens, const int64_t* offsets, const void* other, void* out, void* stream) {
+  // without a token row (dW of empty groups only) the token operands are not read
+  int s = M == 0 ? INTLORA_OK : check_ptrs({tokens, other}, what);
+  if (s) return s;
+  if ((s = check_ptrs({out}, what))) return s;
+  if ((s = ensure_device())) return s;
+  return launch_status(intlora::launch_grouped(direction, M, E, d, n, dtype, out_dtype, tokens, offsets, other, out,
+                                               static_cast<hipStream_t>(stream)),
+                       what);
+}
+
+int fp8_linear(const char* what, int64_t M, int64_t E, int64_t d, int64_t n, const uint8_t* xq, const uint8_t* sx,
+               const int64_t* offsets, const uint8_t* wq, const uint8_t* sw, uint16_t* Y, void* stream) {
+  int s = check_layer(M, E, d, n, what);
+  if (s) return s;
+  if (n % 16 != 0) return fail(INTLORA_ESHAPE, "%s needs n a multiple of 16 (got %lld)", what, (long long)n);
+  if (M == 0 || d == 0) return ok();
+  if ((s = check_ptrs({xq, sx, wq, sw, Y}, what))) return s;
+  if ((s = ensure_device())) return s;
+  return launch_status(intlora::launch_fp8_linear(M, E, d, n, xq, sx, offsets, wq, sw, Y,
+                                                  static_cast<hipStream_t>(stream)),
+                       what);
+}
+
+int check_grads(int64_t count, const void* const* grads, const int64_t* numel, const int32_t* dtype,
+                const char* what) {
+  if (count < 0 || count > kMaxGrads)
+    return fail(INTLORA_ESHAPE, "%s: count must be in [0, %lld] (got %lld)", what, (long long)kMaxGrads,
+                (long long)count);
+  if (count > 0 && (!grads || !numel || !dtype)) return fail(INTLORA_EINVAL, "%s: NULL host array", what);
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const int s = check_dtype(dtype[i], true, what);
+    if (s) return s;
+    if (numel[i] < 0 || numel[i] >= kMaxNumel || (total += numel[i]) >= kMaxNumel)
+      return fail(INTLORA_ESHAPE, "%s: bad element count %lld of tensor %lld", what, (long long)numel[i], (long long)i);
+    if (numel[i] == 0) continue;
+    if (!grads[i]) return fail(INTLORA_EINVAL, "%s: tensor %lld is NULL", what, (long long)i);
+    if (!aligned16(grads[i]))
+      return fail(INTLORA_EALIGN, "%s: pointer %p of tensor %lld not 16-byte aligned", what, grads[i], (long long)i);
+  }
+  return INTLORA_OK;
+}
+
+// Outputs present, aligned, and disjoint from every other tensor of the call: otherwise two
+// blocks would write the same element, or one would read what another has scaled.
+int check_clip_outputs(int64_t count, const void* const* grads, void* const* out, const int64_t* numel,
+                       const int32_t* dtype) {
+  if (count == 0) return INTLORA_OK;
+  if (!out) return fail(INTLORA_EINVAL, "grad_clip: NULL host array");
+  struct Range {
+    uintptr_t lo, hi;
+    int64_t tensor;
+    bool output;
+  };
+  std::unique_ptr<Range[]> r(new (std::nothrow) Range[2 * (size_t)count]);
+  if (!r) return fail(INTLORA_EINVAL, "grad_clip: no host memory for %lld tensors", (long long)count);
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (numel[i] == 0) continue;
+    if (!out[i]) return fail(INTLORA_EINVAL, "grad_clip: output %lld is NULL", (long long)i);
+    if (!aligned16(out[i]))
+      return fail(INTLORA_EALIGN, "grad_clip: pointer %p of output %lld not 16-byte aligned", out[i], (long long)i);
+    const uintptr_t bytes = (uintptr_t)numel[i] * (dtype[i] == INTLORA_FP32 ? 4 : 2);
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out[i]), g = reinterpret_cast<uintptr_t>(grads[i]);
+    r[n++] = Range{o, o + bytes, i, true};
+    if (g != o) r[n++] = Range{g, g + bytes, i, false};
+  }
+  std::sort(r.get(), r.get() + n, [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  // one sweep: the furthest end of an output, and of any range, among those that start before
+  uintptr_t out_end = 0, any_end = 0;
+  for (int64_t k = 0; k < n; ++k) {
+    if (r[k].lo < out_end || (r[k].output && r[k].lo < any_end))
+      return fail(INTLORA_EINVAL, "grad_clip: the output or input of tensor %lld overlaps another output",
+                  (long long)r[k].tensor);
+    if (r[k].output && r[k].hi > out_end) out_end = r[k].hi;
+    if (r[k].hi > any_end) any_end = r[k].hi;
+  }
+  return INTLORA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -277,7 +402,7 @@ const char* intlora_status_string(int status) {
 
 const char* intlora_last_error(void) { return g_err; }
 
-int intlora_version(void) { return 104; }
+int intlora_version(void) { return 105; }
 
 size_t intlora_workspace_bytes(int op, const intlora_desc* desc, int64_t M) {
   (void)M;
@@ -636,6 +761,111 @@ int intlora_linear_fwd_codes(int64_t M, int64_t d, int64_t n, const int8_t* xq, 
   return launch_status(intlora::launch_linear_codes(M, d, n, xq, s_x, u_code, w_round, z, z_bar, s_bar, Y_bf16,
                                                     acc_dbg, static_cast<hipStream_t>(stream)),
                        "linear_codes");
+}
+
+int intlora_fp8_quant_act(int64_t M, int64_t n, int dtype, const void* X, uint8_t* xq, uint8_t* sx, void* stream) {
+  int s = check_dtype(dtype, true, "fp8_quant_act");
+  if (s) return s;
+  if (M < 0 || M >= kMaxDim || n < 1 || n > kMaxFeatures || n % 16 != 0)
+    return fail(INTLORA_ESHAPE, "fp8_quant_act needs n a multiple of 16 and <= 2^20 (got M=%lld n=%lld)", (long long)M,
+                (long long)n);
+  if (M * ((n + 127) / 128) >= (int64_t(1) << 34)) return fail(INTLORA_ESHAPE, "fp8_quant_act: too many blocks");
+  if (M == 0) return ok();
+  if ((s = check_ptrs({X, xq, sx}, "fp8_quant_act"))) return s;
+  if ((s = ensure_device())) return s;
+  return launch_status(intlora::launch_fp8_quant_act(M, n, dtype, X, xq, sx, static_cast<hipStream_t>(stream)),
+                       "fp8_quant_act");
+}
+
+int intlora_fp8_quant_weight(int64_t E, int64_t d, int64_t n, int dtype, const void* W, uint8_t* wq, uint8_t* sw,
+                             uint8_t* wq_t, uint8_t* sw_t, void* stream) {
+  int s = check_dtype(dtype, true, "fp8_quant_weight");
+  if (s) return s;
+  if ((s = check_layer(1, E, d, n, "fp8_quant_weight"))) return s;
+  if (n % 16 != 0) return fail(INTLORA_ESHAPE, "fp8_quant_weight needs n a multiple of 16 (got %lld)", (long long)n);
+  if ((wq_t == nullptr) != (sw_t == nullptr))
+    return fail(INTLORA_EINVAL, "fp8_quant_weight: wq_t and sw_t go together (both or neither)");
+  if (wq_t && d % 16 != 0)
+    return fail(INTLORA_ESHAPE, "fp8_quant_weight: the transposed codes need d a multiple of 16 (got %lld)",
+                (long long)d);
+  if (d == 0) return ok();
+  if ((s = check_ptrs({W, wq, sw}, "fp8_quant_weight"))) return s;
+  if ((s = check_opt(wq_t, "wq_t")) || (s = check_opt(sw_t, "sw_t"))) return s;
+  if ((s = ensure_device())) return s;
+  return launch_status(intlora::launch_fp8_quant_weight(E, d, n, dtype, W, wq, sw, wq_t, sw_t,
+                                                        static_cast<hipStream_t>(stream)),
+                       "fp8_quant_weight");
+}
+
+int intlora_fp8_linear_fwd(int64_t M, int64_t d, int64_t n, const uint8_t* xq, const uint8_t* sx, const uint8_t* wq,
+                           const uint8_t* sw, uint16_t* Y_bf16, void* stream) {
+  return fp8_linear("fp8_linear_fwd", M, 1, d, n, xq, sx, nullptr, wq, sw, Y_bf16, stream);
+}
+
+int intlora_fp8_grouped_linear_fwd(int64_t M, int64_t E, int64_t d, int64_t n, const uint8_t* xq, const uint8_t* sx,
+                                   const int64_t* offsets, const uint8_t* wq, const uint8_t* sw, uint16_t* Y_bf16,
+                                   void* stream) {
+  const int s = check_offsets(E, offsets, "fp8_grouped_linear_fwd");
+  if (s) return s;
+  return fp8_linear("fp8_grouped_linear_fwd", M, E, d, n, xq, sx, offsets, wq, sw, Y_bf16, stream);
+}
+
+int intlora_grouped_linear_fwd(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, const void* X,
+                               const int64_t* offsets, const void* W, void* Y, void* stream) {
+  const int s = check_grouped(M, E, d, n, dtype, dtype, offsets, "grouped_linear_fwd");
+  if (s) return s;
+  if (M == 0 || d == 0) return ok();
+  return run_grouped("grouped_linear_fwd", intlora::kGroupedFwd, M, E, d, n, dtype, dtype, X, offsets, W, Y, stream);
+}
+
+int intlora_grouped_linear_dx(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, const void* dY,
+                              const int64_t* offsets, const void* W, void* dX, void* stream) {
+  const int s = check_grouped(M, E, d, n, dtype, dtype, offsets, "grouped_linear_dx");
+  if (s) return s;
+  if (d == 0) return fail(INTLORA_ESHAPE, "grouped_linear_dx needs d >= 8");
+  if (M == 0) return ok();
+  return run_grouped("grouped_linear_dx", intlora::kGroupedDx, M, E, d, n, dtype, dtype, dY, offsets, W, dX, stream);
+}
+
+int intlora_grouped_linear_dw(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype, const void* dY,
+                              const void* X, const int64_t* offsets, void* dW, void* stream) {
+  const int s = check_grouped(M, E, d, n, dtype, out_dtype, offsets, "grouped_linear_dw");
+  if (s) return s;
+  if (d == 0) return ok();
+  return run_grouped("grouped_linear_dw", intlora::kGroupedDw, M, E, d, n, dtype, out_dtype, dY, offsets, X, dW,
+                     stream);
+}
+
+size_t intlora_grad_ws_bytes(int64_t count, const int64_t* numel) {
+  if (count < 0 || count > kMaxGrads || (count > 0 && !numel)) return 0;
+  for (int64_t i = 0; i < count; ++i)
+    if (numel[i] < 0 || numel[i] >= kMaxNumel) return 0;
+  return intlora::grad_ws_bytes(count, numel);
+}
+
+int intlora_grad_sumsq(int64_t count, const void* const* grads, const int64_t* numel, const int32_t* dtype,
+                       double* sumsq, void* ws, size_t ws_bytes, void* stream) {
+  int s = check_grads(count, grads, numel, dtype, "grad_sumsq");
+  if (s) return s;
+  if ((s = check_ptrs({sumsq}, "grad_sumsq"))) return s;
+  if ((s = check_ws(ws, ws_bytes, intlora::grad_ws_bytes(count, numel)))) return s;
+  if ((s = ensure_device())) return s;
+  return launch_status(intlora::launch_grad_sumsq(count, grads, numel, dtype, sumsq, ws,
+                                                  static_cast<hipStream_t>(stream)),
+                       "grad_sumsq");
+}
+
+int intlora_grad_clip(int64_t count, const void* const* grads, void* const* out, const int64_t* numel,
+                      const int32_t* dtype, const double* sumsq, double max_norm, float* norm_out, void* stream) {
+  int s = check_grads(count, grads, numel, dtype, "grad_clip");
+  if (s) return s;
+  if (!(max_norm >= 0.0)) return fail(INTLORA_EINVAL, "grad_clip: max_norm must be >= 0 (got %g)", max_norm);
+  if ((s = check_ptrs({sumsq}, "grad_clip")) || (s = check_opt(norm_out, "norm_out"))) return s;
+  if ((s = check_clip_outputs(count, grads, out, numel, dtype))) return s;
+  if ((s = ensure_device())) return s;
+  return launch_status(intlora::launch_grad_clip(count, grads, out, numel, dtype, sumsq, max_norm, norm_out,
+                                                 static_cast<hipStream_t>(stream)),
+                       "grad_clip");
 }
 
 int intlora_debug_ln(int64_t count, const uint32_t* G, float* out, void* stream) {

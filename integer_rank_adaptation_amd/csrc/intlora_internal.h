@@ -85,4 +85,24 @@ hipError_t launch_linear_codes(int64_t M, int64_t d, int64_t n, const int8_t* xq
                                const uint8_t* ucode, const uint8_t* wcode, const int32_t* z, const int32_t* zbar,
                                const float* sbar, uint16_t* Y, int32_t* acc_dbg, hipStream_t st);
 
+// Floating-point linear layers (fplinear.hip).  dtype: INTLORA_BF16 / _FP16 / _FP32.
+enum { kGroupedFwd = 0, kGroupedDx = 1, kGroupedDw = 2 };
+int fp8_scale_stride(int64_t n);  // scale bytes per row of n columns
+hipError_t launch_fp8_quant_act(int64_t M, int64_t n, int dtype, const void* X, uint8_t* xq, uint8_t* sx,
+                                hipStream_t st);
+hipError_t launch_fp8_quant_weight(int64_t E, int64_t d, int64_t n, int dtype, const void* W, uint8_t* wq,
+                                   uint8_t* sw, uint8_t* wt, uint8_t* swt, hipStream_t st);
+hipError_t launch_fp8_linear(int64_t M, int64_t E, int64_t d, int64_t n, const uint8_t* xq, const uint8_t* sx,
+                             const int64_t* offsets, const uint8_t* wq, const uint8_t* sw, uint16_t* Y,
+                             hipStream_t st);
+// tokens: X (forward) or dY; other: W (forward, dX) or X (dW); out: Y, dX or dW.
+hipError_t launch_grouped(int direction, int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype,
+                          const void* tokens, const int64_t* offsets, const void* other, void* out, hipStream_t st);
+// Gradient norm and clipping (gradclip.hip); src, dst, numel, dtype are host arrays.
+size_t grad_ws_bytes(int64_t count, const int64_t* numel);
+hipError_t launch_grad_sumsq(int64_t count, const void* const* src, const int64_t* numel, const int32_t* dtype,
+                             double* sumsq, void* ws, hipStream_t st);
+hipError_t launch_grad_clip(int64_t count, const void* const* src, void* const* dst, const int64_t* numel,
+                            const int32_t* dtype, const double* sumsq, double max_norm, float* norm, hipStream_t st);
+
 }  // namespace intlora

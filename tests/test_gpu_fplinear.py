@@ -1,0 +1,360 @@
+"""The floating-point linear layers on the GPU against plain binary64 definitions.
+
+Codes and scale bytes are compared for equality.  A product of K terms accumulated in
+binary32 is within (K + 16) 2^-23 sum |a| |b| of the exact one (the bound for any order of
+summation with at most K + 16 roundings, each by at most one unit of 2^-23, which covers
+truncation), and the final rounding to t adds finfo(t).eps / 2 of the value, or half the
+smallest subnormal of t.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import fplinear as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def ops():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from integer_rank_adaptation_amd import ops as _ops
+
+    _ops.B.lib()
+    return _ops
+
+
+def rng(seed):
+    return np.random.Generator(np.random.PCG64(seed))
+
+
+def randn(seed, shape, std=1.0, dtype=torch.float32):
+    return torch.from_numpy((rng(seed).standard_normal(shape) * std).astype(np.float32)).to(dtype)
+
+
+def f64(t):
+    return t.cpu().double().numpy()
+
+
+def codes_of(t):
+    return t.cpu().view(torch.uint8).numpy()
+
+
+def check(got, want, mag, k, what=""):
+    """got (tensor) against the exact product `want` with magnitudes `mag`, k terms."""
+    t = got.dtype
+    tiny = torch.finfo(t).smallest_normal * torch.finfo(t).eps / 2 if t != torch.bfloat16 else 0.0
+    acc = (k + 16) * 2.0**-23 * mag
+    tol = acc + (torch.finfo(t).eps / 2) * (np.abs(want) + acc) + tiny
+    diff = np.abs(f64(got) - want)
+    bad = ~(diff <= tol)
+    assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:4].tolist(), float(np.nanmax(diff)))
+
+
+def offsets_of(rows, lead=0):
+    return torch.tensor(np.concatenate([[lead], lead + np.cumsum(rows)]), dtype=torch.int64)
+
+
+# --------------------------------------------------------------------------- quantizers
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,n", [(1, 16), (3, 128), (5, 144), (37, 1040), (2, 4096), (129, 512)])
+def test_quant_act_exact(ops, dtype, M, n):
+    g = rng(M * 31 + n)
+    x = g.standard_normal((M, n)) * np.exp2(g.integers(-12, 4, (M, 1)))
+    X = torch.from_numpy(x.astype(np.float32)).to(TYPES[dtype])
+    X[0, : n // 2] = 0  # a block of zeros where n > 256
+    if M > 2:
+        X[2, 0] = 448.0  # exactly the largest code
+        X[2, 1] = -449.0
+    xq, sx = ops.fp8_quant_act(X.cuda())
+    cq, cs = ref.quantize(X.double().numpy(), 1)
+    assert np.array_equal(sx.cpu().numpy(), cs)
+    assert np.array_equal(codes_of(xq), cq)
+
+
+def test_quant_act_every_tie_and_extremes(ops):
+    """All midpoints between neighbouring codes, under scales over the whole exponent range."""
+    vals = ref.e4m3_values()[:0x7F]
+    mids = (vals[:-1] + vals[1:]) / 2
+    pts = np.concatenate([vals, mids, np.nextafter(mids.astype(np.float32), 0), np.nextafter(mids.astype(np.float32), 999)])
+    pts = np.concatenate([pts, -pts])
+    pts = np.resize(pts, -(-pts.size // 112) * 112).reshape(-1, 112)
+    rows = []
+    for e in (-149, -140, -127, -126, -60, 0, 60, 119):
+        b = np.zeros((pts.shape[0], 128))
+        b[:, :112] = pts
+        b[:, 127] = 448.0  # fixes the block's scale
+        rows.append(np.ldexp(b, e).astype(np.float32))
+    X = torch.from_numpy(np.concatenate(rows))
+    X = torch.cat([X, torch.tensor([[3.4028234e38] + [0.0] * 126 + [1e-45], [1e-45] * 128])])
+    xq, sx = ops.fp8_quant_act(X.cuda())
+    cq, cs = ref.quantize(X.double().numpy(), 1)
+    assert np.array_equal(sx.cpu().numpy(), cs)
+    assert np.array_equal(codes_of(xq), cq)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_quant_nonfinite_blocks(ops, bad):
+    X = randn(3, (4, 384), dtype=torch.bfloat16)
+    X[1, 200] = bad
+    xq, sx = ops.fp8_quant_act(X.cuda())
+    cq, cs = ref.quantize(X.double().numpy(), 1)
+    assert np.array_equal(sx.cpu().numpy(), cs) and cs[1, 1] == 255
+    assert np.array_equal(codes_of(xq), cq)
+    w = ops.fp8_quant_weight(randn(4, (48, 384)).cuda())
+    for M in (4, 40):  # both kernels: the row with the block is NaN, the others are not
+        Xm = X.repeat(M // 4, 1)
+        Y = ops.fp8_linear(*ops.fp8_quant_act(Xm.cuda()), w["wq"], w["sw"]).cpu()
+        nan = torch.isnan(Y).all(1)
+        assert nan.tolist() == [i % 4 == 1 for i in range(M)]
+        assert not torch.isnan(Y[~nan]).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("E,d,n", [(1, 16, 16), (1, 128, 128), (2, 144, 272), (3, 320, 1040), (1, 1, 128)])
+def test_quant_weight_exact(ops, dtype, E, d, n):
+    W = randn(d + n, (E, d, n), 0.02, TYPES[dtype])
+    W[:, :, n // 2] *= 50
+    two = d % 16 == 0
+    o = ops.fp8_quant_weight(W.cuda(), transpose=two)
+    for e in range(E):
+        cq, cs = ref.quantize(W[e].double().numpy(), 128)
+        assert np.array_equal(codes_of(o["wq"][e]), cq)
+        assert np.array_equal(o["sw"][e].cpu().numpy(), cs)
+        if two:
+            assert np.array_equal(codes_of(o["wq_t"][e]), cq.T)
+            st = np.full((-(-n // 128), ops.fp8_scale_bytes(d)), 127, np.uint8)
+            st[:, : cs.shape[0]] = cs[:, : st.shape[0]].T
+            assert np.array_equal(o["sw_t"][e].cpu().numpy(), st)
+    flat = ops.fp8_quant_weight(W[0].cuda())
+    assert torch.equal(flat["wq"].view(torch.uint8), o["wq"][0].view(torch.uint8)) and torch.equal(flat["sw"], o["sw"][0])
+
+
+# --------------------------------------------------------------------------- 8-bit layer
+@pytest.mark.parametrize("M,d,n", [(1, 1, 16), (1, 16, 128), (2, 33, 144), (16, 320, 512), (17, 64, 4096), (32, 129, 1040),
+                                   (33, 256, 640), (64, 300, 128), (127, 257, 272), (129, 511, 144), (200, 1283, 2576),
+                                   (384, 768, 1024), (5, 640, 8208)])
+def test_fp8_linear(ops, M, d, n):
+    X, W = randn(M + d, (M, n)), randn(M + n, (d, n), 0.02)
+    X[:, n // 3] *= 10
+    xq, sx = ops.fp8_quant_act(X.cuda())
+    w = ops.fp8_quant_weight(W.cuda())
+    Y = ops.fp8_linear(xq, sx, w["wq"], w["sw"])
+    x = ref.dequantize(codes_of(xq), sx.cpu().numpy(), 1)
+    wd = ref.dequantize(codes_of(w["wq"]), w["sw"].cpu().numpy(), 128)
+    y, mag = ref.grouped(x, [0, M], wd[None])
+    check(Y, y, mag, n)
+
+
+def test_fp8_linear_scales_spread(ops):
+    """Scales that differ by block and by row over many binades: each block takes its own."""
+    M, d, n = 70, 300, 1536
+    g = rng(5)
+    X = randn(1, (M, n)) * torch.from_numpy(np.exp2(g.integers(-20, 20, (M, n // 128))).astype(np.float32)).repeat_interleave(128, 1)
+    W = randn(2, (d, n)) * torch.from_numpy(np.exp2(g.integers(-20, 20, (3, n // 128))).astype(np.float32)).repeat_interleave(128, 1).repeat_interleave(128, 0)[:d]
+    for m in (M, 7):
+        xq, sx = ops.fp8_quant_act(X[:m].cuda())
+        w = ops.fp8_quant_weight(W.cuda())
+        Y = ops.fp8_linear(xq, sx, w["wq"], w["sw"])
+        y, mag = ref.grouped(ref.dequantize(codes_of(xq), sx.cpu().numpy(), 1), [0, m],
+                             ref.dequantize(codes_of(w["wq"]), w["sw"].cpu().numpy(), 128)[None])
+        check(Y, y, mag, n)
+
+
+def test_fp8_input_gradient(ops):
+    """dX = dY W is the same product on the transposed codes; against the formula and against
+    differences of the layer's exact function <dY, X W^T>."""
+    M, d, n = 50, 272, 400
+    W = randn(1, (d, n), 0.02)
+    w = ops.fp8_quant_weight(W.cuda(), transpose=True)
+    dY = randn(2, (M, d), 0.1)
+    dq, sd = ops.fp8_quant_act(dY.cuda())
+    dX = ops.fp8_linear(dq, sd, w["wq_t"], w["sw_t"])
+    wd = ref.dequantize(codes_of(w["wq"]), w["sw"].cpu().numpy(), 128)
+    dy = ref.dequantize(codes_of(dq), sd.cpu().numpy(), 1)
+    want, mag = ref.grouped(dy, [0, M], wd.T[None])
+    check(dX, want, mag, d)
+    x = f64(randn(3, (M, n)))
+    f = lambda v: float((dy * (v @ wd.T)).sum())  # noqa: E731
+    for i, j in ((0, 0), (M - 1, n - 1), (17, 133)):
+        h = np.zeros_like(x)
+        h[i, j] = 0.5
+        slope = f(x + h) - f(x - h)  # linear in x: exact up to binary64 rounding
+        assert abs(slope - want[i, j]) <= 1e-9 * max(1.0, mag[i, j])
+
+
+GROUPS = [
+    [5], [0, 5], [5, 0], [0, 0, 7, 0, 0], [16, 17, 1, 0, 33], [128, 129, 127, 1], [300, 0, 2, 40, 64, 5],
+    [1] * 70, [0] * 63 + [40] + [0] * 5 + [3], [2, 100] * 40,
+]
+
+
+@pytest.mark.parametrize("rows", GROUPS, ids=lambda r: f"{len(r)}groups_{sum(r)}rows")
+@pytest.mark.parametrize("d,n", [(48, 144), (257, 640)])
+def test_fp8_grouped(ops, rows, d, n):
+    E, lead, tail = len(rows), 3, 4
+    M = lead + sum(rows) + tail
+    off = offsets_of(rows, lead)
+    X, W = randn(M, (M, n)), randn(E, (E, d, n), 0.02)
+    xq, sx = ops.fp8_quant_act(X.cuda())
+    w = ops.fp8_quant_weight(W.cuda())
+    out = torch.full((M, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    Y = ops.fp8_grouped_linear(xq, sx, off.cuda(), w["wq"], w["sw"], out=out)
+    assert Y is out
+    x = ref.dequantize(codes_of(xq), sx.cpu().numpy(), 1)
+    wd = np.stack([ref.dequantize(codes_of(w["wq"][e]), w["sw"][e].cpu().numpy(), 128) for e in range(E)])
+    y, mag = ref.grouped(x, off.tolist(), wd)
+    check(Y[lead:M - tail], y[lead:M - tail], mag[lead:M - tail], n)
+    assert (Y[:lead] == 7).all() and (Y[M - tail:] == 7).all()  # rows of no group stay
+
+
+# --------------------------------------------------------------------------- 16-bit, gradients
+@pytest.mark.parametrize("rows", GROUPS, ids=lambda r: f"{len(r)}groups_{sum(r)}rows")
+@pytest.mark.parametrize("dtype,d,n", [("bf16", 264, 72), ("fp16", 48, 344), ("bf16", 8, 8)])
+def test_grouped_step(ops, rows, dtype, d, n):
+    E, lead, tail = len(rows), 2, 5
+    M = lead + sum(rows) + tail
+    t = TYPES[dtype]
+    off = offsets_of(rows, lead)
+    X, W, dY = randn(M, (M, n), 1.0, t), randn(E, (E, d, n), 0.05, t), randn(d, (M, d), 0.1, t)
+    x, w, dy = X.double().numpy(), W.double().numpy(), dY.double().numpy()
+    Xd, Wd, dYd, offd = X.cuda(), W.cuda(), dY.cuda(), off.cuda()
+    live = slice(lead, M - tail)
+    y, mag = ref.grouped(x, off.tolist(), w)
+    out = torch.full((M, d), 7.0, dtype=t, device="cuda")
+    Y = ops.grouped_linear(Xd, offd, Wd, out=out)
+    check(Y[live], y[live], mag[live], n, "forward")
+    assert (Y[:lead] == 7).all() and (Y[M - tail:] == 7).all()
+    dx, mag = ref.grouped(dy, off.tolist(), w.transpose(0, 2, 1))
+    out = torch.full((M, n), 7.0, dtype=t, device="cuda")
+    dX = ops.grouped_linear_dx(dYd, offd, Wd, out=out)
+    check(dX[live], dx[live], mag[live], d, "dX")
+    assert (dX[:lead] == 7).all() and (dX[M - tail:] == 7).all()
+    dw, mag, counts = ref.grouped_dw(dy, x, off.tolist())
+    for o in (t, torch.float32):
+        dW = ops.grouped_linear_dw(dYd, Xd, offd, dtype=o)
+        check(dW, dw, mag, max(rows), "dW")
+        assert all((dW[e] == 0).all() for e in range(E) if counts[e] == 0)
+
+
+@pytest.mark.parametrize("M,d,n", [(1, 640, 1032), (40, 520, 264), (300, 264, 520), (513, 136, 2056)])
+def test_grouped_one_group_without_offsets(ops, M, d, n):
+    X, W, dY = randn(1, (M, n), dtype=torch.bfloat16), randn(2, (1, d, n), 0.05, torch.bfloat16), randn(3, (M, d), 0.1, torch.bfloat16)
+    x, w, dy = X.double().numpy(), W.double().numpy(), dY.double().numpy()
+    y, mag = ref.grouped(x, [0, M], w)
+    check(ops.grouped_linear(X.cuda(), None, W.cuda()), y, mag, n)
+    dx, mag = ref.grouped(dy, [0, M], w.transpose(0, 2, 1))
+    check(ops.grouped_linear_dx(dY.cuda(), None, W.cuda()), dx, mag, d)
+    dw, mag, _ = ref.grouped_dw(dy, x, [0, M])
+    check(ops.grouped_linear_dw(dY.cuda(), X.cuda(), None, dtype=torch.float32), dw, mag, M)
+
+
+def test_nan_stays_in_its_rows(ops):
+    """A NaN or infinity of one group, row or column tail reaches no other output, although the
+    tiles of neighbouring groups and the ends of rows share loads."""
+    rows, d, n = [40, 5, 60], 264, 72
+    M = sum(rows)
+    off = offsets_of(rows).cuda()
+    for t in (torch.bfloat16, torch.float16):
+        X, W, dY = randn(1, (M, n), 1.0, t), randn(2, (3, d, n), 0.05, t), randn(3, (M, d), 0.1, t)
+        X[42], W[1], dY[42] = float("nan"), float("inf"), float("inf")
+        Y = ops.grouped_linear(X.cuda(), off, W.cuda()).cpu()
+        dX = ops.grouped_linear_dx(dY.cuda(), off, W.cuda()).cpu()
+        dW = ops.grouped_linear_dw(dY.cuda(), X.cuda(), off).cpu()
+        out = torch.ones(M, dtype=torch.bool)
+        out[40:45] = False
+        assert torch.isfinite(Y[out]).all() and torch.isfinite(dX[out]).all()
+        assert torch.isnan(Y[42]).all()
+        assert torch.isfinite(dW[0]).all() and torch.isfinite(dW[2]).all() and torch.isnan(dW[1]).all()
+
+
+def test_bad_offsets_stay_inside(ops):
+    """Offsets outside [0, M] or descending count as the definition says."""
+    M, d, n = 90, 64, 64
+    X, W, dY = randn(1, (M, n), dtype=torch.bfloat16), randn(2, (4, d, n), 0.05, torch.bfloat16), randn(3, (M, d), dtype=torch.bfloat16)
+    for off in ([-5, 30, 20, 1 << 40, 50], [200, 300, 0, 1, 2], [0, 90, -(1 << 50), 90, 1 << 62]):
+        b = ref.boundaries(off, M)
+        y, mag = ref.grouped(X.double().numpy(), off, W.double().numpy())
+        o = torch.tensor(off, dtype=torch.int64, device="cuda")
+        out = torch.full((M, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        ops.grouped_linear(X.cuda(), o, W.cuda(), out=out)
+        check(out[b[0]:b[-1]], y[b[0]:b[-1]], mag[b[0]:b[-1]], n)
+        assert (out[:b[0]] == 7).all() and (out[b[-1]:] == 7).all()
+        dw, mag, _ = ref.grouped_dw(dY.double().numpy(), X.double().numpy(), off)
+        check(ops.grouped_linear_dw(dY.cuda(), X.cuda(), o, dtype=torch.float32), dw, mag, M)
+
+
+def test_grouped_gradients_by_differences(ops):
+    """dX and dW against differences of f = <dY, Y(X, W)> in binary64 (f is bilinear, so a
+    central difference is its slope up to binary64 rounding)."""
+    rows, d, n = [20, 0, 37], 40, 56
+    M, off = sum(rows), offsets_of([20, 0, 37])
+    X, W, dY = randn(1, (M, n), dtype=torch.bfloat16), randn(2, (3, d, n), 0.05, torch.bfloat16), randn(3, (M, d), 0.1, torch.bfloat16)
+    x, w, dy = X.double().numpy(), W.double().numpy(), dY.double().numpy()
+    f = lambda a, b: float((dy * ref.grouped(a, off.tolist(), b)[0]).sum())  # noqa: E731
+    dX = f64(ops.grouped_linear_dx(dY.cuda(), off.cuda(), W.cuda()))
+    dW = f64(ops.grouped_linear_dw(dY.cuda(), X.cuda(), off.cuda(), dtype=torch.float32))
+    _, magx = ref.grouped(dy, off.tolist(), w.transpose(0, 2, 1))
+    _, magw, _ = ref.grouped_dw(dy, x, off.tolist())
+    for i, j in ((0, 0), (19, 55), (20, 7), (56, 55)):
+        h = np.zeros_like(x)
+        h[i, j] = 0.5
+        slope = f(x + h, w) - f(x - h, w)
+        assert abs(dX[i, j] - slope) <= 2.0**-8 * abs(slope) + (d + 16) * 2.0**-22 * magx[i, j]
+    for e, i, j in ((0, 0, 0), (0, 39, 55), (1, 3, 3), (2, 17, 20)):
+        h = np.zeros_like(w)
+        h[e, i, j] = 0.5
+        slope = f(x, w + h) - f(x, w - h)
+        assert abs(dW[e, i, j] - slope) <= (M + 16) * 2.0**-22 * magw[e, i, j] + 1e-12
+
+
+# --------------------------------------------------------------------------- clipping
+def _grads(seed, shapes, dtypes):
+    return [randn(seed + i, s, 0.01, TYPES[t]) for i, (s, t) in enumerate(zip(shapes, dtypes))]
+
+
+@pytest.mark.parametrize("max_norm", [0.0, 0.05, 1e6])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_clip(ops, max_norm, inplace):
+    shapes = [(1,), (7,), (0, 5), (640, 4), (3, 16384), (16385,), (129, 1021), (5, 5, 5)] * 20
+    types = (["fp32", "bf16", "fp16"] * 60)[: len(shapes)]
+    gs = _grads(1, shapes, types)
+    dev = [g.cuda() for g in gs]
+    out = dev if inplace else [torch.full_like(g, 3.0) for g in dev]
+    norm = ops.clip_grad_norm(dev, max_norm, out=None if inplace else out)
+    total = ref.sumsq([g.double().numpy() for g in gs])
+    want = total ** 0.5
+    # binary64 sums of n terms, then one binary32 rounding
+    assert abs(float(norm) - want) <= want * 2.0**-24 * 1.001
+    c = np.float32(ref.clip_factor(total, max_norm))
+    for g, o in zip(gs, out):
+        exact = g.double().numpy() * float(c)
+        t = g.dtype
+        half = torch.finfo(t).eps / 2
+        # the factor may be the neighbouring binary32 value (its binary64 argument is off by
+        # rounding): 2^-23; the product is rounded to binary32 and, for 16 bits, once more
+        tol = (2.0**-23 + 2.0**-24 + (half if t != torch.float32 else 0.0)) * np.abs(exact) * 1.001
+        tol = tol + torch.finfo(t).smallest_normal * torch.finfo(t).eps
+        assert (np.abs(f64(o) - exact) <= tol).all()
+        if max_norm == 1e6:
+            assert torch.equal(o.cpu(), g)
+    if not inplace:
+        assert all(torch.equal(a.cpu(), b) for a, b in zip(dev, gs))
+
+
+def test_clip_empty_and_nonfinite(ops):
+    assert float(ops.clip_grad_norm([], 1.0)) == 0.0
+    assert float(ops.clip_grad_norm([torch.empty(0, device="cuda")], 1.0)) == 0.0
+    g = [torch.ones(100, device="cuda"), torch.ones(33, device="cuda", dtype=torch.bfloat16)]
+    g[0][5] = float("inf")
+    n = ops.clip_grad_norm(g, 1.0)
+    assert torch.isinf(n).all() and torch.isnan(g[0][5]) and (g[0][:5] == 0).all() and (g[1] == 0).all()
+    g = [torch.ones(100, device="cuda"), torch.full((5,), float("nan"), device="cuda")]
+    n = ops.clip_grad_norm(g, 1.0)
+    assert torch.isnan(n).all() and torch.isnan(g[0]).all()
+    big = [torch.full((1000,), 1e30, device="cuda")]  # squares beyond binary32
+    n = ops.clip_grad_norm(big, 1.0)
+    assert abs(float(n) / (1e30 * 1000 ** 0.5) - 1) < 1e-6 and abs(float(big[0][3]) * 1000 ** 0.5 - 1) < 1e-6
