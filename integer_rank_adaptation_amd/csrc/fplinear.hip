@@ -34,13 +34,50 @@ enum { L_NT = 0, L_NN = 1, L_TN = 2 };
 
 constexpr uint32_t kOOB = 0x80000000u;  // a buffer offset past every record: the lane reads zeros
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
-  const int64_t cap = 0x7FFFFFF0;  // lane offsets stay below 2^31: every tile and stage has a base of its own
-  const int nrec = (int)(bytes < 0 ? 0 : (bytes > cap ? cap : bytes));
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, nrec, 0x00020000);
+typedef uint32_t rsrc_t __attribute__((ext_vector_type(4)));
+
+// Buffer descriptor of `bytes` bytes from `base` (none if negative): what lies past them
+// reads zeros.  Lane offsets stay below 2^31: every tile and stage has a base of its own.
+__device__ __forceinline__ rsrc_t make_desc(const void* base, int bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  // (uniform values; readfirstlane keeps them in scalar registers)
+  return rsrc_t{(uint32_t)__builtin_amdgcn_readfirstlane((int)a),
+                (uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32) & 0xFFFF),
+                (uint32_t)__builtin_amdgcn_readfirstlane(bytes < 0 ? 0 : bytes), 0x00020000u};
 }
 
-// At most N direct loads still in flight, and every LDS read returned.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  const int64_t cap = 0x7FFFFFF0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0,
+                                           (int)(bytes < 0 ? 0 : (bytes > cap ? cap : bytes)), 0x00020000);
+}
+
+// Direct load: lane l's 16 (4) bytes at `offset` of the buffer go to LDS at lds + 16 l (4 l).
+// As instructions of our own and not the builtin, for which the compiler waits until every
+// direct load in flight has landed before almost every LDS read; the stage loop's own waits
+// order the two (with the compiler's waits the dX and dW loops took 1.5 times as long).  There
+// is no output register; M0 is reserved (the compiler writes it right before each use of its
+// own).  The s_nop covers the wait states between writes of M0 or the descriptor and their use.
+__device__ __forceinline__ void direct_load16(const rsrc_t& r, uint32_t lds, uint32_t offset) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                   :
+                   : "s"(lds), "v"(offset), "s"(r)
+                   : "memory");
+}
+__device__ __forceinline__ void direct_load4(const rsrc_t& r, uint32_t lds, uint32_t offset) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                   :
+                   : "s"(lds), "v"(offset), "s"(r)
+                   : "memory");
+}
+
+// At most N direct loads still in flight.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+// The same, and every LDS read returned.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
@@ -57,23 +94,21 @@ struct Group {
   int e, row0, rows;
 };
 
-// The unit (row tile x units_per_tile) number `want` over all groups whose row count lies
-// in [least, most]; each such group has ceil(rows / bm) row tiles.  False when there are
-// fewer.  A wave takes 64 groups at a time, one per lane; all waves find the same.
-__device__ __forceinline__ bool find_unit(const int64_t* __restrict__ offsets, int E, int T, int want, int bm,
-                                          int units_per_tile, int least, int most, Group& g, int& unit) {
-  const int lane = threadIdx.x & 63;
-  if (offsets == nullptr) {  // one group of all rows
-    g.e = 0;
-    g.row0 = 0;
-    g.rows = T;
-    unit = want;
-    return T >= least && T <= most && want < (T + bm - 1) / bm * units_per_tile;
+// Row tiles of all groups in order.  A wave looks at 64 groups at a time, one per lane, and
+// keeps the chunk it looked at last (in LDS: it is needed once per tile); all waves of a
+// block compute the same.
+struct Groups {
+  const int64_t* offsets;  // NULL: one group of all T rows
+  int* at;                 // the wave's 3 x 64 words of LDS: first row, rows, running units
+  int E, T, bm, per_tile;  // rows per tile; units per row tile
+  int least, most;         // groups with other row counts have no tiles
+  int e0, before, done;    // the chunk's first group, its first boundary, the units in front of it
+
+  __device__ __forceinline__ int units(int n) const {
+    return n >= least && n <= most ? (n + bm - 1) / bm * per_tile : 0;
   }
-  int before = clamp_row(offsets[0], T);  // boundary in front of this chunk of groups
-  int done = 0;                           // units in front of it
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
+  __device__ __forceinline__ void chunk() {
+    const int lane = threadIdx.x & 63, e = e0 + lane;
     int b = e < E ? clamp_row(offsets[e + 1], T) : 0;
     if (b < before) b = before;
 #pragma unroll
@@ -83,31 +118,60 @@ __device__ __forceinline__ bool find_unit(const int64_t* __restrict__ offsets, i
     }
     int a = __shfl_up(b, 1);
     if (lane == 0) a = before;
-    const int rows = b - a;
-    const int mine = rows >= least && rows <= most ? (rows + bm - 1) / bm * units_per_tile : 0;
-    int inc = mine;
+    int inc = units(b - a);
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) {
       const int o = __shfl_up(inc, s);
       if (lane >= s) inc += o;
     }
-    const uint64_t hit = __builtin_amdgcn_ballot_w64(done + inc > want);
-    if (hit) {
-      const int src = __builtin_ctzll(hit);
-      g.e = e0 + src;
-      g.row0 = __builtin_amdgcn_readlane(a, src);
-      g.rows = __builtin_amdgcn_readlane(rows, src);
-      unit = want - done - __builtin_amdgcn_readlane(inc - mine, src);
-      return true;
-    }
-    done += __builtin_amdgcn_readlane(inc, 63);
-    before = __builtin_amdgcn_readlane(b, 63);
+    at[lane] = a;
+    at[64 + lane] = b - a;
+    at[128 + lane] = inc;
+    __builtin_amdgcn_wave_barrier();
   }
-  return false;
-}
+  __device__ __forceinline__ void first() {
+    e0 = 0;
+    done = 0;
+    before = __builtin_amdgcn_readfirstlane(clamp_row(offsets[0], T));
+    chunk();
+  }
+  __device__ __forceinline__ bool advance() {
+    if (e0 + 64 >= E) return false;
+    done += __builtin_amdgcn_readfirstlane(at[128 + 63]);
+    before = __builtin_amdgcn_readfirstlane(at[63] + at[64 + 63]);
+    e0 += 64;
+    chunk();
+    return true;
+  }
+  // Number of units; leaves the last chunk in place.
+  __device__ __forceinline__ int total() {
+    if (offsets == nullptr) return units(T);
+    first();
+    while (advance()) {
+    }
+    return done + __builtin_amdgcn_readfirstlane(at[128 + 63]);
+  }
+  // The group of unit `want` (below total()), and the unit's number inside it.
+  __device__ __forceinline__ Group find(int want, int& unit) {
+    if (offsets == nullptr) {
+      unit = want;
+      return Group{0, 0, T};
+    }
+    if (want < done) first();
+    uint64_t hit;
+    while ((hit = __builtin_amdgcn_ballot_w64(done + at[128 + (threadIdx.x & 63)] > want)) == 0) {
+      if (!advance()) break;
+    }
+    const int src = hit ? __builtin_ctzll(hit) : 63;
+    const int row0 = __builtin_amdgcn_readfirstlane(at[src]), rows = __builtin_amdgcn_readfirstlane(at[64 + src]);
+    unit = want - done - (__builtin_amdgcn_readfirstlane(at[128 + src]) - units(rows));
+    return Group{e0 + src, row0, rows};
+  }
+};
 
 // Rows of group e.
 __device__ __forceinline__ Group group_rows(const int64_t* __restrict__ offsets, int e, int T) {
+  if (offsets == nullptr) return Group{0, 0, T};
   const int lane = threadIdx.x & 63;
   int a = 0;
   for (int j = lane; j <= e; j += 64) {
@@ -120,7 +184,7 @@ __device__ __forceinline__ Group group_rows(const int64_t* __restrict__ offsets,
     a = o > a ? o : a;
   }
   a = __builtin_amdgcn_readfirstlane(a);
-  const int b = clamp_row(offsets[e + 1], T);
+  const int b = __builtin_amdgcn_readfirstlane(clamp_row(offsets[e + 1], T));
   return Group{e, a, b > a ? b - a : 0};
 }
 
@@ -132,70 +196,77 @@ __device__ __forceinline__ int xcd_slot(int b, int n) {
 }
 
 // ------------------------------------------------------------------------ tiled kernel
-// A block computes BM x BN outputs with 4 waves (2 x 2), each (BM / 2) x (BN / 2) in tiles
-// of 32 x 32.  The contraction goes in stages of 64 bytes of a row (32 16-bit or 64 8-bit
-// elements) through a ring of three LDS stages filled by direct loads.
-constexpr int kStages = 3;
-constexpr int kScaleBytes = 1024;  // 8-bit: 128 rows' and the weight blocks' scale dwords of a stage
-
-template <int TY, int LAY, int BM, int BN>
+// A block computes BM x BN outputs at a time, each wave WM x WN of them in tiles of 32 x 32.
+// The contraction goes in stages of 128 bytes of a row (64 16-bit or 128 8-bit elements)
+// through a ring of ST LDS buffers filled by direct loads; a stage is two sub-steps of 64
+// bytes.
+template <int TY_, int LAY_, int BM_, int BN_, int WM_, int WN_, int ST_>
 struct Tile {
+  static constexpr int TY = TY_, LAY = LAY_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_;
   static constexpr bool F8 = TY == T_FP8;
   static constexpr int EB = F8 ? 1 : 2;        // bytes per element
-  static constexpr int BK = 64 / EB;           // elements per stage
-  static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64;
-  static constexpr int STAGE = A_BYTES + B_BYTES + (F8 ? kScaleBytes : 0);
-  static constexpr int AL = A_BYTES / 4096, BL = B_BYTES / 4096;  // direct loads per wave and stage
-  static constexpr int LOADS = AL + BL + (F8 ? 1 : 0);
-  static constexpr int WM = BM / 2, WN = BN / 2, MT = WM / 32, NT = WN / 32;
-  static constexpr int RING = kStages * STAGE;
+  static constexpr int BK = 128 / EB;          // elements per stage
+  static constexpr int WAVES_N = BN / WN, WAVES = BM / WM * WAVES_N, THREADS = 64 * WAVES;
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+  // 8-bit: the scale dwords of a stage, 64 per wave: BM rows', then the weight blocks'
+  static constexpr int STAGE = A_BYTES + B_BYTES + (F8 ? 256 * WAVES : 0);
+  static constexpr int AL = A_BYTES / 1024 / WAVES, BL = B_BYTES / 1024 / WAVES;  // direct loads per wave and stage
+  static constexpr int AX = AL + (F8 ? 1 : 0), LOADS = AX + BL;  // with the scales' load
+  static constexpr int MT = WM / 32, NT = WN / 32;
+  static constexpr int READS = 2 * (MT + NT);                // LDS fragment reads per sub-step
+  static constexpr int PRODUCTS = MT * NT * (F8 ? 1 : 2);    // matrix instructions per sub-step
+  static constexpr int EPI_ROW = 32 * 2 + 16;                // epilogue staging: 32 rows of 32 16-bit outputs, padded
+  static constexpr int EPI = ST * STAGE, GROUPS = EPI + WAVES * 32 * EPI_ROW;
+  static constexpr int LDS = GROUPS + WAVES * 768;
   static constexpr bool TA = LAY == L_TN, TB = LAY != L_NT;  // operands stored [contraction, columns]
+  static_assert(AL * 1024 * WAVES == A_BYTES && BL * 1024 * WAVES == B_BYTES, "whole loads");
+  static_assert(!F8 || WAVES > BM / 64, "waves for the rows' scales and the weights'");
+  static_assert(LDS <= 160 * 1024, "LDS of a compute unit");
 };
 
-// LDS rows of 64 bytes: the 16-byte chunk c of row r lies at c ^ swz64(r), so that the 16
-// lanes of a fragment read touch every bank once.
-__device__ __forceinline__ int swz64(int row) { return (row ^ (row >> 2)) & 3; }
-
-// Rows [contraction k][columns]: a transposing read takes 4 rows x 32 bytes per 16 lanes;
-// chunk c of row k lies at c ^ 2 (k & 3), which puts the four rows on different banks.
-__device__ __forceinline__ int swzT(int k) { return 2 * (k & 3); }
-
-// Byte offset, from the operand tile's first byte, of the 16 bytes that this lane brings to
-// LDS with its load q: row-contiguous operand (TR = 0, ld bytes per row, rows = outputs) or
-// [contraction, columns] operand of C columns (TR = 1, rows = contraction).
+// An operand tile of C rows / columns in LDS.  Row-contiguous operands (TR = 0) lie as rows
+// of 128 bytes with the 16-byte chunk c of row r at c ^ (r / 2) % 8: the 16 lanes that a
+// 16-byte read serves at a time then touch every bank once.  [contraction, columns] operands
+// (TR = 1) lie as rows of 2 C bytes with chunk c of contraction row k at c ^ 4 (k % 4): a
+// transposing read takes 4 rows x 64 bytes per 32 lanes, which this puts on different banks.
+// Direct loads bring 1 KB each, always whole runs of 128 bytes or more: with runs of 64 bytes
+// (twice as many requests to L2) the loads alone took 25 % longer.
 template <bool TR, int C>
-__device__ __forceinline__ uint32_t lane_offset(int g, int lane, uint32_t ld, int& kk) {
-  if (!TR) {
-    const int row = 16 * g + (lane >> 2);
-    kk = 16 * ((lane & 3) ^ swz64(row));
-    return (uint32_t)row * ld + kk;
+struct Operand {
+  static constexpr int PER = TR ? C / 8 : 8;  // 16-byte chunks per LDS row
+  static constexpr int ROWS = 64 / PER;       // LDS rows per load
+  static_assert(C == 128 || C == 256, "the flip below");
+  // This lane's place in a load: byte offset of its row, and of its chunk in the row for even
+  // loads; the swizzle flips bit 6 of the latter for odd ones (C = 128 columns: not).
+  static __device__ __forceinline__ uint32_t row(int lane, uint32_t ld) { return (uint32_t)(lane / PER) * ld; }
+  static __device__ __forceinline__ int chunk(int lane) {
+    const int r = lane / PER;
+    return 16 * ((lane % PER) ^ (TR ? 4 * (r & 3) : r >> 1));
   }
-  constexpr int PER = C / 8;  // chunks per row
-  const int row = (64 / PER) * g + lane / PER;
-  kk = 0;
-  return (uint32_t)row * ld + 16 * ((lane % PER) ^ swzT(row));
-}
+  static __device__ __forceinline__ int flip(int q) { return (q & 1) == 0 || (TR && ROWS == 4) ? 0 : TR ? 128 : 64; }
+  // LDS offset of this lane's first fragment of the 32-row tiles from r0 (a multiple of 64);
+  // lane half h takes the contraction chunk 4 sub + 2 h + ks of a stage
+  static __device__ __forceinline__ uint32_t frag(int lane, int r0) {
+    const int h = lane >> 5, r = lane & 31;
+    if (!TR) return (uint32_t)((r0 + r) * 128 + (((2 * h) ^ ((r >> 1) & 7)) << 4));
+    // lane j of 16 points at contraction row j / 4, columns 4 (j % 4) .. + 3, and receives
+    // column j, the four rows
+    const int j = lane & 15, k = 16 * h + (j >> 2), col = r0 + (lane & 16) + 4 * (j & 3);
+    return (uint32_t)(k * (2 * C) + (((col >> 3) ^ (4 * (k & 3))) << 4) + ((col & 7) << 1));
+  }
+  // Fragment of 16 bytes of tile x from the operand's LDS at offset `at` = frag + its start.
+  static __device__ __forceinline__ v4i read(const uint8_t* lds, uint32_t at, int x, int sub, int ks) {
+    if (!TR) return *reinterpret_cast<const v4i*>(lds + (at ^ (uint32_t)((4 * sub + ks) << 4)) + x * 4096);
+    const uint8_t* p = lds + (at ^ (uint32_t)(x << 6)) + (4 * sub + ks) * 16 * C;
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t)p);
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t)(p + 4 * 2 * C));
+    const int2 a = __builtin_bit_cast(int2, lo), b = __builtin_bit_cast(int2, hi);
+    return v4i{a.x, a.y, b.x, b.y};
+  }
+};
 
-// Fragment of 16 bytes (sub-step ks of lane half h: contraction chunk 2 h + ks of the
-// stage) for the 32 rows / columns from r0.
-template <bool TR, int C>
-__device__ __forceinline__ v4i read_frag(const uint8_t* S, int r0, int ks) {
-  const int lane = threadIdx.x & 63, h = lane >> 5;
-  if (!TR) {
-    const int row = r0 + (lane & 31);
-    return *reinterpret_cast<const v4i*>(S + row * 64 + (((2 * h + ks) ^ swz64(lane & 31)) << 4));
-  }
-  // two transposing reads of 4 contraction rows x 16 columns per 16 lanes: lane j points at
-  // row j / 4, columns 4 (j % 4) .. + 3 and receives column j, the four rows
-  const int j = lane & 15;
-  const int k = 8 * (2 * h + ks) + (j >> 2);
-  const int col = r0 + (lane & 16) + 4 * (j & 3);
-  const uint32_t at = (uint32_t)(k * (2 * C) + (((col >> 3) ^ swzT(k)) << 4) + ((col & 7) << 1));
-  const uint8_t* p = S + at;
-  v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t)p);
-  v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t)(p + 4 * 2 * C));
-  const int2 a = __builtin_bit_cast(int2, lo), b = __builtin_bit_cast(int2, hi);
-  return v4i{a.x, a.y, b.x, b.y};
+__device__ __forceinline__ int read_word(const uint8_t* lds, uint32_t at) {
+  return *reinterpret_cast<const int*>(lds + at);
 }
 
 template <int TY>
@@ -222,249 +293,409 @@ struct GemmArgs {
   int T, E, least, most;  // groups with rows outside [least, most] are not this launch's
   int rows, cols, kdim;   // TN: output rows; columns; contraction length (NT, NN)
   int lds;                // scale bytes per row
-  int tiles;              // the launch's block count
+  int cus;                // blocks of the large tiles' launch
+  int direct;             // no large tiles: the small ones are counted by themselves
 };
 
-template <int TY, int LAY, int TO, int BM, int BN>
-__global__ void __launch_bounds__(256, 2) k_gemm(const GemmArgs p) {
-  using C = Tile<TY, LAY, BM, BN>;
+constexpr int kBig = 256;        // the large tiles: kBig x kBig outputs, one block per compute unit
+constexpr int kTailShare = 65;  // a last round of at least this many large tiles (of 256) is not cut up
+
+// Large tiles that a full grid of `cus` blocks takes in whole rounds; the rest is cut into
+// small tiles, which fill the chip where a round of few large tiles would leave most
+// compute units idle.
+__device__ __forceinline__ int whole_rounds(int total, int cus) {
+  const int rem = total % cus;
+  return rem * 256 >= kTailShare * cus ? total : total - rem;
+}
+
+// One output tile: its place, and where its operands start.  na, nb: bytes from there to the
+// end of the operand's last row (row-contiguous operands); the [contraction, columns] ones
+// are bounded by their rows, stage by stage.
+struct Work {
+  const uint8_t *pa, *pb, *ps;
+  int na, nb, ns;
+  int stages, kdim;
+  Group g;
+  int m0, n0;
+  bool live;
+};
+
+// The stage that is loaded next: ST stages ahead of the one at work, and so at times in the
+// next tile.
+struct Stream {
+  const uint8_t *pa, *pb, *ps;
+  int na, nb, ns;
+  int k, left;  // stage in the tile; contraction elements from it on
+  int xa, xb;   // bytes of a [contraction, columns] row in front of the tile
+};
+
+template <class C, int TO>
+__global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 : 2) k_gemm(const GemmArgs p) {
+  constexpr int TY = C::TY, LAY = C::LAY, BM = C::BM, BN = C::BN;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wid >> 1, wn = wid & 1;
-  const int tiles_n = (p.cols + BN - 1) / BN;
+  const int wm = wid / C::WAVES_N, wn = wid % C::WAVES_N;
+  constexpr bool BIG = BM == kBig;
+  // ---- the launch's list: large tiles [0, whole), or the small tiles that the others
+  // contain, or (direct) all of the small tiles
+  const bool cut = !BIG && !p.direct;
+  const int um = BIG || cut ? kBig : BM, un = BIG || cut ? kBig : BN;  // a unit of the list's order
+  const int units_n = (p.cols + un - 1) / un;
+  const int units_m = (p.rows + um - 1) / um;  // TN
+  Groups gr;
+  gr.offsets = p.offsets;
+  gr.at = reinterpret_cast<int*>(lds + C::GROUPS + wid * 768);
+  gr.E = p.E;
+  gr.T = p.T;
+  gr.bm = um;
+  gr.per_tile = units_n;
+  gr.least = p.least;
+  gr.most = p.most;
+  gr.done = 0;
+  const int total = LAY == L_TN ? p.E * units_m * units_n : gr.total();
+  const int whole = BIG || cut ? whole_rounds(total, p.cus) : 0;
+  constexpr int PER_M = kBig / BM, PER = PER_M * (kBig / BN);
+  const int list = BIG ? whole : cut ? (total - whole) * PER : total;
 
-  // ---- the block's tile
-  Group g;
-  int tm, tn;
-  const int slot = xcd_slot(blockIdx.x, gridDim.x);
-  if (LAY == L_TN) {
-    const int tiles_m = (p.rows + BM - 1) / BM;
-    const int e = slot / (tiles_m * tiles_n);
-    const int in = slot - e * tiles_m * tiles_n;
-    tn = in / tiles_m;
-    tm = in - tn * tiles_m;
-    if (p.offsets == nullptr)
-      g = Group{0, 0, p.T};
-    else
-      g = group_rows(p.offsets, e, p.T);
-  } else {
-    int unit;
-    if (!find_unit(p.offsets, p.E, p.T, slot, BM, tiles_n, p.least, p.most, g, unit)) return;
-    // patches of 8 row tiles: the weight tile of one column is read for all of them in turn
-    const int tiles_m = (g.rows + BM - 1) / BM;
-    const int patch = unit / (8 * tiles_n), first = patch * 8;
-    const int size = tiles_m - first < 8 ? tiles_m - first : 8;
-    const int in = unit - patch * 8 * tiles_n;
-    tn = in / size;
-    tm = first + in - tn * size;
-  }
-  const int m0 = tm * BM, n0 = tn * BN;  // first output row (inside the group, or of dW) and column
-  const int kdim = LAY == L_TN ? g.rows : p.kdim;
-  const int KT = (kdim + C::BK - 1) / C::BK;
-
-  // ---- operand tiles: first byte, bytes to the operand's end, bytes per stage step
   const uint32_t lda = (uint32_t)((LAY == L_TN ? p.rows : p.kdim) * C::EB);
   const uint32_t ldb = (uint32_t)((LAY == L_NT ? p.kdim : p.cols) * C::EB);
-  const uint8_t *pa, *pb;
-  int64_t na, nb, da, db;
-  if (C::TA) {
-    pa = p.A + (int64_t)g.row0 * lda + (int64_t)m0 * C::EB;
-    na = (int64_t)g.rows * lda - (int64_t)m0 * C::EB;
-    da = (int64_t)C::BK * lda;
-  } else {
-    pa = p.A + (int64_t)(g.row0 + m0) * lda;
-    na = (int64_t)(g.rows - m0) * lda;
-    da = 64;
-  }
-  if (LAY == L_NT) {
-    pb = p.B + ((int64_t)g.e * p.cols + n0) * ldb;
-    nb = (int64_t)(p.cols - n0) * ldb;
-    db = 64;
-  } else if (LAY == L_NN) {
-    pb = p.B + (int64_t)g.e * p.kdim * ldb + (int64_t)n0 * C::EB;
-    nb = (int64_t)p.kdim * ldb - (int64_t)n0 * C::EB;
-    db = (int64_t)C::BK * ldb;
-  } else {
-    pb = p.B + (int64_t)g.row0 * ldb + (int64_t)n0 * C::EB;
-    nb = (int64_t)g.rows * ldb - (int64_t)n0 * C::EB;
-    db = (int64_t)C::BK * ldb;
-  }
-  // 8-bit: waves 0 and 1 bring 64 rows' scale dwords each, waves 2 and 3 the weight blocks'
-  const uint8_t* ps = nullptr;
-  int64_t ns = 0;
-  uint32_t so = 0;
-  if (C::F8) {
-    if (wid < 2) {
-      ps = p.sa + (int64_t)(g.row0 + m0) * p.lds;
-      ns = (int64_t)(g.rows - m0) * p.lds;
-      so = (uint32_t)((64 * wid + lane) * p.lds);
+  const int64_t da = C::TA ? (int64_t)C::BK * lda : 128, db = C::TB ? (int64_t)C::BK * ldb : 128;
+
+  auto locate = [&](int at, Work& w) {
+    w.live = at < list;
+    w.pa = p.A;
+    w.pb = p.B;
+    w.ps = p.sa;
+    w.na = w.nb = w.ns = w.kdim = 0;
+    w.stages = 2;
+    w.m0 = w.n0 = 0;
+    if (!w.live) return;
+    int unit = cut ? whole + at / PER : at;
+    const int part = cut ? at % PER : 0;
+    int tiles_m;
+    if (LAY == L_TN) {
+      const int e = unit / (units_m * units_n);
+      unit -= e * units_m * units_n;
+      w.g = group_rows(p.offsets, e, p.T);
+      tiles_m = units_m;
     } else {
-      const int blocks = (p.cols + 127) >> 7;
-      ps = p.sb + ((int64_t)g.e * blocks + (n0 >> 7)) * p.lds;
-      ns = (int64_t)(blocks - (n0 >> 7)) * p.lds;
-      so = (uint32_t)((lane & (BN / 128 - 1)) * p.lds);
+      w.g = gr.find(unit, unit);
+      tiles_m = (w.g.rows + um - 1) / um;
     }
-  }
-
-  uint32_t oa[C::AL], ob[C::BL];
-  int ka[C::AL], kb[C::BL];
-#pragma unroll
-  for (int q = 0; q < C::AL; ++q) oa[q] = lane_offset<C::TA, BM>(wid * C::AL + q, lane, lda, ka[q]);
-#pragma unroll
-  for (int q = 0; q < C::BL; ++q) ob[q] = lane_offset<C::TB, BN>(wid * C::BL + q, lane, ldb, kb[q]);
-
-  // Direct loads of stage kt.  Rows past the operand's end and stages past KT read zeros;
-  // so do the chunks past a row's end in the last stage, in both operands (what lies there
-  // may be a NaN, and 0 x NaN is not 0).
-  auto issue = [&](int kt, uint8_t* S) {
-    const bool live = kt < KT;
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(pa + (live ? kt * da : 0), live ? na - kt * da : 0);
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(pb + (live ? kt * db : 0), live ? nb - kt * db : 0);
-    const int left = kdim * C::EB - kt * 64;  // bytes of a contiguous row from this stage on
-#pragma unroll
-    for (int q = 0; q < C::AL; ++q) {
-      const uint32_t o = C::TA || ka[q] < left ? oa[q] : kOOB;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(S + (wid * C::AL + q) * 1024), 16, o, 0, 0, 0);
+    // patches of 8 row tiles: neighbouring tiles share both operands
+    const int patch = unit / (8 * units_n), top = patch * 8;
+    const int size = tiles_m - top < 8 ? tiles_m - top : 8;
+    const int in = unit - patch * 8 * units_n;
+    w.m0 = (top + in % size) * um + part % PER_M * BM;
+    w.n0 = in / size * un + part / PER_M * BN;
+    const int rows = LAY == L_TN ? p.rows : w.g.rows;
+    if (w.m0 >= rows || w.n0 >= p.cols) {  // a part of a large tile that hangs over the end
+      w.live = false;
+      return;
     }
-#pragma unroll
-    for (int q = 0; q < C::BL; ++q) {
-      const uint32_t o = C::TB || kb[q] < left ? ob[q] : kOOB;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(S + C::A_BYTES + (wid * C::BL + q) * 1024), 16, o, 0, 0,
-                                               0);
+    w.kdim = LAY == L_TN ? w.g.rows : p.kdim;
+    const int k = (w.kdim + C::BK - 1) / C::BK;
+    // a stream that goes on in the next tile is at most one tile ahead; stages past the end
+    // read zeros
+    w.stages = BIG && k < C::ST ? C::ST : (k < 1 ? 1 : k);
+    if (C::TA) {
+      w.pa = p.A + (int64_t)w.g.row0 * lda + (int64_t)w.m0 * C::EB;
+    } else {
+      w.pa = p.A + (int64_t)(w.g.row0 + w.m0) * lda;
+      w.na = (rows - w.m0 < BM ? rows - w.m0 : BM) * (int)lda;
     }
-    if (C::F8) {  // the dword of four 128-blocks that holds this stage's scale
-      const int64_t at = (int64_t)(kt >> 3) * 4;
-      const __amdgpu_buffer_rsrc_t rs = make_rsrc(ps + (live ? at : 0), live ? ns - at : 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(S + C::A_BYTES + C::B_BYTES + wid * 256), 4, so, 0, 0, 0);
+    if (LAY == L_NT) {
+      w.pb = p.B + ((int64_t)w.g.e * p.cols + w.n0) * ldb;
+      w.nb = (p.cols - w.n0 < BN ? p.cols - w.n0 : BN) * (int)ldb;
+    } else if (LAY == L_NN) {
+      w.pb = p.B + (int64_t)w.g.e * p.kdim * ldb + (int64_t)w.n0 * C::EB;
+    } else {
+      w.pb = p.B + (int64_t)w.g.row0 * ldb + (int64_t)w.n0 * C::EB;
+    }
+    if (C::F8) {
+      if (wid < BM / 64) {
+        const int n = rows - w.m0 - 64 * wid;
+        w.ps = p.sa + (int64_t)(w.g.row0 + w.m0 + 64 * wid) * p.lds;
+        w.ns = n <= 0 ? 0 : (n < 64 ? n : 64) * p.lds;
+      } else {
+        const int blocks = (p.cols + 127) >> 7, n = blocks - (w.n0 >> 7);
+        w.ps = p.sb + ((int64_t)w.g.e * blocks + (w.n0 >> 7)) * p.lds;
+        w.ns = (n < BN / 128 ? n : BN / 128) * p.lds;
+      }
     }
   };
 
-  v16f acc[C::MT][C::NT];
-#pragma unroll
-  for (int i = 0; i < C::MT; ++i)
-#pragma unroll
-    for (int j = 0; j < C::NT; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  using OA = Operand<C::TA, BM>;
+  using OB = Operand<C::TB, BN>;
+  // (a wave's loads are consecutive)
+  const uint32_t ra = OA::row(lane, lda), rb = OB::row(lane, ldb);
+  const int ca = OA::chunk(lane), cb = OB::chunk(lane);
+  const uint32_t fa = OA::frag(lane, wm * C::WM), fb = OB::frag(lane, wn * C::WN) + C::A_BYTES;
+  // 8-bit: the first BM / 64 waves bring 64 rows' scale dwords each, the others the weight blocks'
+  const uint32_t so = (uint32_t)((wid < BM / 64 ? lane : lane & (BN / 128 - 1)) * p.lds);
 
-  issue(0, lds);
-  issue(1, lds + C::STAGE);
-  int cur = 0;
-  for (int kt = 0; kt < KT; ++kt) {
-    // stage kt has landed (kt + 1 may be in flight); behind the barrier it is visible to all
-    // waves and every wave is done with stage kt - 1, whose buffer kt + 2 takes
-    wait_loads<C::LOADS>();
-    __builtin_amdgcn_s_barrier();
-    __asm__ volatile("" ::: "memory");
-    const int nxt = cur == 0 ? 2 : cur - 1;  // (cur + 2) % 3
-    issue(kt + 2, lds + nxt * C::STAGE);
-    const uint8_t* S = lds + cur * C::STAGE;
-    const uint8_t* SB = S + C::A_BYTES;
-    v4i af[C::MT][2], bf[C::NT][2];
+  // The stage loads.  Rows past the operand's end and stages past the last read zeros; so do
+  // the chunks past a row's end in the last stage, in both operands (what lies there may be a
+  // NaN, and 0 x NaN is not 0).  A wave's loads of an operand share one descriptor; the loop
+  // is bound by instruction issue, so a load costs one addition besides itself.
+  Stream ls;
+  rsrc_t dsa, dsb, dss;
+  uint32_t va[2], vb[2];  // lane offsets of even and odd loads
+  auto begin_tile = [&](const Work& w) {
+    const int ga = wid * C::AL * OA::ROWS, gb = wid * C::BL * OB::ROWS;  // the wave's first row
+    ls.pa = w.pa + (int64_t)ga * lda;
+    ls.pb = w.pb + (int64_t)gb * ldb;
+    ls.ps = w.ps;
+    ls.na = w.na - ga * (int)lda;
+    ls.nb = w.nb - gb * (int)ldb;
+    ls.ns = w.ns;
+    ls.k = 0;
+    ls.left = w.kdim;
+    ls.xa = w.m0 * C::EB;
+    ls.xb = w.n0 * C::EB;
+  };
+  // Descriptors and lane offsets of the stage, then on to the next one.
+  auto begin_stage = [&]() {
+    const int rows = ls.left < C::BK ? (ls.left < 0 ? 0 : ls.left) : C::BK;  // contraction rows of the stage
+    const int left = ls.left * C::EB;                                        // bytes of a contiguous row
+    const int ga = wid * C::AL * OA::ROWS, gb = wid * C::BL * OB::ROWS;
+    const int ba = C::TA ? (rows - ga) * (int)lda - ls.xa : ls.na;
+    const int bb = C::TB ? (rows - gb) * (int)ldb - ls.xb : ls.nb;
+    dsa = make_desc(ls.pa, left > 0 ? ba : 0);
+    dsb = make_desc(ls.pb, left > 0 ? bb : 0);
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const int xa = ca ^ OA::flip(f), xb = cb ^ OB::flip(f);
+      va[f] = C::TA || xa < left ? ra + xa : kOOB;
+      vb[f] = C::TB || xb < left ? rb + xb : kOOB;
+    }
+    if (C::F8) {  // the dword of four 128-blocks that holds this stage's scale
+      const int at = (ls.k >> 2) * 4;
+      dss = make_desc(ls.ps + at, left > 0 ? ls.ns - at : 0);
+    }
+    ls.pa += da;
+    ls.pb += db;
+    ls.na -= 128;
+    ls.nb -= 128;
+    ls.left -= C::BK;
+    ++ls.k;
+  };
+  auto issue_b = [&](int q, uint32_t S) {  // load number q of the stage's second operand
+    direct_load16(dsb, S + C::A_BYTES + (wid * C::BL + q) * 1024, vb[q & 1] + q * OB::ROWS * ldb);
+  };
+  auto issue_a = [&](int q, uint32_t S) {  // of the first one; the last is the scales'
+    if (q < C::AL)
+      direct_load16(dsa, S + (wid * C::AL + q) * 1024, va[q & 1] + q * OA::ROWS * lda);
+    else
+      direct_load4(dss, S + C::A_BYTES + C::B_BYTES + wid * 256, so);
+  };
+
+  // Fragments of one sub-step in registers.  Two sets alternate: while the matrix cores work
+  // on one, the other is read from LDS.
+  struct Frag {
+    v4i a[C::MT][2], b[C::NT][2];
+  };
+  struct Scales {
+    int x[C::MT], w;
+  };
+  auto read = [&](int q, uint32_t sa, uint32_t sb, int sub, Frag& f) {  // LDS read number q of a sub-step
+    const int x = q >> 1, ks = q & 1;
+    if (x < C::NT)
+      f.b[x][ks] = OB::read(lds, sb, x, sub, ks);
+    else
+      f.a[x - C::NT][ks] = OA::read(lds, sa, x - C::NT, sub, ks);
+  };
+  auto read_scales = [&](int kt, int start, Scales& s) {
+    const uint32_t at = start + C::A_BYTES + C::B_BYTES;
+    const int sh = 8 * (kt & 3);
+    s.w = (int)((uint32_t)read_word(lds, at + 4 * (BM + (wn * C::WN) / 128)) >> sh);
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i)
+      s.x[i] = (int)((uint32_t)read_word(lds, at + 4 * (wm * C::WM + 32 * i + (lane & 31))) >> sh);
+  };
+  v16f acc[C::MT][C::NT];
+  auto product = [&](int q, const Frag& f, const Scales& s) {  // matrix instruction number q of a sub-step
+    const int ks = q / (C::MT * C::NT), i = q % (C::MT * C::NT) / C::NT, j = q % C::NT;
+    if (C::F8) {
+      const v8i a = __builtin_shufflevector(f.a[i][0], f.a[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+      const v8i b = __builtin_shufflevector(f.b[j][0], f.b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 0, 0, 0, s.w, 0, s.x[i]);
+    } else {
+      acc[i][j] = mfma16<TY>(f.b[j][ks], f.a[i][ks], acc[i][j]);
+    }
+  };
+  // behind each matrix instruction: LDS reads of sub-step 0; and in each half of sub-step 1 the
+  // LDS reads and the direct loads of one operand
+  constexpr int PER_P = (C::READS + C::PRODUCTS - 1) / C::PRODUCTS;
+  constexpr int HALF = C::PRODUCTS / 2;
+  constexpr int RB = (2 * C::NT + HALF - 1) / HALF, RA = (2 * C::MT + HALF - 1) / HALF;
+  constexpr int IB = (C::BL + HALF - 1) / HALF, IA = (C::AX + HALF - 1) / HALF;
+
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;  // LDS address of the buffers
+  const int step = gridDim.x;
+  int at = xcd_slot(blockIdx.x, step);
+  Work cur, nxt;
+  locate(at, cur);
+  if (BIG ? at >= list : !cur.live) return;  // (small tiles: one per block)
+  locate(at + step, nxt);
+  begin_tile(cur);
+#pragma unroll
+  for (int s = 0; s < C::ST; ++s) {
+    begin_stage();
+#pragma unroll
+    for (int q = 0; q < C::BL; ++q) issue_b(q, lds0 + s * C::STAGE);
+#pragma unroll
+    for (int q = 0; q < C::AX; ++q) issue_a(q, lds0 + s * C::STAGE);
+  }
+  int ph = 0;  // start of the buffer of the stage at work
+  Frag f0, f1;
+  Scales sc, sn;
+  wait_loads<(C::ST - 1) * C::LOADS>();
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
+#pragma unroll
+  for (int q = 0; q < C::READS; ++q) read(q, fa, fb, 0, f0);
+  if (C::F8) read_scales(0, 0, sc);
+
+  // The stages of a block's consecutive tiles are one stream: the first stages of the next
+  // tile are loaded during the last ones of this tile, and while its epilogue runs.
+  for (;;) {
 #pragma unroll
     for (int i = 0; i < C::MT; ++i)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) af[i][ks] = read_frag<C::TA, BM>(S, wm * C::WM + 32 * i, ks);
+      for (int j = 0; j < C::NT; ++j)
 #pragma unroll
-    for (int j = 0; j < C::NT; ++j)
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+#pragma nounroll
+    for (int kt = 0; kt < cur.stages; ++kt) {
+      const uint32_t S = lds0 + ph;
+      const uint32_t sa = fa + ph, sb = fb + ph;
+      ph = ph == (C::ST - 1) * C::STAGE ? 0 : ph + C::STAGE;
+      const uint32_t na = fa + ph, nb = fb + ph;
+      // sub-step 0 from f0; f1 takes sub-step 1
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) bf[j][ks] = read_frag<C::TB, BN>(SB, wn * C::WN + 32 * j, ks);
-    if (C::F8) {
-      const uint32_t* sc = reinterpret_cast<const uint32_t*>(S + C::A_BYTES + C::B_BYTES);
-      const int sh = 8 * ((kt >> 1) & 3);
-      const int sw = (int)(sc[128 + (wn * C::WN) / 128] >> sh);
-      int sx[C::MT];
+      for (int q = 0; q < C::PRODUCTS; ++q) {
+        product(q, f0, sc);
 #pragma unroll
-      for (int i = 0; i < C::MT; ++i) sx[i] = (int)(sc[wm * C::WM + 32 * i + (lane & 31)] >> sh);
+        for (int r = PER_P * q; r < PER_P * (q + 1) && r < C::READS; ++r) read(r, sa, sb, 1, f1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // Behind this barrier every wave has its fragments of the stage, whose buffer takes stage
+      // kt + ST, and the next stage's second operand has landed for all waves; behind the one
+      // half a sub-step later the first operand has.  So the loads never run dry: half a stage
+      // is in flight at either barrier (with one barrier for both operands the loads alone
+      // took 1.5 times the matrix cores' time; outputs still being stored are newer than the
+      // loads waited for).
+      wait_loads<C::AX + (C::ST - 2) * C::LOADS>();
+      __builtin_amdgcn_s_barrier();
+      __asm__ volatile("" ::: "memory");
+      if (kt + C::ST == cur.stages) begin_tile(nxt);
+      begin_stage();
+      // sub-step 1 from f1; f0 takes the next stage's sub-step 0
 #pragma unroll
-      for (int i = 0; i < C::MT; ++i)
+      for (int q = 0; q < C::PRODUCTS; ++q) {
+        if (q == HALF) {
+          wait_vm<C::BL + (C::ST - 2) * C::LOADS>();
+          __builtin_amdgcn_s_barrier();
+          __asm__ volatile("" ::: "memory");
+          if (C::F8) read_scales(kt + 1 < cur.stages ? kt + 1 : 0, ph, sn);
+        }
+        product(q, f1, sc);
+        if (q < HALF) {
+#pragma unroll
+          for (int r = RB * q; r < RB * (q + 1) && r < 2 * C::NT; ++r) read(r, na, nb, 0, f0);
+#pragma unroll
+          for (int r = IB * q; r < IB * (q + 1) && r < C::BL; ++r) issue_b(r, S);
+        } else {
+#pragma unroll
+          for (int r = RA * (q - HALF); r < RA * (q - HALF + 1) && r < 2 * C::MT; ++r) read(2 * C::NT + r, na, nb, 0, f0);
+#pragma unroll
+          for (int r = IA * (q - HALF); r < IA * (q - HALF + 1) && r < C::AX; ++r) issue_a(r, S);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      sc = sn;
+    }
+
+    // ---- epilogue: lane l holds row l % 32 of a tile and columns 8 a + 4 (l / 32) + 0 .. 3 in
+    // registers 4 a .. 4 a + 3.  16-bit outputs pass through LDS, one 32 x 32 tile at a time
+    // in a part of the wave's own, so that whole 64-byte row pieces are stored.
+    if (cur.live) {
+      uint8_t* stg = lds + C::EPI + wid * 32 * C::EPI_ROW;
+      const int fr = lane & 31, h = lane >> 5;
+      constexpr int EO = TO == T_FP32 ? 4 : 2;
+      const int rows_left = (LAY == L_TN ? p.rows : cur.g.rows) - cur.m0 - wm * C::WM;
+      const int64_t out_row = (LAY == L_TN ? (int64_t)cur.g.e * p.rows : (int64_t)cur.g.row0) + cur.m0 + wm * C::WM;
+      const int c0 = cur.n0 + wn * C::WN;
+      uint8_t* out = static_cast<uint8_t*>(p.C) + (out_row * p.cols + c0) * EO;
+      const int64_t ldo = (int64_t)p.cols * EO;
+      const bool aligned = ldo % 16 == 0;
+#pragma unroll
+      for (int i = 0; i < C::MT; ++i) {
+        const int live = rows_left - 32 * i;
 #pragma unroll
         for (int j = 0; j < C::NT; ++j) {
-          const v8i a = __builtin_shufflevector(af[i][0], af[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
-          const v8i b = __builtin_shufflevector(bf[j][0], bf[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 0, 0, 0, sw, 0, sx[i]);
-        }
-    } else {
+          __builtin_amdgcn_sched_barrier(0);  // one tile's outputs at a time
+          const int cols = p.cols - c0 - 32 * j;
+          uint8_t* o = out + (32 * i) * ldo + 32 * j * EO;
+          if (TO == T_FP32) {
+            if (fr < live) {
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
+              for (int a = 0; a < 4; ++a) {
+                const int c = 8 * a + 4 * h;
+                float* y = reinterpret_cast<float*>(o + fr * ldo) + c;
+                if (c + 4 <= cols)  // columns are a multiple of 8 here: whole groups of four
+                  *reinterpret_cast<float4*>(y) = make_float4(acc[i][j][4 * a], acc[i][j][4 * a + 1],
+                                                              acc[i][j][4 * a + 2], acc[i][j][4 * a + 3]);
+              }
+            }
+          } else {
 #pragma unroll
-        for (int i = 0; i < C::MT; ++i)
+            for (int a = 0; a < 4; ++a)
+              *reinterpret_cast<uint2*>(stg + fr * C::EPI_ROW + (8 * a + 4 * h) * 2) =
+                  make_uint2(pack2<TO>(acc[i][j][4 * a], acc[i][j][4 * a + 1]),
+                             pack2<TO>(acc[i][j][4 * a + 2], acc[i][j][4 * a + 3]));
+            __builtin_amdgcn_wave_barrier();
+            if (aligned) {  // columns are a multiple of 8: whole 16-byte pieces
 #pragma unroll
-          for (int j = 0; j < C::NT; ++j) acc[i][j] = mfma16<TY>(bf[j][ks], af[i][ks], acc[i][j]);
-    }
-    cur = cur == 2 ? 0 : cur + 1;
-  }
-  wait_loads<0>();
-  __syncthreads();
-
-  // ---- epilogue: lane l holds row l % 32 of a tile and columns 8 a + 4 (l / 32) + 0 .. 3 in
-  // registers 4 a .. 4 a + 3.  A wave passes 32 rows x WN columns at a time through its own
-  // part of the ring and stores whole row pieces.
-  constexpr int OB = TO == T_FP32 ? 4 : 2;
-  constexpr int RS = C::WN * OB + 16;
-  static_assert(4 * 32 * RS <= C::RING, "epilogue staging fits the ring");
-  uint8_t* stg = lds + wid * 32 * RS;
-  const int fr = lane & 31, h = lane >> 5;
-  const int rows_left = (LAY == L_TN ? p.rows : g.rows) - m0 - wm * C::WM;
-  const int c0 = n0 + wn * C::WN, cols_left = p.cols - c0;
-  const int64_t out_row = (LAY == L_TN ? (int64_t)g.e * p.rows : (int64_t)g.row0) + m0 + wm * C::WM;
-  uint8_t* out = static_cast<uint8_t*>(p.C) + (out_row * p.cols + c0) * OB;
-  const bool whole = ((int64_t)p.cols * OB) % 16 == 0 && cols_left >= C::WN;
-#pragma unroll
-  for (int i = 0; i < C::MT; ++i) {
-#pragma unroll
-    for (int j = 0; j < C::NT; ++j)
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const float y0 = acc[i][j][4 * a], y1 = acc[i][j][4 * a + 1], y2 = acc[i][j][4 * a + 2],
-                    y3 = acc[i][j][4 * a + 3];
-        uint8_t* at = stg + fr * RS + (32 * j + 8 * a + 4 * h) * OB;
-        if (TO == T_FP32)
-          *reinterpret_cast<float4*>(at) = make_float4(y0, y1, y2, y3);
-        else
-          *reinterpret_cast<uint2*>(at) = make_uint2(pack2<TO>(y0, y1), pack2<TO>(y2, y3));
-      }
-    __builtin_amdgcn_wave_barrier();
-    const int live = rows_left - 32 * i < 32 ? rows_left - 32 * i : 32;
-    if (whole) {
-      constexpr int PER = C::WN * OB / 16;  // 16-byte pieces per row
-#pragma unroll
-      for (int q = 0; q < 32 * PER / 64; ++q) {
-        const int id = q * 64 + lane, r = id / PER, c = id % PER;
-        if (r < live)
-          *reinterpret_cast<v4i*>(out + (int64_t)(32 * i + r) * p.cols * OB + 16 * c) =
-              *reinterpret_cast<const v4i*>(stg + r * RS + 16 * c);
-      }
-    } else {
-      for (int r = 0; r < live; ++r)
-        for (int c = lane; c < C::WN; c += 64)
-          if (c < cols_left) {
-            if (TO == T_FP32)
-              reinterpret_cast<float*>(out + (int64_t)(32 * i + r) * p.cols * OB)[c] =
-                  reinterpret_cast<const float*>(stg + r * RS)[c];
-            else
-              reinterpret_cast<uint16_t*>(out + (int64_t)(32 * i + r) * p.cols * OB)[c] =
-                  reinterpret_cast<const uint16_t*>(stg + r * RS)[c];
+              for (int q = 0; q < 2; ++q) {
+                const int r = 16 * q + (lane >> 2), c = lane & 3;
+                const v4i v = *reinterpret_cast<const v4i*>(stg + r * C::EPI_ROW + 16 * c);
+                if (r < live && 8 * c < cols) *reinterpret_cast<v4i*>(o + r * ldo + 16 * c) = v;
+              }
+            } else {
+#pragma unroll 1
+              for (int r = h; r < 32; r += 2) {
+                const uint16_t v = *reinterpret_cast<const uint16_t*>(stg + r * C::EPI_ROW + 2 * fr);
+                if (r < live && fr < cols) reinterpret_cast<uint16_t*>(o + r * ldo)[fr] = v;
+              }
+            }
+            __builtin_amdgcn_wave_barrier();
           }
+        }
+      }
     }
-    __builtin_amdgcn_wave_barrier();
+    at += step;
+    if (at >= list) break;
+    cur = nxt;
+    locate(at + step, nxt);
   }
+  wait_loads<0>();  // the stages loaded past the last tile (zeros)
 }
 
-template <int TY, int LAY, int TO, int BM, int BN>
-hipError_t launch_gemm(const GemmArgs& a, hipStream_t st) {
-  using C = Tile<TY, LAY, BM, BN>;
+template <class C, int TO>
+hipError_t launch_gemm(const GemmArgs& a, int64_t blocks, hipStream_t st) {
   static thread_local int ready_dev = -1;
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   if (dev != ready_dev) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm<TY, LAY, TO, BM, BN>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, C::RING);
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm<C, TO>), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            C::LDS);
     if (e != hipSuccess) return e;
     ready_dev = dev;
   }
-  k_gemm<TY, LAY, TO, BM, BN><<<dim3((unsigned)a.tiles), 256, C::RING, st>>>(a);
+  k_gemm<C, TO><<<dim3((unsigned)blocks), C::THREADS, C::LDS, st>>>(a);
   return hipGetLastError();
 }
 
@@ -588,22 +819,24 @@ hipError_t launch_few(const GemmArgs& a, hipStream_t st) {
 // work; a group that is not a kernel's costs its blocks one look at the offsets.
 constexpr int kFew = 32;
 
+
+
+int device_cus() {
+  static thread_local int known_dev = -1, cus = 0;
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return 256;
+  if (dev != known_dev) {
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus < 1) return 256;
+    known_dev = dev;
+  }
+  return cus;
+}
+
 template <int TY, int LAY, int TO>
 hipError_t run_gemm(GemmArgs a, hipStream_t st) {
-  constexpr int BM = 128, BN = 256;
-  const int64_t tn = ((int64_t)a.cols + BN - 1) / BN;
-  int64_t tiles;
-  if (LAY == L_TN) {
-    tiles = (int64_t)a.E * (((int64_t)a.rows + BM - 1) / BM) * tn;
-  } else {
-    const int64_t full = (a.T + BM - 1) / BM;
-    const int64_t groups = a.E < a.T ? a.E : a.T;
-    tiles = (full + groups - 1) * tn;
-  }
-  if (tiles >= (int64_t(1) << 31) - 256) return hipErrorInvalidValue;
-  a.tiles = (int)tiles;
   a.least = 1;
   a.most = 0x7FFFFFFF;
+  a.cus = device_cus();
   if (LAY == L_NT) {
     const bool few = (int64_t)a.T <= (int64_t)kFew * a.E;
     if (few) {
@@ -614,7 +847,33 @@ hipError_t run_gemm(GemmArgs a, hipStream_t st) {
       a.least = kFew + 1;
     }
   }
-  return launch_gemm<TY, LAY, TO, BM, BN>(a, st);
+  // The most tiles there can be: exact for dW and without offsets, else each group may add
+  // one row tile.
+  const int64_t groups = a.E < a.T ? a.E : a.T;
+  auto tiles = [&](int64_t b) {
+    const int64_t tn = ((int64_t)a.cols + b - 1) / b;
+    if (LAY == L_TN) return (int64_t)a.E * (((int64_t)a.rows + b - 1) / b) * tn;
+    return (((int64_t)a.T + b - 1) / b + groups - 1) * tn;
+  };
+  const int64_t units = tiles(kBig);
+  // Small tiles: with four stages in flight where compute units get one of them each at most,
+  // else two blocks per unit with two stages each.
+  using Small4 = Tile<TY, LAY, 128, 128, 64, 64, 4>;
+  using Small2 = Tile<TY, LAY, 128, 128, 64, 64, 2>;
+  // They alone: where large tiles would not fill a round, or be mostly empty (groups that
+  // average less than a large tile's rows).
+  if (units * 256 < (int64_t)kTailShare * a.cus || (LAY != L_TN && (int64_t)a.T < kBig * groups)) {
+    a.direct = 1;
+    const int64_t n = tiles(128);
+    return 4 * n <= 5 * a.cus ? launch_gemm<Small4, TO>(a, n, st) : launch_gemm<Small2, TO>(a, n, st);
+  }
+  const hipError_t e =
+      launch_gemm<Tile<TY, LAY, kBig, kBig, 64, 128, 2>, TO>(a, units < a.cus ? units : a.cus, st);
+  if (e != hipSuccess) return e;
+  // what is left over: less than a round
+  const bool sure = LAY == L_TN || a.offsets == nullptr;
+  if (sure && (units % a.cus == 0 || units % a.cus * 256 >= (int64_t)kTailShare * a.cus)) return hipSuccess;
+  return launch_gemm<Small4, TO>(a, 4 * (sure ? units % a.cus : (units < a.cus ? units : a.cus)), st);
 }
 
 // ------------------------------------------------------------------------ quantizers
