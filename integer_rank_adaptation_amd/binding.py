@@ -126,7 +126,8 @@ def _stream(stream):
         return stream
     import torch
 
-    return torch.cuda.current_stream().cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of the Stream object's time
+    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
 
 
 def _check(status: int, where: str):

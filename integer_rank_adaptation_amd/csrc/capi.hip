@@ -355,11 +355,12 @@ int check_clip_outputs(int64_t count, const void* const* grads, void* const* out
   struct Range {
     uintptr_t lo, hi;
     int64_t tensor;
-    bool output;
   };
-  std::unique_ptr<Range[]> r(new (std::nothrow) Range[2 * (size_t)count]);
-  if (!r) return fail(INTLORA_EINVAL, "grad_clip: no host memory for %lld tensors", (long long)count);
-  int64_t n = 0;
+  std::unique_ptr<Range[]> mem(new (std::nothrow) Range[2 * (size_t)count]);
+  if (!mem) return fail(INTLORA_EINVAL, "grad_clip: no host memory for %lld tensors", (long long)count);
+  Range *w = mem.get(), *r = w + count;  // written; read by an output elsewhere
+  int64_t nw = 0, nr = 0;
+  bool sw = true, sr = true;  // (lists that were allocated in order need no sort)
   for (int64_t i = 0; i < count; ++i) {
     if (numel[i] == 0) continue;
     if (!out[i]) return fail(INTLORA_EINVAL, "grad_clip: output %lld is NULL", (long long)i);
@@ -367,19 +368,25 @@ int check_clip_outputs(int64_t count, const void* const* grads, void* const* out
       return fail(INTLORA_EALIGN, "grad_clip: pointer %p of output %lld not 16-byte aligned", out[i], (long long)i);
     const uintptr_t bytes = (uintptr_t)numel[i] * (dtype[i] == INTLORA_FP32 ? 4 : 2);
     const uintptr_t o = reinterpret_cast<uintptr_t>(out[i]), g = reinterpret_cast<uintptr_t>(grads[i]);
-    r[n++] = Range{o, o + bytes, i, true};
-    if (g != o) r[n++] = Range{g, g + bytes, i, false};
+    sw = sw && (nw == 0 || w[nw - 1].lo <= o);
+    w[nw++] = Range{o, o + bytes, i};
+    if (g == o) continue;
+    sr = sr && (nr == 0 || r[nr - 1].lo <= g);
+    r[nr++] = Range{g, g + bytes, i};
   }
-  std::sort(r.get(), r.get() + n, [](const Range& a, const Range& b) { return a.lo < b.lo; });
-  // one sweep: the furthest end of an output, and of any range, among those that start before
-  uintptr_t out_end = 0, any_end = 0;
-  for (int64_t k = 0; k < n; ++k) {
-    if (r[k].lo < out_end || (r[k].output && r[k].lo < any_end))
-      return fail(INTLORA_EINVAL, "grad_clip: the output or input of tensor %lld overlaps another output",
-                  (long long)r[k].tensor);
-    if (r[k].output && r[k].hi > out_end) out_end = r[k].hi;
-    if (r[k].hi > any_end) any_end = r[k].hi;
+  const auto before = [](const Range& a, const Range& b) { return a.lo < b.lo; };
+  if (!sw) std::sort(w, w + nw, before);
+  if (!sr) std::sort(r, r + nr, before);
+  int64_t bad = -1;
+  for (int64_t k = 1; k < nw && bad < 0; ++k)
+    if (w[k].lo < w[k - 1].hi) bad = w[k].tensor;
+  for (int64_t k = 0, j = 0; k < nr && bad < 0; ++k) {  // the outputs do not overlap each other here
+    while (j < nw && w[j].hi <= r[k].lo) ++j;
+    if (j < nw && w[j].lo < r[k].hi) bad = r[k].tensor;
   }
+  if (bad >= 0)
+    return fail(INTLORA_EINVAL, "grad_clip: the output or input of tensor %lld overlaps another output",
+                (long long)bad);
   return INTLORA_OK;
 }
 
@@ -769,7 +776,7 @@ int intlora_fp8_quant_act(int64_t M, int64_t n, int dtype, const void* X, uint8_
   if (M < 0 || M >= kMaxDim || n < 1 || n > kMaxFeatures || n % 16 != 0)
     return fail(INTLORA_ESHAPE, "fp8_quant_act needs n a multiple of 16 and <= 2^20 (got M=%lld n=%lld)", (long long)M,
                 (long long)n);
-  if (M * ((n + 127) / 128) >= (int64_t(1) << 34)) return fail(INTLORA_ESHAPE, "fp8_quant_act: too many blocks");
+  if (M * ((n + 127) / 128) >= kMaxDim) return fail(INTLORA_ESHAPE, "fp8_quant_act: too many blocks");
   if (M == 0) return ok();
   if ((s = check_ptrs({X, xq, sx}, "fp8_quant_act"))) return s;
   if ((s = ensure_device())) return s;

@@ -77,7 +77,9 @@ __device__ __forceinline__ void wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
-// The same, and every LDS read returned.
+// Every LDS read returned.
+__device__ __forceinline__ void wait_lgkm() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
+// Both.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
@@ -227,7 +229,7 @@ struct Tile {
 // An operand tile of C rows / columns in LDS.  Row-contiguous operands (TR = 0) lie as rows
 // of 128 bytes with the 16-byte chunk c of row r at c ^ (r / 2) % 8: the 16 lanes that a
 // 16-byte read serves at a time then touch every bank once.  [contraction, columns] operands
-// (TR = 1) lie as rows of 2 C bytes with chunk c of contraction row k at c ^ 4 (k % 4): a
+// (TR = 1) lie as rows of 2 C bytes with chunk c of contraction row k at c ^ swz(k): a
 // transposing read takes 4 rows x 64 bytes per 32 lanes, which this puts on different banks.
 // Direct loads bring 1 KB each, always whole runs of 128 bytes or more: with runs of 64 bytes
 // (twice as many requests to L2) the loads alone took 25 % longer.
@@ -235,16 +237,19 @@ template <bool TR, int C>
 struct Operand {
   static constexpr int PER = TR ? C / 8 : 8;  // 16-byte chunks per LDS row
   static constexpr int ROWS = 64 / PER;       // LDS rows per load
-  static_assert(C == 128 || C == 256, "the flip below");
+  static_assert(C == 64 || C == 128 || C == 256, "the swizzle below");
+  // TR: the 4 rows x 64 bytes of 32 lanes on different banks (rows of 128 bytes: 2 rows cover all)
+  static __device__ __forceinline__ int swz(int k) { return C == 64 ? 2 * (k & 2) : 4 * (k & 3); }
   // This lane's place in a load: byte offset of its row, and of its chunk in the row for even
   // loads; the swizzle flips bit 6 of the latter for odd ones (C = 128 columns: not).
   static __device__ __forceinline__ uint32_t row(int lane, uint32_t ld) { return (uint32_t)(lane / PER) * ld; }
   static __device__ __forceinline__ int chunk(int lane) {
     const int r = lane / PER;
-    return 16 * ((lane % PER) ^ (TR ? 4 * (r & 3) : r >> 1));
+    return 16 * ((lane % PER) ^ (TR ? swz(r) : r >> 1));
   }
-  static __device__ __forceinline__ int flip(int q) { return (q & 1) == 0 || (TR && ROWS == 4) ? 0 : TR ? 128 : 64; }
-  // LDS offset of this lane's first fragment of the 32-row tiles from r0 (a multiple of 64);
+  static __device__ __forceinline__ int flip(int q) { return (q & 1) == 0 || (TR && ROWS != 2) ? 0 : TR ? 128 : 64; }
+  // LDS offset of this lane's first fragment of the 32-row tiles from r0 (a multiple of 32 x
+  // their number);
   // lane half h takes the contraction chunk 4 sub + 2 h + ks of a stage
   static __device__ __forceinline__ uint32_t frag(int lane, int r0) {
     const int h = lane >> 5, r = lane & 31;
@@ -252,7 +257,7 @@ struct Operand {
     // lane j of 16 points at contraction row j / 4, columns 4 (j % 4) .. + 3, and receives
     // column j, the four rows
     const int j = lane & 15, k = 16 * h + (j >> 2), col = r0 + (lane & 16) + 4 * (j & 3);
-    return (uint32_t)(k * (2 * C) + (((col >> 3) ^ (4 * (k & 3))) << 4) + ((col & 7) << 1));
+    return (uint32_t)(k * (2 * C) + (((col >> 3) ^ swz(k)) << 4) + ((col & 7) << 1));
   }
   // Fragment of 16 bytes of tile x from the operand's LDS at offset `at` = frag + its start.
   static __device__ __forceinline__ v4i read(const uint8_t* lds, uint32_t at, int x, int sub, int ks) {
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
       } else {
         const int blocks = (p.cols + 127) >> 7, n = blocks - (w.n0 >> 7);
         w.ps = p.sb + ((int64_t)w.g.e * blocks + (w.n0 >> 7)) * p.lds;
-        w.ns = (n < BN / 128 ? n : BN / 128) * p.lds;
+        w.ns = (n < (BN + 127) / 128 ? n : (BN + 127) / 128) * p.lds;
       }
     }
   };
@@ -432,7 +437,7 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
   const int ca = OA::chunk(lane), cb = OB::chunk(lane);
   const uint32_t fa = OA::frag(lane, wm * C::WM), fb = OB::frag(lane, wn * C::WN) + C::A_BYTES;
   // 8-bit: the first BM / 64 waves bring 64 rows' scale dwords each, the others the weight blocks'
-  const uint32_t so = (uint32_t)((wid < BM / 64 ? lane : lane & (BN / 128 - 1)) * p.lds);
+  const uint32_t so = (uint32_t)((wid < BM / 64 ? lane : lane & (BN / 128 > 1 ? 1 : 0)) * p.lds);
 
   // The stage loads.  Rows past the operand's end and stages past the last read zeros; so do
   // the chunks past a row's end in the last stage, in both operands (what lies there may be a
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
                 if (r < live && 8 * c < cols) *reinterpret_cast<v4i*>(o + r * ldo + 16 * c) = v;
               }
             } else {
-#pragma unroll 1
+#pragma unroll 4
               for (int r = h; r < 32; r += 2) {
                 const uint16_t v = *reinterpret_cast<const uint16_t*>(stg + r * C::EPI_ROW + 2 * fr);
                 if (r < live && fr < cols) reinterpret_cast<uint16_t*>(o + r * ldo)[fr] = v;
@@ -700,69 +705,167 @@ hipError_t launch_gemm(const GemmArgs& a, int64_t blocks, hipStream_t st) {
 }
 
 // ------------------------------------------------------------------------ few rows
-// Groups of few rows are bound by the weights' bytes: a block streams 16 weight rows
-// straight into registers, its waves taking runs of 512 bytes of the contraction in turn,
-// against 16 x TT token rows; the waves' sums meet in LDS in a fixed order.
-template <int TY, int TT>
-__global__ void __launch_bounds__(512, 2) k_few(const GemmArgs p) {
-  constexpr bool F8 = TY == T_FP8;
+// Groups of few rows are bound by the weights' bytes.  A tile is 16 weight rows against 16 TT
+// token rows; `ks` waves share one, taking runs of 256 bytes of the contraction in turn, and
+// their sums meet in LDS in a fixed order (ks = 1: every wave has tiles of its own, and no
+// barrier).  Each wave keeps a ring of runs of its own in LDS, filled by direct loads of 4 rows
+// x 256 bytes.  The grid is persistent and the runs of a wave's consecutive tiles are one
+// stream, so the memory is kept busy across a tile's end.  (Fragments loaded straight into registers take 16 bytes from
+// each of 16 rows per 16 lanes: 16-token products then streamed 3 TB/s.)
+template <int TY_, int TT_>
+struct Few {
+  static constexpr int TY = TY_, TT = TT_;
+  static constexpr bool F8 = TY == T_FP8;
+  static constexpr int WAVES = TT == 1 ? 8 : 4, RING = 2;       // streams of a block; runs in flight of each
+  static constexpr int RUN = 4096 * (1 + TT) + (F8 ? 512 : 0);  // LDS bytes of a run
+  static constexpr int LOADS = 4 * (1 + TT) + (F8 ? 2 : 0);     // direct loads of a run
+  static constexpr int SUMS = WAVES * RING * RUN, GROUPS = SUMS + 2 * WAVES * TT * 1024;
+  static constexpr int LDS = GROUPS + WAVES * 768;
+  static_assert(LDS <= 160 * 1024 && (RING - 1) * LOADS < 64, "LDS and load counter");
+};
+
+template <class C>
+__global__ void __launch_bounds__(64 * C::WAVES, 2) k_few(const GemmArgs p, int ks) {
+  constexpr int TY = C::TY, TT = C::TT, WAVES = C::WAVES, RING = C::RING;
+  constexpr bool F8 = C::F8;
   constexpr int EB = F8 ? 1 : 2;
   constexpr int TO = TY == T_FP16 ? T_FP16 : T_BF16;
-  __shared__ __attribute__((aligned(16))) float part[8][TT][256];
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int waves = blockDim.x >> 6;
   const int fr = lane & 15, q = lane >> 4;
-  Group g;
-  if (p.offsets == nullptr)
-    g = Group{0, 0, p.T};
-  else
-    g = group_rows(p.offsets, (int)blockIdx.y, p.T);
-  if (g.rows < p.least || g.rows > p.most || g.rows == 0) return;
-  const int n0 = blockIdx.x * 16;
-  const uint32_t ld = (uint32_t)(p.kdim * EB);
-  const int runs = (int)((ld + 511) >> 9);
-  const uint8_t* wb = p.B + ((int64_t)g.e * p.cols + n0) * ld;
-  const __amdgpu_buffer_rsrc_t rw = make_rsrc(wb, (int64_t)(p.cols - n0 < 16 ? p.cols - n0 : 16) * ld);
+  const int ld = p.kdim * EB;
+  const int runs = (ld + 255) >> 8;
+  const int tiles_n = (p.cols + 15) >> 4;
   const int blocks = (p.cols + 127) >> 7;
-  const uint8_t* swp = F8 ? p.sb + ((int64_t)g.e * blocks + (n0 >> 7)) * p.lds : nullptr;
+  Groups gr;
+  gr.offsets = p.offsets;
+  gr.at = reinterpret_cast<int*>(lds + C::GROUPS + wid * 768);
+  gr.E = p.E;
+  gr.T = p.T;
+  gr.bm = 16 * TT;
+  gr.per_tile = tiles_n;
+  gr.least = p.least;
+  gr.most = p.most;
+  gr.done = 0;
+  const int total = gr.total();
 
-  for (int t0 = 0; t0 < g.rows; t0 += 16 * TT) {
-    const int64_t row0 = (int64_t)g.row0 + t0;
-    const int rows = g.rows - t0 < 16 * TT ? g.rows - t0 : 16 * TT;
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.A + row0 * ld, (int64_t)rows * ld);
-    const __amdgpu_buffer_rsrc_t rsx = make_rsrc(F8 ? p.sa + row0 * p.lds : nullptr, F8 ? (int64_t)rows * p.lds : 0);
+  // A tile: 16 weight rows and up to 16 TT token rows of one group
+  struct Place {
+    const uint8_t *w, *x, *sw, *sx;
+    int wrows, xrows, n0;
+    int64_t row0;
+  };
+  auto locate = [&](int at, Place& t) {
+    if (at >= total) {  // past the block's last tile: no bytes
+      t.w = p.B;
+      t.x = p.A;
+      t.sw = p.sb;
+      t.sx = p.sa;
+      t.wrows = t.xrows = t.n0 = 0;
+      t.row0 = 0;
+      return;
+    }
+    int unit;
+    const Group g = gr.find(at, unit);
+    const int part = unit / tiles_n;  // 16 TT rows of the group
+    t.n0 = (unit - part * tiles_n) * 16;
+    t.row0 = (int64_t)g.row0 + part * 16 * TT;
+    t.xrows = g.rows - part * 16 * TT < 16 * TT ? g.rows - part * 16 * TT : 16 * TT;
+    t.wrows = p.cols - t.n0 < 16 ? p.cols - t.n0 : 16;
+    t.w = p.B + ((int64_t)g.e * p.cols + t.n0) * ld;
+    t.x = p.A + t.row0 * ld;
+    t.sw = F8 ? p.sb + ((int64_t)g.e * blocks + (t.n0 >> 7)) * p.lds : nullptr;
+    t.sx = F8 ? p.sa + t.row0 * p.lds : nullptr;
+  };
+
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds + wid * RING * C::RUN;
+  // Load l of an operand: rows 4 l .. 4 l + 3; the 16-byte chunk c of row r lies at c ^ r % 16,
+  // so that the 16 rows' chunks of one column are on different banks.
+  const int lrow = lane >> 4, lchunk = lane & 15;
+  uint32_t off[4];  // rows 4 l + lrow of the weights, and 16 l' more of the tokens
+  int chunk[4];
+#pragma unroll
+  for (int l = 0; l < 4; ++l) {
+    chunk[l] = 16 * (lchunk ^ (4 * l + lrow));
+    off[l] = (uint32_t)((4 * l + lrow) * ld) + chunk[l];
+  }
+  // Rows past the operand's end and chunks past a row's end read zeros (a NaN may lie there).
+  auto load_run = [&](const Place& t, int run, int place) {
+    const uint32_t S = lds0 + place * C::RUN;
+    const int k0 = run << 8, left = ld - k0;
+    const rsrc_t rw = make_desc(t.w + k0, t.wrows * ld - k0);
+    const rsrc_t rx = make_desc(t.x + k0, t.xrows * ld - k0);
+#pragma unroll
+    for (int l = 0; l < 4 * (1 + TT); ++l) {
+      const uint32_t o = chunk[l & 3] < left ? off[l & 3] : kOOB;
+      direct_load16(l < 4 ? rw : rx, S + 1024 * l, l < 8 ? o : o + 16 * ld);
+    }
+    if (F8) {  // the dword of four 128-blocks that holds the run's two scales
+      const int at = (run >> 1) * 4;
+      direct_load4(make_desc(t.sx + at, t.xrows * p.lds - at), S + 4096 * (1 + TT), (uint32_t)(lane * p.lds));
+      direct_load4(make_desc(t.sw + at, t.wrows > 0 ? 4 : 0), S + 4096 * (1 + TT) + 256, 0);
+    }
+  };
+
+  const int slots = WAVES / ks, slot = wid / ks, kw = wid - slot * ks;  // tiles at a time; this wave's; its share
+  const int step = gridDim.x * slots;
+  const int first = xcd_slot(blockIdx.x, gridDim.x) * slots;
+  if (first >= total) return;
+  const int mine = runs > kw ? (runs - kw + ks - 1) / ks : 0;  // runs of a tile that are this wave's
+  // The stream of loads is RING runs ahead, and so in one of the next tiles at times.
+  Place lp, cur;
+  int la = first + slot, lr = 0;  // its tile, and its run among the wave's
+  locate(la, lp);
+  auto load_next = [&](int place) {
+    if (lr == mine) {
+      lr = 0;
+      la += step;
+      locate(la, lp);
+    }
+    load_run(lp, kw + lr * ks, place);
+    ++lr;
+  };
+  if (mine > 0)
+    for (int r = 0; r < RING; ++r) load_next(r);
+  int place = 0, parity = 0;
+  for (int base = first; base < total; base += step) {
+    const int at = base + slot;  // (past the last tile: no bytes, no outputs)
     v4f acc[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int run = wid; run < runs; run += waves) {
-      v4i w[8], x[TT][8];
-      uint32_t swd = 0, sxd[TT];
+    for (int i = 0; i < mine; ++i) {
+      const int run = kw + i * ks;
+      wait_loads<(RING - 1) * C::LOADS>();  // all but the newer runs have landed
+      __asm__ volatile("" ::: "memory");
+      const uint8_t* S = lds + (wid * RING + place) * C::RUN;
+      v4i w[4], x[TT][4];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {  // chunk u: bytes 64 u + 16 q .. of the run
-        const uint32_t k = (uint32_t)run * 512 + 64 * u + 16 * q;
-        const uint32_t ow = k < ld ? (uint32_t)fr * ld + k : kOOB;
-        w[u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rw, ow, 0, 0));
+      for (int u = 0; u < 4; ++u) {
+        const int c = ((4 * u + q) ^ fr) << 4;
+        w[u] = *reinterpret_cast<const v4i*>(S + fr * 256 + c);
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const uint32_t ox = k < ld ? (uint32_t)(16 * t + fr) * ld + k : kOOB;
-          x[t][u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, ox, 0, 0));
-        }
+        for (int t = 0; t < TT; ++t) x[t][u] = *reinterpret_cast<const v4i*>(S + 4096 * (1 + t) + fr * 256 + c);
       }
+      int sw = 0, sx[TT];
       if (F8) {
-        swd = *reinterpret_cast<const uint32_t*>(swp + 4 * run);
+        const int sh = 16 * (run & 1);
+        sw = (int)((uint32_t)read_word(S, 4096 * (1 + TT) + 256) >> sh);
 #pragma unroll
         for (int t = 0; t < TT; ++t)
-          sxd[t] = __builtin_amdgcn_raw_buffer_load_b32(rsx, (uint32_t)((16 * t + fr) * p.lds + 4 * run), 0, 0);
+          sx[t] = (int)((uint32_t)read_word(S, 4096 * (1 + TT) + 4 * (16 * t + fr)) >> sh);
       }
+      wait_lgkm();  // the run is in registers: its place takes the next one
+      load_next(place);
+      place = place == RING - 1 ? 0 : place + 1;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
           if (F8) {
             const v8i a = __builtin_shufflevector(x[t][2 * u], x[t][2 * u + 1], 0, 1, 2, 3, 4, 5, 6, 7);
             const v8i b = __builtin_shufflevector(w[2 * u], w[2 * u + 1], 0, 1, 2, 3, 4, 5, 6, 7);
-            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc[t], 0, 0, 0, (int)(swd >> (8 * u)), 0,
-                                                                      (int)(sxd[t] >> (8 * u)));
+            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc[t], 0, 0, 0, sw >> (8 * u), 0,
+                                                                      sx[t] >> (8 * u));
           } else {
 #pragma unroll
             for (int v = 2 * u; v < 2 * u + 2; ++v) {
@@ -776,48 +879,81 @@ __global__ void __launch_bounds__(512, 2) k_few(const GemmArgs p) {
           }
         }
     }
-#pragma unroll
-    for (int t = 0; t < TT; ++t) *reinterpret_cast<v4f*>(&part[wid][t][4 * lane]) = acc[t];
-    __syncthreads();
     // lane l of a tile: token l % 16, columns 4 (l / 16) + 0 .. 3
-    for (int id = tid; id < TT * 64; id += blockDim.x) {
-      const int t = id >> 6, l = id & 63;
-      v4f s = v4f{0.f, 0.f, 0.f, 0.f};
-      for (int w = 0; w < waves; ++w) s += *reinterpret_cast<const v4f*>(&part[w][t][4 * l]);
-      const int row = 16 * t + (l & 15), col = n0 + 4 * (l >> 4);
-      if (row < rows) {
-        uint16_t* y = static_cast<uint16_t*>(p.C) + (row0 + row) * p.cols + col;
-        const uint32_t lo = pack2<TO>(s.x, s.y), hi = pack2<TO>(s.z, s.w);
-        if ((p.cols & 3) == 0 && col + 4 <= p.cols) {
-          *reinterpret_cast<uint2*>(y) = make_uint2(lo, hi);
-        } else {
-          const uint16_t v[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+    auto store = [&](int t, v4f s) {
+      const int row = 16 * t + fr, col = cur.n0 + 4 * q;
+      if (row >= cur.xrows) return;
+      uint16_t* y = static_cast<uint16_t*>(p.C) + (cur.row0 + row) * p.cols + col;
+      const uint32_t lo = pack2<TO>(s.x, s.y), hi = pack2<TO>(s.z, s.w);
+      if ((p.cols & 3) == 0 && col + 4 <= p.cols) {
+        *reinterpret_cast<uint2*>(y) = make_uint2(lo, hi);
+      } else {
+        const uint16_t o[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (col + c < p.cols) y[c] = v[c];
-        }
+        for (int c = 0; c < 4; ++c)
+          if (col + c < p.cols) y[c] = o[c];
+      }
+    };
+    if (ks == 1) {
+      locate(at, cur);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) store(t, acc[t]);
+    } else {
+      // the sums of even and odd tiles take turns, so one barrier a tile is enough
+      float* part = reinterpret_cast<float*>(lds + C::SUMS) + parity * WAVES * TT * 256;
+      parity ^= 1;
+#pragma unroll
+      for (int t = 0; t < TT; ++t) *reinterpret_cast<v4f*>(part + (wid * TT + t) * 256 + 4 * lane) = acc[t];
+      wait_lgkm();
+      __builtin_amdgcn_s_barrier();
+      __asm__ volatile("" ::: "memory");
+      if (kw < TT) {  // ks >= TT
+        locate(at, cur);
+        v4f s = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int v = 0; v < ks; ++v)
+          s += *reinterpret_cast<const v4f*>(part + ((slot * ks + v) * TT + kw) * 256 + 4 * lane);
+        store(kw, s);
       }
     }
-    __syncthreads();
   }
+  wait_loads<0>();
 }
 
-template <int TY>
-hipError_t launch_few(const GemmArgs& a, hipStream_t st) {
-  const int runs = (int)(((int64_t)a.kdim * (TY == T_FP8 ? 1 : 2) + 511) / 512);
-  const int waves = runs >= 8 ? 8 : runs >= 4 ? 4 : runs >= 2 ? 2 : 1;
-  const dim3 grid((unsigned)((a.cols + 15) / 16), (unsigned)a.E);
-  if (a.most <= 16)
-    k_few<TY, 1><<<grid, 64 * waves, 0, st>>>(a);
-  else
-    k_few<TY, 2><<<grid, 64 * waves, 0, st>>>(a);
+template <int TY, int TT>
+hipError_t launch_few_tt(const GemmArgs& a, hipStream_t st) {
+  using C = Few<TY, TT>;
+  static thread_local int ready_dev = -1;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  if (dev != ready_dev) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_few<C>), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            C::LDS);
+    if (e != hipSuccess) return e;
+    ready_dev = dev;
+  }
+  const int64_t groups = a.E < a.T ? a.E : a.T;
+  const int64_t tiles = ((int64_t)a.cols + 15) / 16 * ((a.T + 16 * TT - 1) / (16 * TT) + groups - 1);
+  int ks = C::WAVES;
+  const int64_t runs = ((int64_t)a.kdim * (TY == T_FP8 ? 1 : 2) + 255) / 256;
+  while (ks > 1 && runs < 2 * ks && tiles * ks >= 2 * (int64_t)a.cus * C::WAVES) ks /= 2;
+  const int64_t blocks = (tiles * ks + C::WAVES - 1) / C::WAVES;
+  k_few<C><<<dim3((unsigned)(blocks < a.cus ? blocks : a.cus)), 64 * C::WAVES, C::LDS, st>>>(a, ks);
   return hipGetLastError();
 }
 
-// Groups of up to kFew rows go to the few-row kernel, the others to the tiled one.  Without
-// the offsets (device memory) the host knows only T and E, so it launches whichever can have
-// work; a group that is not a kernel's costs its blocks one look at the offsets.
-constexpr int kFew = 32;
+// 16 token rows at a time also where groups average half as many: one of 17 to 32 rows then
+// reads its weights twice (the second time from cache).
+template <int TY>
+hipError_t launch_few(const GemmArgs& a, hipStream_t st) {
+  const int64_t groups = a.E < a.T ? a.E : a.T;
+  return a.most <= 16 || a.T <= 8 * groups ? launch_few_tt<TY, 1>(a, st) : launch_few_tt<TY, 2>(a, st);
+}
+
+// Groups of few rows go to the few-row kernel, the others to the tiled one.  Without the
+// offsets (device memory) the host knows only T and E, so it launches whichever can have work;
+// a group that is not a kernel's has no tiles there.
+constexpr int kFew = 16;
 
 
 
@@ -837,16 +973,6 @@ hipError_t run_gemm(GemmArgs a, hipStream_t st) {
   a.least = 1;
   a.most = 0x7FFFFFFF;
   a.cus = device_cus();
-  if (LAY == L_NT) {
-    const bool few = (int64_t)a.T <= (int64_t)kFew * a.E;
-    if (few) {
-      GemmArgs f = a;
-      f.most = a.T < kFew ? a.T : kFew;
-      const hipError_t e = launch_few<TY>(f, st);
-      if (e != hipSuccess || a.T <= kFew) return e;
-      a.least = kFew + 1;
-    }
-  }
   // The most tiles there can be: exact for dW and without offsets, else each group may add
   // one row tile.
   const int64_t groups = a.E < a.T ? a.E : a.T;
@@ -855,6 +981,20 @@ hipError_t run_gemm(GemmArgs a, hipStream_t st) {
     if (LAY == L_TN) return (int64_t)a.E * (((int64_t)a.rows + b - 1) / b) * tn;
     return (((int64_t)a.T + b - 1) / b + groups - 1) * tn;
   };
+  if (LAY == L_NT) {
+    // Few rows: 16 to a group on average, or 32 in all, or so little work that tiles would
+    // leave most compute units idle (4096 x 4096 in 8 bits: 64 rows 10 us against 23, 128 rows
+    // 15 against 23; 14336 x 4096, 64 rows: 27 against 25).
+    const bool little = (a.T + 32 * groups - 1) / (32 * groups) * tiles(128) * 2 <= a.cus;
+    if (little || a.T <= kFew * groups || a.T <= 2 * kFew) {
+      GemmArgs f = a;
+      const int limit = little ? 8 * kFew : 2 * kFew;
+      f.most = a.T < limit ? a.T : limit;
+      const hipError_t e = launch_few<TY>(f, st);
+      if (e != hipSuccess || a.T <= limit) return e;
+      a.least = limit + 1;
+    }
+  }
   const int64_t units = tiles(kBig);
   // Small tiles: with four stages in flight where compute units get one of them each at most,
   // else two blocks per unit with two stages each.
@@ -864,7 +1004,9 @@ hipError_t run_gemm(GemmArgs a, hipStream_t st) {
   // average less than a large tile's rows).
   if (units * 256 < (int64_t)kTailShare * a.cus || (LAY != L_TN && (int64_t)a.T < kBig * groups)) {
     a.direct = 1;
-    const int64_t n = tiles(128);
+    const int64_t n = tiles(128), n64 = tiles(64);
+    if (n64 <= a.cus) return launch_gemm<Tile<TY, LAY, 64, 64, 32, 64, 8>, TO>(a, n64, st);
+    if (n64 <= 2 * a.cus) return launch_gemm<Tile<TY, LAY, 64, 64, 32, 64, 4>, TO>(a, n64, st);
     return 4 * n <= 5 * a.cus ? launch_gemm<Small4, TO>(a, n, st) : launch_gemm<Small2, TO>(a, n, st);
   }
   const hipError_t e =
@@ -941,18 +1083,19 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], uint32_t byte) {
 }
 
 // Activations: 16 lanes take one block of 1 x 128 (8 elements each); the largest magnitude
-// goes round the 16 lanes as integer bits, so a NaN wins.
+// goes round the 16 lanes as integer bits, so a NaN wins.  Bound by memory: 8192 x 14336 bf16
+// 65 us, 5.4 TB/s (two or four blocks per 16 lanes with their loads together: the same or
+// slower, and 0.3 to 1.4 us more at 64 x 4096).
 template <int TI>
-__global__ void __launch_bounds__(256) k_fp8_act(int64_t units, int n, int nb, int lds, const void* __restrict__ X,
-                                                 uint8_t* __restrict__ xq, uint8_t* __restrict__ sx) {
-  const int64_t u = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int l = threadIdx.x & 15;
+__global__ void __launch_bounds__(256) k_fp8_act(uint32_t units, uint32_t n, uint32_t nb, uint32_t lds,
+                                                 const void* __restrict__ X, uint8_t* __restrict__ xq,
+                                                 uint8_t* __restrict__ sx) {
+  const uint32_t l = threadIdx.x & 15;
+  const uint32_t u = blockIdx.x * 16 + (threadIdx.x >> 4);
   if (u >= units) return;  // whole groups of 16 lanes leave together
-  const int64_t row = u / nb;
-  const int b = (int)(u - row * nb);
-  const int k = 128 * b + 8 * l;
+  const uint32_t row = u / nb, b = u - row * nb, k = 128 * b + 8 * l;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (k < n) load8<TI>(X, row * n + k, v);
+  if (k < n) load8<TI>(X, (int64_t)row * n + k, v);
   uint32_t m = amax8(v);
 #pragma unroll
   for (int s = 8; s; s >>= 1) {
@@ -960,9 +1103,9 @@ __global__ void __launch_bounds__(256) k_fp8_act(int64_t units, int n, int nb, i
     m = o > m ? o : m;
   }
   const uint32_t byte = scale_byte(m);
-  if (k < n) *reinterpret_cast<uint2*>(xq + row * n + k) = codes8(v, byte);
-  if (l == 0) sx[row * lds + b] = (uint8_t)byte;
-  if (b == nb - 1 && l > 0 && b + l < lds) sx[row * lds + b + l] = 127;
+  if (k < n) *reinterpret_cast<uint2*>(xq + (int64_t)row * n + k) = codes8(v, byte);
+  if (l == 0 || (b == nb - 1 && b + l < lds))  // and the bytes that pad the row
+    sx[(int64_t)row * lds + b + l] = (uint8_t)(l == 0 ? byte : 127u);
 }
 
 // Weights: one block of 128 x 128 per workgroup, and, when asked for, the same codes
@@ -1037,15 +1180,14 @@ int fp8_scale_stride(int64_t n) { return (int)(4 * ((n + 511) / 512)); }
 
 hipError_t launch_fp8_quant_act(int64_t M, int64_t n, int dtype, const void* X, uint8_t* xq, uint8_t* sx,
                                 hipStream_t st) {
-  const int nb = (int)((n + 127) / 128), lds = fp8_scale_stride(n);
-  const int64_t units = M * nb;
-  const dim3 grid((unsigned)((units + 15) / 16));
+  const uint32_t nb = (uint32_t)((n + 127) / 128), lds = (uint32_t)fp8_scale_stride(n), units = (uint32_t)(M * nb);
+  const dim3 grid((units + 15) / 16);
   if (dtype == T_FP32)
-    k_fp8_act<T_FP32><<<grid, 256, 0, st>>>(units, (int)n, nb, lds, X, xq, sx);
+    k_fp8_act<T_FP32><<<grid, 256, 0, st>>>(units, (uint32_t)n, nb, lds, X, xq, sx);
   else if (dtype == T_FP16)
-    k_fp8_act<T_FP16><<<grid, 256, 0, st>>>(units, (int)n, nb, lds, X, xq, sx);
+    k_fp8_act<T_FP16><<<grid, 256, 0, st>>>(units, (uint32_t)n, nb, lds, X, xq, sx);
   else
-    k_fp8_act<T_BF16><<<grid, 256, 0, st>>>(units, (int)n, nb, lds, X, xq, sx);
+    k_fp8_act<T_BF16><<<grid, 256, 0, st>>>(units, (uint32_t)n, nb, lds, X, xq, sx);
   return hipGetLastError();
 }
 

@@ -19,6 +19,8 @@ enum { D_BF16 = 0, D_FP16 = 1, D_FP32 = 2 };
 constexpr int kPerLaunch = 112;     // 112 x 32 bytes of entries: under the 4 KB of kernel arguments
 constexpr int kChunk = 16384;       // elements per block
 constexpr int kThreads = 256;
+constexpr int kSmallChunks = 16;    // at most so many chunks are summed by one block
+constexpr int64_t kMaxTensors = 65536;
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef float f2 __attribute__((ext_vector_type(2)));
@@ -40,17 +42,16 @@ struct Table {
 };
 static_assert(sizeof(Table) + 64 <= 4096, "kernel arguments are limited to 4 KB");
 
-// The entry that chunk c belongs to (entries have ascending chunk0; uniform over the block).
+// The entry that chunk c belongs to (entries have ascending chunk0): the lanes look at all
+// entries at once, where a binary search would be seven dependent loads.
 __device__ __forceinline__ int find_entry(const Table& t, int c) {
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.t[mid].chunk0 <= c)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  return lo;
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kPerLaunch; i += 64)
+    n += __builtin_popcountll(
+        __builtin_amdgcn_ballot_w64(i + lane < t.count && t.t[i + lane < kPerLaunch ? i + lane : 0].chunk0 <= c));
+  return n - 1;
 }
 
 template <int D>
@@ -82,8 +83,7 @@ __device__ __forceinline__ void widen(u4 r, float* v) {
 template <int D>
 __device__ __forceinline__ double sum_chunk(const void* src, int64_t i0, int64_t i1) {
   constexpr int V = D == D_FP32 ? 4 : 8;
-  constexpr int STEP = kThreads * V;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x & (kThreads - 1);
   double s = 0.0;
   const int64_t full = i0 + (i1 - i0) / V * V;
   const u4* p = reinterpret_cast<const u4*>(static_cast<const uint8_t*>(src) + i0 * (D == D_FP32 ? 4 : 2));
@@ -105,7 +105,6 @@ __device__ __forceinline__ double sum_chunk(const void* src, int64_t i0, int64_t
     const double v = (double)load1<D>(src, i);
     s = fma(v, v, s);
   }
-  (void)STEP;
   return s;
 }
 
@@ -134,11 +133,44 @@ __global__ void __launch_bounds__(kThreads) k_grad_sumsq(const Table t, double* 
   if (threadIdx.x == 0) partial[t.partial0 + c] = (w[0] + w[1]) + (w[2] + w[3]);
 }
 
+// Small lists: one block takes all chunks, in order, and writes the sum itself (one launch
+// less: 56 k elements 5 us against 6 + the gap between two launches).
+__global__ void __launch_bounds__(1024) k_grad_sumsq_small(const Table t, double* __restrict__ sumsq) {
+  __shared__ double w[16];
+  const int sub = threadIdx.x >> 8;  // four chunks at a time
+  double s = 0.0;
+  for (int c = sub; c < t.chunks; c += 4) {
+    const Entry& e = t.t[__builtin_amdgcn_readfirstlane(find_entry(t, c))];
+    const int64_t i0 = (int64_t)(c - e.chunk0) * kChunk;
+    const int64_t i1 = i0 + kChunk < e.numel ? i0 + kChunk : e.numel;
+    if (e.dtype == D_FP32)
+      s += sum_chunk<D_FP32>(e.src, i0, i1);
+    else if (e.dtype == D_FP16)
+      s += sum_chunk<D_FP16>(e.src, i0, i1);
+    else
+      s += sum_chunk<D_BF16>(e.src, i0, i1);
+  }
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double r = 0.0;
+    for (int k = 0; k < 16; ++k) r += w[k];
+    sumsq[0] = r;
+  }
+}
+
 __global__ void __launch_bounds__(1024) k_grad_total(const double* __restrict__ partial, int64_t n,
                                                      double* __restrict__ sumsq) {
   __shared__ double w[16];
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += 1024) s += partial[i];
+  for (int64_t i = threadIdx.x; i < n; i += 8 * 1024) {  // eight loads in flight
+    double v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = i + u * 1024 < n ? partial[i + u * 1024] : 0.0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += v[u];
+  }
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = s;
   __syncthreads();
@@ -252,6 +284,10 @@ hipError_t launch_grad_sumsq(int64_t count, const void* const* src, const int64_
     i = fill(t, i, count, src, nullptr, numel, dtype);
     if (t.count == 0) break;
     t.partial0 = done;
+    if (done == 0 && i == count && t.chunks <= kSmallChunks) {
+      k_grad_sumsq_small<<<1, 1024, 0, st>>>(t, sumsq);
+      return hipGetLastError();
+    }
     k_grad_sumsq<<<dim3((unsigned)t.chunks), kThreads, 0, st>>>(t, partial);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -265,15 +301,26 @@ hipError_t launch_grad_clip(int64_t count, const void* const* src, void* const* 
                             const int32_t* dtype, const double* sumsq, double max_norm, float* norm, hipStream_t st) {
   Table t;
   t.partial0 = 0;
-  bool first = true;
-  for (int64_t i = 0; i < count || first;) {
+  // where the launches' tensors begin; the last ones first (see k_grad_clip)
+  static_assert(kMaxTensors / kPerLaunch < 640, "launches of the longest list");
+  int64_t begin[640];
+  int launches = 0;
+  for (int64_t i = 0; i < count;) {
+    begin[launches] = i;
     i = fill(t, i, count, src, dst, numel, dtype);
-    if (t.count == 0 && (!first || norm == nullptr)) break;
-    k_grad_clip<<<dim3((unsigned)(t.chunks > 0 ? t.chunks : 1)), kThreads, 0, st>>>(t, sumsq, max_norm,
-                                                                                    first ? norm : nullptr);
+    if (t.count > 0) ++launches;
+  }
+  if (launches == 0) {
+    t.count = t.chunks = 0;
+    if (norm == nullptr) return hipSuccess;
+    k_grad_clip<<<1, kThreads, 0, st>>>(t, sumsq, max_norm, norm);
+    return hipGetLastError();
+  }
+  for (int k = launches - 1; k >= 0; --k) {
+    fill(t, begin[k], count, src, dst, numel, dtype);
+    k_grad_clip<<<dim3((unsigned)t.chunks), kThreads, 0, st>>>(t, sumsq, max_norm, k == 0 ? norm : nullptr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    first = false;
   }
   return hipSuccess;
 }

@@ -3,7 +3,9 @@ memory only) and run one IntLoRA step through libintlora.so.  No arithmetic of t
 method happens here."""
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 
 import torch
 
@@ -254,34 +256,44 @@ def linear_codes(xq, sx, ucode, wcode, z, zbar, sbar, d, acc_dbg=False, out=None
 
 # ---------------------------------------------------------------- floating-point layers
 _FLOAT = {torch.bfloat16: B.INTLORA_BF16, torch.float16: B.INTLORA_FP16, torch.float32: B.INTLORA_FP32}
+_HALF = (torch.bfloat16, torch.float16)
+_E4M3 = (torch.float8_e4m3fn,)
+_BYTES = (torch.uint8,)
 
 
-def _want(name, t, shape, *dtypes):
-    """t has this shape, one of these types, is contiguous and lies on the current device (where
-    the call is enqueued); ValueError otherwise."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+def _want(name, t, shape, dtypes, dev):
+    """The address of t, which has this shape, one of these types, is contiguous and lies on
+    the current device `dev` (where the call is enqueued); ValueError otherwise."""
+    if t.get_device() != dev:  # -1 for a host tensor
         raise ValueError(f"{name}: expected a tensor on the current device, got {t.device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype not in dtypes:
-        raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
-    return t
+    return t.data_ptr()
 
 
-def _dims(name, t, dim):
-    if t.dim() not in (dim if isinstance(dim, tuple) else (dim,)):
-        raise ValueError(f"{name}: expected {dim} dimensions, got shape {tuple(t.shape)}")
-    return tuple(t.shape)
+def _dims(name, t, *dims):
+    if t.dim() not in dims:
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dims))} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
 
 
-def _offsets(offsets, E):
+def _offsets(offsets, E, dev):
     if offsets is None:
         if E != 1:
             raise ValueError("offsets: needed with more than one group")
         return None
-    return _want("offsets", offsets, (E + 1,), torch.int64)
+    return _want("offsets", offsets, (E + 1,), (torch.int64,), dev)
+
+
+def _output(out, shape, dtype, like, dev):
+    if out is None:
+        out = like.new_empty(shape, dtype=dtype)
+        return out, out.data_ptr()
+    return out, _want("out", out, shape, (dtype,), dev)
 
 
 def fp8_scale_bytes(n):
@@ -290,15 +302,14 @@ def fp8_scale_bytes(n):
 
 
 def fp8_quant_act(X, out=None):
-    """e4m3 codes of X [M, n] (bf16, fp16 or fp32) and their scale bytes, one per 128 columns."""
+    """e4m3 codes of X [M, n] (bf16, fp16 or fp32) and their scale bytes, one per 128 columns:
+    (xq [M, n] float8_e4m3fn, sx [M, fp8_scale_bytes(n)] uint8)."""
     M, n = _dims("X", X, 2)
-    _want("X", X, (M, n), *_FLOAT)
-    xq, sx = out or (torch.empty((M, n), dtype=torch.float8_e4m3fn, device=X.device),
-                     torch.empty((M, fp8_scale_bytes(n)), dtype=torch.uint8, device=X.device))
-    if out:
-        _want("xq", xq, (M, n), torch.float8_e4m3fn)
-        _want("sx", sx, (M, fp8_scale_bytes(n)), torch.uint8)
-    B.intlora_fp8_quant_act(M, n, _FLOAT[X.dtype], X, xq, sx)
+    dev = torch.cuda.current_device()
+    x = _want("X", X, (M, n), _FLOAT, dev)
+    xq, xp = _output(out[0] if out else None, (M, n), torch.float8_e4m3fn, X, dev)
+    sx, sp = _output(out[1] if out else None, (M, fp8_scale_bytes(n)), torch.uint8, X, dev)
+    B.intlora_fp8_quant_act(M, n, _FLOAT[X.dtype], x, xp, sp)
     return xq, sx
 
 
@@ -306,41 +317,33 @@ def fp8_quant_weight(W, transpose=False):
     """e4m3 codes of a weight [d, n] or of E of them [E, d, n] with one scale per 128 x 128
     block: dict(wq, sw), and with `transpose` the same codes transposed (wq_t, sw_t), on which
     fp8_linear computes the input gradient dY W from dY's codes."""
-    shape = _dims("W", W, (2, 3))
-    _want("W", W, shape, *_FLOAT)
+    shape = _dims("W", W, 2, 3)
+    w = _want("W", W, shape, _FLOAT, torch.cuda.current_device())
     E, (d, n) = (shape[0] if len(shape) == 3 else 1), shape[-2:]
     lead = shape[:-2]
-    o = dict(wq=torch.empty(shape, dtype=torch.float8_e4m3fn, device=W.device),
-             sw=torch.empty((*lead, (d + 127) // 128, fp8_scale_bytes(n)), dtype=torch.uint8, device=W.device))
+    o = dict(wq=W.new_empty(shape, dtype=torch.float8_e4m3fn),
+             sw=W.new_empty((*lead, (d + 127) // 128, fp8_scale_bytes(n)), dtype=torch.uint8))
     if transpose:
-        o["wq_t"] = torch.empty((*lead, n, d), dtype=torch.float8_e4m3fn, device=W.device)
-        o["sw_t"] = torch.empty((*lead, (n + 127) // 128, fp8_scale_bytes(d)), dtype=torch.uint8, device=W.device)
-    B.intlora_fp8_quant_weight(E, d, n, _FLOAT[W.dtype], W, o["wq"], o["sw"], o.get("wq_t"), o.get("sw_t"))
+        o["wq_t"] = W.new_empty((*lead, n, d), dtype=torch.float8_e4m3fn)
+        o["sw_t"] = W.new_empty((*lead, (n + 127) // 128, fp8_scale_bytes(d)), dtype=torch.uint8)
+    B.intlora_fp8_quant_weight(E, d, n, _FLOAT[W.dtype], w, o["wq"], o["sw"], o.get("wq_t"), o.get("sw_t"))
     return o
 
 
-def _fp8_operands(xq, sx, wq, sw, lead):
+def _fp8_operands(xq, sx, wq, sw, lead, dev):
     M, n = _dims("xq", xq, 2)
-    d = wq.shape[-2]
-    _want("xq", xq, (M, n), torch.float8_e4m3fn)
-    _want("sx", sx, (M, fp8_scale_bytes(n)), torch.uint8)
-    _want("wq", wq, (*lead, d, n), torch.float8_e4m3fn)
-    _want("sw", sw, (*lead, (d + 127) // 128, fp8_scale_bytes(n)), torch.uint8)
-    return M, d, n
-
-
-def _output(out, shape, dtype, device):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _want("out", out, shape, dtype)
+    d, s = wq.shape[-2], fp8_scale_bytes(n)
+    return M, d, n, (_want("xq", xq, (M, n), _E4M3, dev), _want("sx", sx, (M, s), _BYTES, dev),
+                     _want("wq", wq, (*lead, d, n), _E4M3, dev), _want("sw", sw, (*lead, (d + 127) // 128, s), _BYTES, dev))
 
 
 def fp8_linear(xq, sx, wq, sw, out=None):
     """Y [M, d] (bf16) of codes and scales as fp8_quant_act and fp8_quant_weight make them."""
     _dims("wq", wq, 2)
-    M, d, n = _fp8_operands(xq, sx, wq, sw, ())
-    Y = _output(out, (M, d), torch.bfloat16, xq.device)
-    B.intlora_fp8_linear_fwd(M, d, n, xq, sx, wq, sw, Y)
+    dev = torch.cuda.current_device()
+    M, d, n, p = _fp8_operands(xq, sx, wq, sw, (), dev)
+    Y, y = _output(out, (M, d), torch.bfloat16, xq, dev)
+    B.intlora_fp8_linear_fwd(M, d, n, *p, y)
     return Y
 
 
@@ -348,9 +351,10 @@ def fp8_grouped_linear(xq, sx, offsets, wq, sw, out=None):
     """As fp8_linear with one weight per group of rows: wq [E, d, n], rows offsets[e] ..
     offsets[e + 1] - 1 take weight e.  Rows in no group are left as they are in `out`."""
     E = _dims("wq", wq, 3)[0]
-    M, d, n = _fp8_operands(xq, sx, wq, sw, (E,))
-    Y = _output(out, (M, d), torch.bfloat16, xq.device)
-    B.intlora_fp8_grouped_linear_fwd(M, E, d, n, xq, sx, _offsets(offsets, E), wq, sw, Y)
+    dev = torch.cuda.current_device()
+    M, d, n, (x, s, w, v) = _fp8_operands(xq, sx, wq, sw, (E,), dev)
+    Y, y = _output(out, (M, d), torch.bfloat16, xq, dev)
+    B.intlora_fp8_grouped_linear_fwd(M, E, d, n, x, s, _offsets(offsets, E, dev), w, v, y)
     return Y
 
 
@@ -359,10 +363,10 @@ def grouped_linear(X, offsets, W, out=None):
     are multiplied by W[e]^T.  Rows in no group are left as they are in `out`."""
     M, n = _dims("X", X, 2)
     E, d, _ = _dims("W", W, 3)
-    _want("X", X, (M, n), torch.bfloat16, torch.float16)
-    _want("W", W, (E, d, n), X.dtype)
-    Y = _output(out, (M, d), X.dtype, X.device)
-    B.intlora_grouped_linear_fwd(M, E, d, n, _FLOAT[X.dtype], X, _offsets(offsets, E), W, Y)
+    dev = torch.cuda.current_device()
+    x, w = _want("X", X, (M, n), _HALF, dev), _want("W", W, (E, d, n), (X.dtype,), dev)
+    Y, y = _output(out, (M, d), X.dtype, X, dev)
+    B.intlora_grouped_linear_fwd(M, E, d, n, _FLOAT[X.dtype], x, _offsets(offsets, E, dev), w, y)
     return Y
 
 
@@ -370,10 +374,10 @@ def grouped_linear_dx(dY, offsets, W, out=None):
     """The gradient of grouped_linear's X: dX [M, n] of dY [M, d] and W [E, d, n]."""
     M, d = _dims("dY", dY, 2)
     E, _, n = _dims("W", W, 3)
-    _want("dY", dY, (M, d), torch.bfloat16, torch.float16)
-    _want("W", W, (E, d, n), dY.dtype)
-    dX = _output(out, (M, n), dY.dtype, dY.device)
-    B.intlora_grouped_linear_dx(M, E, d, n, _FLOAT[dY.dtype], dY, _offsets(offsets, E), W, dX)
+    dev = torch.cuda.current_device()
+    y, w = _want("dY", dY, (M, d), _HALF, dev), _want("W", W, (E, d, n), (dY.dtype,), dev)
+    dX, x = _output(out, (M, n), dY.dtype, dY, dev)
+    B.intlora_grouped_linear_dx(M, E, d, n, _FLOAT[dY.dtype], y, _offsets(offsets, E, dev), w, x)
     return dX
 
 
@@ -383,63 +387,82 @@ def grouped_linear_dw(dY, X, offsets, dtype=None, out=None):
     form is the G of ste_backward."""
     M, d = _dims("dY", dY, 2)
     n = _dims("X", X, 2)[1]
-    _want("dY", dY, (M, d), torch.bfloat16, torch.float16)
-    _want("X", X, (M, n), dY.dtype)
+    dev = torch.cuda.current_device()
+    y, x = _want("dY", dY, (M, d), _HALF, dev), _want("X", X, (M, n), (dY.dtype,), dev)
     E = 1 if offsets is None else offsets.numel() - 1
     dtype = dtype or (dY.dtype if out is None else out.dtype)
     if dtype not in (dY.dtype, torch.float32):
         raise ValueError(f"dtype: expected {dY.dtype} or torch.float32, got {dtype}")
-    dW = _output(out, (E, d, n), dtype, dY.device)
-    B.intlora_grouped_linear_dw(M, E, d, n, _FLOAT[dY.dtype], _FLOAT[dtype], dY, X, _offsets(offsets, E), dW)
+    dW, w = _output(out, (E, d, n), dtype, dY, dev)
+    B.intlora_grouped_linear_dw(M, E, d, n, _FLOAT[dY.dtype], _FLOAT[dtype], y, x, _offsets(offsets, E, dev), w)
     return dW
 
 
 # ---------------------------------------------------------------- gradient norm, clipping
+# (lists of hundreds of tensors: the checks go over the whole list at a time)
+def _host(ctype, code, values):
+    """A C array of the values (array.array converts them in half of ctypes' time)."""
+    a = array.array(code, values)
+    return (ctype * len(a)).from_buffer(a) if a else (ctype * 0)()
+
+
 def _pointers(name, ts, dev):
-    for t in ts:
-        if t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"{name}: expected contiguous tensors on the current device")
-    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+    if ts and (set(map(torch.Tensor.get_device, ts)) != {dev} or not all(map(torch.Tensor.is_contiguous, ts))):
+        raise ValueError(f"{name}: expected contiguous tensors on the current device")
+    return _host(ctypes.c_void_p, "Q", map(torch.Tensor.data_ptr, ts))
+
+
+_dtype = operator.attrgetter("dtype")
+
+
+def _types(name, ts):
+    try:
+        return _host(ctypes.c_int32, "i", map(_FLOAT.__getitem__, map(_dtype, ts)))
+    except KeyError as e:
+        raise ValueError(f"{name}: expected bf16, fp16 or fp32 tensors, got {e.args[0]}") from None
+
+
+def _numels(ts):
+    return _host(ctypes.c_int64, "q", map(torch.Tensor.numel, ts))
+
+
+def _sumsq(ptrs, numel, types, dev):
+    ws = torch.empty(8 + B.intlora_grad_ws_bytes(numel) // 8, dtype=torch.float64, device=dev)  # the sum, then the parts
+    sumsq = ws[:1]
+    B.intlora_grad_sumsq(ptrs, numel, types, sumsq, ws[8:])
+    return sumsq
+
+
+def _clip(ptrs, numel, types, grads, sumsq, max_norm, out, dev):
+    outs = ptrs
+    if out is not None:
+        outs = _pointers("out", out, dev)
+        if len(out) != len(grads) or list(map(_dtype, out)) != list(map(_dtype, grads)) or \
+                bytes(_numels(out)) != bytes(numel):
+            raise ValueError("out: expected tensors of the gradients' sizes and types")
+    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    B.intlora_grad_clip(ptrs, outs, numel, types, sumsq, max_norm, norm)
+    return norm
 
 
 def clip_grad_norm(grads, max_norm, out=None):
     """Scales a list of gradients (bf16, fp16, fp32) by min(1, max_norm / (norm + 1e-6)), norm
-    being the 2-norm over all of them, in place or into `out` (tensors of the same shapes and
+    being the 2-norm over all of them, in place or into `out` (tensors of the same sizes and
     types), and returns the norm as a device tensor [1] (fp32); nothing waits for the GPU.
     Ranks that each hold a part call grad_sumsq, add their sums and call grad_clip."""
-    return grad_clip(grads, grad_sumsq(grads), max_norm, out)
-
-
-def _grad_arrays(grads, dev):
-    try:
-        types = [_FLOAT[t.dtype] for t in grads]
-    except KeyError as e:
-        raise ValueError(f"grads: expected bf16, fp16 or fp32 tensors, got {e.args[0]}") from None
-    k = len(grads)
-    return _pointers("grads", grads, dev), (ctypes.c_int64 * k)(*[t.numel() for t in grads]), (ctypes.c_int32 * k)(*types)
+    dev = torch.cuda.current_device()
+    a = _pointers("grads", grads, dev), _numels(grads), _types("grads", grads)
+    return _clip(*a, grads, _sumsq(*a, dev), max_norm, out, dev)
 
 
 def grad_sumsq(grads):
     """The sum of all squared gradients, a device tensor [1] (fp64)."""
     dev = torch.cuda.current_device()
-    ptrs, numel, types = _grad_arrays(grads, dev)
-    sumsq = torch.empty(2, dtype=torch.float64, device=dev)[:1]
-    ws = torch.empty(B.intlora_grad_ws_bytes(numel), dtype=torch.uint8, device=dev)
-    B.intlora_grad_sumsq(ptrs, numel, types, sumsq, ws)
-    return sumsq
+    return _sumsq(_pointers("grads", grads, dev), _numels(grads), _types("grads", grads), dev)
 
 
 def grad_clip(grads, sumsq, max_norm, out=None):
     """The second half of clip_grad_norm, from a sum of squares (fp64 [1]) over all ranks."""
     dev = torch.cuda.current_device()
-    _want("sumsq", sumsq, (1,), torch.float64)
-    ptrs, numel, types = _grad_arrays(grads, dev)
-    if out is None:
-        outs = ptrs
-    else:
-        if [(t.shape, t.dtype) for t in out] != [(t.shape, t.dtype) for t in grads]:
-            raise ValueError("out: expected tensors of the gradients' shapes and types")
-        outs = _pointers("out", out, dev)
-    norm = torch.empty(1, dtype=torch.float32, device=dev)
-    B.intlora_grad_clip(ptrs, outs, numel, types, sumsq, max_norm, norm)
-    return norm
+    _want("sumsq", sumsq, (1,), (torch.float64,), dev)
+    return _clip(_pointers("grads", grads, dev), _numels(grads), _types("grads", grads), grads, sumsq, max_norm, out, dev)
