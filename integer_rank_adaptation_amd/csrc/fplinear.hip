@@ -145,6 +145,29 @@ struct Groups {
     chunk();
     return true;
   }
+  // At most 64 groups, the ones of most rows first: at[] = their numbers, first rows, rows.
+  __device__ __forceinline__ void sort() {
+    if (offsets == nullptr) {
+      at[0] = at[64] = 0;
+      at[128] = T;
+      __builtin_amdgcn_wave_barrier();
+      return;
+    }
+    first();
+    const int lane = threadIdx.x & 63;
+    const int row0 = at[lane], rows = at[64 + lane];
+    int rank = 0;
+    for (int j = 0; j < E; ++j) {
+      const int o = __builtin_amdgcn_readlane(rows, j);
+      rank += o > rows || (o == rows && j < lane);
+    }
+    if (lane < E) {
+      at[rank] = lane;
+      at[64 + rank] = row0;
+      at[128 + rank] = rows;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
   // Number of units; leaves the last chunk in place.
   __device__ __forceinline__ int total() {
     if (offsets == nullptr) return units(T);
@@ -210,8 +233,9 @@ struct Tile {
   static constexpr int BK = 128 / EB;          // elements per stage
   static constexpr int WAVES_N = BN / WN, WAVES = BM / WM * WAVES_N, THREADS = 64 * WAVES;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
-  // 8-bit: the scale dwords of a stage, 64 per wave: BM rows', then the weight blocks'
-  static constexpr int STAGE = A_BYTES + B_BYTES + (F8 ? 256 * WAVES : 0);
+  // 8-bit: the scale dwords of a stage, BM rows', then the weight blocks' (64 per load; the
+  // waves past the rows' all bring the latter)
+  static constexpr int STAGE = A_BYTES + B_BYTES + (F8 ? 4 * BM + 256 : 0);
   static constexpr int AL = A_BYTES / 1024 / WAVES, BL = B_BYTES / 1024 / WAVES;  // direct loads per wave and stage
   static constexpr int AX = AL + (F8 ? 1 : 0), LOADS = AX + BL;  // with the scales' load
   static constexpr int MT = WM / 32, NT = WN / 32;
@@ -241,7 +265,7 @@ struct Operand {
   // TR: the 4 rows x 64 bytes of 32 lanes on different banks (rows of 128 bytes: 2 rows cover all)
   static __device__ __forceinline__ int swz(int k) { return C == 64 ? 2 * (k & 2) : 4 * (k & 3); }
   // This lane's place in a load: byte offset of its row, and of its chunk in the row for even
-  // loads; the swizzle flips bit 6 of the latter for odd ones (C = 128 columns: not).
+  // loads; the swizzle flips a bit of the latter for odd ones (TR = 1: where a load is 2 rows).
   static __device__ __forceinline__ uint32_t row(int lane, uint32_t ld) { return (uint32_t)(lane / PER) * ld; }
   static __device__ __forceinline__ int chunk(int lane) {
     const int r = lane / PER;
@@ -249,8 +273,7 @@ struct Operand {
   }
   static __device__ __forceinline__ int flip(int q) { return (q & 1) == 0 || (TR && ROWS != 2) ? 0 : TR ? 128 : 64; }
   // LDS offset of this lane's first fragment of the 32-row tiles from r0 (a multiple of 32 x
-  // their number);
-  // lane half h takes the contraction chunk 4 sub + 2 h + ks of a stage
+  // their number); lane half h takes the contraction chunk 4 sub + 2 h + ks of a stage.
   static __device__ __forceinline__ uint32_t frag(int lane, int r0) {
     const int h = lane >> 5, r = lane & 31;
     if (!TR) return (uint32_t)((r0 + r) * 128 + (((2 * h) ^ ((r >> 1) & 7)) << 4));
@@ -358,6 +381,10 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
   gr.most = p.most;
   gr.done = 0;
   const int total = LAY == L_TN ? p.E * units_m * units_n : gr.total();
+  // dW: a tile costs its group's rows, so the tiles of the largest groups come first and every
+  // other round goes through the blocks backwards, which evens their loads out
+  const bool sorted = LAY == L_TN && (BIG || cut) && p.E <= 64;
+  if (sorted) gr.sort();
   const int whole = BIG || cut ? whole_rounds(total, p.cus) : 0;
   constexpr int PER_M = kBig / BM, PER = PER_M * (kBig / BN);
   const int list = BIG ? whole : cut ? (total - whole) * PER : total;
@@ -381,7 +408,11 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
     if (LAY == L_TN) {
       const int e = unit / (units_m * units_n);
       unit -= e * units_m * units_n;
-      w.g = group_rows(p.offsets, e, p.T);
+      if (sorted)
+        w.g = Group{__builtin_amdgcn_readfirstlane(gr.at[e]), __builtin_amdgcn_readfirstlane(gr.at[64 + e]),
+                    __builtin_amdgcn_readfirstlane(gr.at[128 + e])};
+      else
+        w.g = group_rows(p.offsets, e, p.T);
       tiles_m = units_m;
     } else {
       w.g = gr.find(unit, unit);
@@ -492,7 +523,7 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
     if (q < C::AL)
       direct_load16(dsa, S + (wid * C::AL + q) * 1024, va[q & 1] + q * OA::ROWS * lda);
     else
-      direct_load4(dss, S + C::A_BYTES + C::B_BYTES + wid * 256, so);
+      direct_load4(dss, S + C::A_BYTES + C::B_BYTES + (wid < BM / 64 ? wid : BM / 64) * 256, so);
   };
 
   // Fragments of one sub-step in registers.  Two sets alternate: while the matrix cores work
@@ -538,11 +569,13 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;  // LDS address of the buffers
   const int step = gridDim.x;
-  int at = xcd_slot(blockIdx.x, step);
+  const int slot = xcd_slot(blockIdx.x, step);
+  auto tile_of = [&](int round) { return round * step + (sorted && (round & 1) ? step - 1 - slot : slot); };
+  int round = 0;
   Work cur, nxt;
-  locate(at, cur);
-  if (BIG ? at >= list : !cur.live) return;  // (small tiles: one per block)
-  locate(at + step, nxt);
+  locate(tile_of(0), cur);
+  if (BIG ? tile_of(0) >= list : !cur.live) return;  // (small tiles: one per block)
+  locate(tile_of(1), nxt);
   begin_tile(cur);
 #pragma unroll
   for (int s = 0; s < C::ST; ++s) {
@@ -680,10 +713,10 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
         }
       }
     }
-    at += step;
-    if (at >= list) break;
+    ++round;
+    if (tile_of(round) >= list) break;
     cur = nxt;
-    locate(at + step, nxt);
+    locate(tile_of(round + 1), nxt);
   }
   wait_loads<0>();  // the stages loaded past the last tile (zeros)
 }
@@ -1012,10 +1045,12 @@ hipError_t run_gemm(GemmArgs a, hipStream_t st) {
   const hipError_t e =
       launch_gemm<Tile<TY, LAY, kBig, kBig, 64, 128, 2>, TO>(a, units < a.cus ? units : a.cus, st);
   if (e != hipSuccess) return e;
-  // what is left over: less than a round
+  // what is left over: less than kTailShare of a round
   const bool sure = LAY == L_TN || a.offsets == nullptr;
-  if (sure && (units % a.cus == 0 || units % a.cus * 256 >= (int64_t)kTailShare * a.cus)) return hipSuccess;
-  return launch_gemm<Small4, TO>(a, 4 * (sure ? units % a.cus : (units < a.cus ? units : a.cus)), st);
+  int64_t rest = ((int64_t)kTailShare * a.cus - 1) / 256;
+  if (units < rest) rest = units;
+  if (sure) rest = units % a.cus <= rest ? units % a.cus : 0;
+  return rest == 0 ? hipSuccess : launch_gemm<Small2, TO>(a, 4 * rest, st);
 }
 
 // ------------------------------------------------------------------------ quantizers

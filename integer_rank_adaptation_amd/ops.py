@@ -417,6 +417,9 @@ _dtype = operator.attrgetter("dtype")
 
 def _types(name, ts):
     try:
+        one = set(map(_dtype, ts))
+        if len(one) == 1:
+            return _host(ctypes.c_int32, "i", [_FLOAT[one.pop()]] * len(ts))
         return _host(ctypes.c_int32, "i", map(_FLOAT.__getitem__, map(_dtype, ts)))
     except KeyError as e:
         raise ValueError(f"{name}: expected bf16, fp16 or fp32 tensors, got {e.args[0]}") from None
@@ -437,8 +440,7 @@ def _clip(ptrs, numel, types, grads, sumsq, max_norm, out, dev):
     outs = ptrs
     if out is not None:
         outs = _pointers("out", out, dev)
-        if len(out) != len(grads) or list(map(_dtype, out)) != list(map(_dtype, grads)) or \
-                bytes(_numels(out)) != bytes(numel):
+        if len(out) != len(grads) or bytes(_types("out", out)) != bytes(types) or bytes(_numels(out)) != bytes(numel):
             raise ValueError("out: expected tensors of the gradients' sizes and types")
     norm = torch.empty(1, dtype=torch.float32, device=dev)
     B.intlora_grad_clip(ptrs, outs, numel, types, sumsq, max_norm, norm)

@@ -5,6 +5,14 @@ binary32 is within (K + 16) 2^-23 sum |a| |b| of the exact one (the bound for an
 summation with at most K + 16 roundings, each by at most one unit of 2^-23, which covers
 truncation), and the final rounding to t adds finfo(t).eps / 2 of the value, or half the
 smallest subnormal of t.
+
+The block-scaled 8-bit matrix instruction adds its products eight at a time (k = 8 j .. 8 j + 7
+here) on a common grid: with E the largest sum of two operands' exponents among the eight, the
+grid is 2^(E - 13), and only from there on sums have 24 bits (test_fp8_group_alignment pins
+this).  The largest product is at least 2^E and, with 8 significand bits, on the grid itself;
+the seven others are moved by at most one grid step each.  So a group is off by at most
+7 x 2^(E - 13) <= 7 x 2^-13 max |a b| over the group, and 8-bit products have the sum of that
+over their groups besides.
 """
 import numpy as np
 import pytest
@@ -43,11 +51,25 @@ def codes_of(t):
     return t.cpu().view(torch.uint8).numpy()
 
 
-def check(got, want, mag, k, what=""):
+def aligned(x, w):
+    """7 x 2^-13 of the largest product of each group of eight, summed: x [M, n], w [d, n]."""
+    x, w = np.abs(x).astype(np.float32), np.abs(w).astype(np.float32)
+    n = -(-x.shape[1] // 8) * 8
+    x, w = (np.pad(a, ((0, 0), (0, n - a.shape[1]))) for a in (x, w))
+    total = np.zeros((x.shape[0], w.shape[0]), np.float32)
+    for j in range(0, n, 8):
+        m = np.outer(x[:, j], w[:, j])
+        for k in range(j + 1, j + 8):
+            np.maximum(m, np.outer(x[:, k], w[:, k]), out=m)
+        total += m
+    return 7 * 2.0**-13 * total.astype(np.float64)
+
+
+def check(got, want, mag, k, what="", extra=0.0):
     """got (tensor) against the exact product `want` with magnitudes `mag`, k terms."""
     t = got.dtype
     tiny = torch.finfo(t).smallest_normal * torch.finfo(t).eps / 2 if t != torch.bfloat16 else 0.0
-    acc = (k + 16) * 2.0**-23 * mag
+    acc = (k + 16) * 2.0**-23 * mag + extra
     tol = acc + (torch.finfo(t).eps / 2) * (np.abs(want) + acc) + tiny
     diff = np.abs(f64(got) - want)
     bad = ~(diff <= tol)
@@ -146,7 +168,36 @@ def test_fp8_linear(ops, M, d, n):
     x = ref.dequantize(codes_of(xq), sx.cpu().numpy(), 1)
     wd = ref.dequantize(codes_of(w["wq"]), w["sw"].cpu().numpy(), 128)
     y, mag = ref.grouped(x, [0, M], wd[None])
-    check(Y, y, mag, n)
+    check(Y, y, mag, n, extra=aligned(x, wd))
+
+
+def test_fp8_group_alignment(ops):
+    """What the 8-bit tolerance rests on: +2^16, -2^16 at k = 0, 1 and one product 2^-t at k = p.
+    In their group of eight a product of 2^3 or more (13 bits below) is kept; in the next group
+    of eight one of 2^-8 or more; in any other all of them."""
+    n = 128
+    lanes = [(p, t) for p in range(2, n) for t in range(-12, 19)]
+    x, w = np.zeros((len(lanes), n), np.float32), np.zeros((len(lanes), n), np.float32)
+    for i, (p, t) in enumerate(lanes):
+        x[i, 0] = w[i, 0] = w[i, 1] = 256.0
+        x[i, 1] = -256.0
+        e = -(t // 2) if t >= 0 else (-t) // 2
+        x[i, p], w[i, p] = 2.0**e, 2.0 ** (-t - e)
+    M = len(lanes)
+    q = lambda a: torch.from_numpy(ref.to_e4m3(a)).cuda().view(torch.float8_e4m3fn)  # noqa: E731
+    one = torch.full((M, 4), 127, dtype=torch.uint8, device="cuda")
+    for rows in (16, 512):  # the few-row kernel, the tiled one
+        for i in range(0, M, rows):
+            m = min(rows, M - i)
+            sw = torch.full(((m + 127) // 128, 4), 127, dtype=torch.uint8, device="cuda")
+            Y = f64(ops.fp8_linear(q(x[i:i + m]), one[:m].contiguous(), q(w[i:i + m]), sw))
+            for r in range(m):
+                p, t = lanes[i + r]
+                kept = t <= -3 if p < 8 else t <= 8 if p < 16 else True
+                if kept:
+                    assert Y[r, r] == 2.0**-t, (rows, p, t, Y[r, r])
+                else:
+                    assert abs(Y[r, r] - 2.0**-t) <= (2.0**3 if p < 8 else 2.0**-8)
 
 
 def test_fp8_linear_scales_spread(ops):
@@ -159,9 +210,10 @@ def test_fp8_linear_scales_spread(ops):
         xq, sx = ops.fp8_quant_act(X[:m].cuda())
         w = ops.fp8_quant_weight(W.cuda())
         Y = ops.fp8_linear(xq, sx, w["wq"], w["sw"])
-        y, mag = ref.grouped(ref.dequantize(codes_of(xq), sx.cpu().numpy(), 1), [0, m],
-                             ref.dequantize(codes_of(w["wq"]), w["sw"].cpu().numpy(), 128)[None])
-        check(Y, y, mag, n)
+        x = ref.dequantize(codes_of(xq), sx.cpu().numpy(), 1)
+        wd = ref.dequantize(codes_of(w["wq"]), w["sw"].cpu().numpy(), 128)
+        y, mag = ref.grouped(x, [0, m], wd[None])
+        check(Y, y, mag, n, extra=aligned(x, wd))
 
 
 def test_fp8_input_gradient(ops):
@@ -176,7 +228,7 @@ def test_fp8_input_gradient(ops):
     wd = ref.dequantize(codes_of(w["wq"]), w["sw"].cpu().numpy(), 128)
     dy = ref.dequantize(codes_of(dq), sd.cpu().numpy(), 1)
     want, mag = ref.grouped(dy, [0, M], wd.T[None])
-    check(dX, want, mag, d)
+    check(dX, want, mag, d, extra=aligned(dy, wd.T))
     x = f64(randn(3, (M, n)))
     f = lambda v: float((dy * (v @ wd.T)).sum())  # noqa: E731
     for i, j in ((0, 0), (M - 1, n - 1), (17, 133)):
@@ -207,7 +259,11 @@ def test_fp8_grouped(ops, rows, d, n):
     x = ref.dequantize(codes_of(xq), sx.cpu().numpy(), 1)
     wd = np.stack([ref.dequantize(codes_of(w["wq"][e]), w["sw"][e].cpu().numpy(), 128) for e in range(E)])
     y, mag = ref.grouped(x, off.tolist(), wd)
-    check(Y[lead:M - tail], y[lead:M - tail], mag[lead:M - tail], n)
+    extra = np.zeros_like(y)
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        extra[r] = aligned(x[r], wd[e])
+    check(Y[lead:M - tail], y[lead:M - tail], mag[lead:M - tail], n, extra=extra[lead:M - tail])
     assert (Y[:lead] == 7).all() and (Y[M - tail:] == 7).all()  # rows of no group stay
 
 
@@ -309,6 +365,205 @@ def test_grouped_gradients_by_differences(ops):
         h[e, i, j] = 0.5
         slope = f(x, w + h) - f(x, w - h)
         assert abs(dW[e, i, j] - slope) <= (M + 16) * 2.0**-22 * magw[e, i, j] + 1e-12
+
+
+# Sizes that reach every way the work is cut up: whole rounds of large tiles, a last round that
+# is not cut, one that is (forward and dX by rows, dW by weights), small tiles alone.
+@pytest.mark.parametrize("rows,d,n", [
+    ([4300], 4096, 64), ([2100, 0, 2300, 41], 4096, 72), ([700, 300, 900, 280], 1536, 40), ([520, 600], 2304, 264),
+    ([20] * 9, 1536, 1280), ([3, 0, 70, 11, 200, 1, 0, 9, 30], 1544, 1288), ([260] * 70, 264, 40),
+])
+def test_grouped_tile_schedules(ops, rows, d, n):
+    M = sum(rows)
+    off = offsets_of(rows)
+    t = torch.bfloat16
+    X, W, dY = randn(M, (M, n), 1.0, t), randn(d, (len(rows), d, n), 0.05, t), randn(n, (M, d), 0.1, t)
+    x, w, dy = X.double().numpy(), W.double().numpy(), dY.double().numpy()
+    Xd, Wd, dYd, offd = X.cuda(), W.cuda(), dY.cuda(), off.cuda()
+    y, mag = ref.grouped(x, off.tolist(), w)
+    check(ops.grouped_linear(Xd, offd, Wd), y, mag, n, "forward")
+    dx, mag = ref.grouped(dy, off.tolist(), w.transpose(0, 2, 1))
+    check(ops.grouped_linear_dx(dYd, offd, Wd), dx, mag, d, "dX")
+    # wide inputs the other way round, so that dX has many columns
+    y, mag = ref.grouped(dy, off.tolist(), w.transpose(0, 2, 1).copy())
+    check(ops.grouped_linear(dYd, offd, Wd.transpose(1, 2).contiguous()), y, mag, d, "forward of W^T")
+    dx, mag = ref.grouped(x, off.tolist(), w)
+    check(ops.grouped_linear_dx(Xd, offd, Wd.transpose(1, 2).contiguous()), dx, mag, n, "dX of W^T")
+    dw, mag, _ = ref.grouped_dw(dy, x, off.tolist())
+    check(ops.grouped_linear_dw(dYd, Xd, offd, dtype=torch.float32), dw, mag, max(rows), "dW")
+
+
+@pytest.mark.parametrize("M,d,n", [(4300, 4096, 64), (2100, 2304, 400), (1200, 1283, 272)])
+def test_fp8_tile_schedules(ops, M, d, n):
+    X, W = randn(M, (M, n)), randn(d, (d, n), 0.02)
+    xq, sx = ops.fp8_quant_act(X.cuda())
+    w = ops.fp8_quant_weight(W.cuda())
+    x = ref.dequantize(codes_of(xq), sx.cpu().numpy(), 1)
+    wd = ref.dequantize(codes_of(w["wq"]), w["sw"].cpu().numpy(), 128)
+    y, mag = ref.grouped(x, [0, M], wd[None])
+    check(ops.fp8_linear(xq, sx, w["wq"], w["sw"]), y, mag, n, extra=aligned(x, wd))
+
+
+# --------------------------------------------------------------------------- far offsets
+def test_weights_past_32_bits(ops):
+    """The last of 70 experts lies past 4 GiB; few rows and tiled kernel, 8 bits."""
+    E, d, n = 70, 8192, 8192
+    wq = torch.zeros((E, d, n), dtype=torch.uint8, device="cuda")
+    sw = torch.full((E, d // 128, ops.fp8_scale_bytes(n)), 127, dtype=torch.uint8, device="cuda")
+    last = ops.fp8_quant_weight(randn(1, (d, n), 0.02).cuda())
+    wq[-1], sw[-1] = last["wq"].view(torch.uint8), last["sw"]
+    wd = ref.dequantize(codes_of(last["wq"])[-64:], last["sw"].cpu().numpy()[-1:].repeat(64, 0), 1)
+    for M in (3, 300):
+        xq, sx = ops.fp8_quant_act(randn(M, (M, n)).cuda())
+        off = torch.zeros(E + 1, dtype=torch.int64)
+        off[-1] = M
+        Y = ops.fp8_grouped_linear(xq, sx, off.cuda(), wq.view(torch.float8_e4m3fn), sw)
+        x = ref.dequantize(codes_of(xq), sx.cpu().numpy(), 1)
+        y, mag = ref.grouped(x, [0, M], wd[None])
+        check(Y[:, -64:], y, mag, n, extra=aligned(x, wd))
+
+
+def test_rows_past_32_bits(ops):
+    """600 k token rows of 8 KB: the last group's rows lie past 4 GiB in X and dY."""
+    M, n, d, tail = 600_000, 4096, 16, 200
+    X = torch.zeros((M, n), dtype=torch.bfloat16, device="cuda")
+    X[-tail:] = randn(1, (tail, n), dtype=torch.bfloat16).cuda()
+    W = randn(2, (2, d, n), 0.05, torch.bfloat16)
+    off = torch.tensor([0, M - tail, M], dtype=torch.int64, device="cuda")
+    Y = ops.grouped_linear(X, off, W.cuda())
+    x, w = f64(X[-tail:]), W.double().numpy()
+    y, mag = ref.grouped(x, [0, tail], w[1:])
+    check(Y[-tail:], y, mag, n)
+    assert (Y[:-tail] == 0).all()
+    # the same rows as dY of a wide layer: dX and dW from them
+    W2 = randn(3, (2, n, d), 0.05, torch.bfloat16)
+    dX = ops.grouped_linear_dx(X, off, W2.cuda())
+    dx, mag = ref.grouped(x, [0, tail], W2.double().numpy()[1:].transpose(0, 2, 1))
+    check(dX[-tail:], dx, mag, n)
+    x2 = randn(4, (M, d), 1.0, torch.bfloat16).cuda()
+    dW = ops.grouped_linear_dw(X, x2, off, dtype=torch.float32)
+    dw, mag, _ = ref.grouped_dw(x, f64(x2[-tail:]), [0, tail])
+    check(dW[1], dw[0], mag[0], tail)
+    assert (dW[0] == 0).all()
+
+
+# --------------------------------------------------------------------------- streams, graphs
+def _step(ops, s):
+    xq, sx = ops.fp8_quant_act(s["X"])
+    y8 = ops.fp8_grouped_linear(xq, sx, s["off"], s["wq"], s["sw"])
+    y = ops.grouped_linear(s["X"], s["off"], s["W"])
+    dx = ops.grouped_linear_dx(s["dY"], s["off"], s["W"])
+    dw = ops.grouped_linear_dw(s["dY"], s["X"], s["off"], dtype=torch.float32)
+    out = [torch.empty_like(dx), torch.empty_like(dw)]
+    norm = ops.clip_grad_norm([dx, dw], 0.5, out=out)
+    return [y8, y, dx, dw, norm, *out]
+
+
+def _state(ops, seed, rows, d=520, n=400):
+    M, E = sum(rows), len(rows)
+    W = randn(seed, (E, d, n), 0.05, torch.bfloat16).cuda()
+    q = ops.fp8_quant_weight(W)
+    return dict(X=randn(seed + 1, (M, n), 1.0, torch.bfloat16).cuda(), dY=randn(seed + 2, (M, d), 0.1, torch.bfloat16).cuda(),
+                off=offsets_of(rows).cuda(), W=W, wq=q["wq"], sw=q["sw"])
+
+
+def test_repeated_calls_are_bit_identical(ops):
+    s = _state(ops, 1, [100, 0, 300, 17])
+    a = [t.clone() for t in _step(ops, s)]
+    for _ in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(a, _step(ops, s)))
+
+
+def test_two_streams_at_once(ops):
+    states = [_state(ops, 10, [200, 3, 150]), _state(ops, 20, [64, 400, 1, 0, 9])]
+    want = [[t.clone() for t in _step(ops, s)] for s in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    got = [None, None]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = _step(ops, states[i])
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, g))
+
+
+def test_graph_replays_with_new_inputs(ops):
+    """A captured step, replayed on other inputs and other group sizes between eager steps."""
+    s = _state(ops, 30, [120, 40, 0, 260])
+    other = _state(ops, 40, [0, 300, 119, 1])
+    _step(ops, s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = _step(ops, s)
+    for source in (other, _state(ops, 50, [420, 0, 0, 0]), _state(ops, 60, [1, 2, 3, 414]), other):
+        for k in s:
+            s[k].copy_(source[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        want = _step(ops, source)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_train_step_of_an_adapter(ops):
+    """The calls as a training step makes them: G = dY^T X (fp32) feeds the straight-through
+    backward, whose dA and dB are clipped together; against binary64 throughout."""
+    from oracle import algebra
+
+    M, d, n, r = 200, 264, 320, 8
+    X, dY = randn(1, (M, n), 1.0, torch.bfloat16), randn(2, (M, d), 0.1, torch.bfloat16)
+    g = rng(3)
+    wr = g.integers(0, 256, (d, n)).astype(np.uint8)
+    z = g.integers(100, 150, d).astype(np.int32)
+    A, Bm = g.standard_normal((d, r)).astype(np.float32), g.standard_normal((r, n)).astype(np.float32)
+    G = ops.grouped_linear_dw(dY.cuda(), X.cuda(), None, dtype=torch.float32)[0]
+    st = dict(wround=torch.from_numpy(wr).cuda(), z=torch.from_numpy(z).cuda())
+    o = ops.ste_backward(st, torch.from_numpy(A).cuda(), torch.from_numpy(Bm).cuda(), G, 8)
+    grads = [o["dA"], o["dB"]]
+    before = [t.clone() for t in grads]
+    norm = ops.clip_grad_norm(grads, 1.0)
+    G64, mag, _ = ref.grouped_dw(dY.double().numpy(), X.double().numpy(), [0, M])
+    dA, dB = algebra.ste_backward(wr, z, A.astype(np.float64), Bm.astype(np.float64), G64[0])[:2]
+    eG = (M + 16) * 2.0**-23 * mag[0]
+    # |error| of dA: G's through |B|, and the product's own
+    tA = eG @ np.abs(Bm.T) + (n + 16) * 2.0**-23 * ((np.abs(G64[0]) + eG) @ np.abs(Bm.T))
+    tB = np.abs(A.T) @ eG + (d + 16) * 2.0**-23 * (np.abs(A.T) @ (np.abs(G64[0]) + eG))
+    assert (np.abs(f64(before[0]) - dA) <= tA).all() and (np.abs(f64(before[1]) - dB) <= tB).all()
+    total = ref.sumsq([f64(t) for t in before])
+    assert abs(float(norm) - total**0.5) <= total**0.5 * 2.0**-23
+    c = float(np.float32(ref.clip_factor(total, 1.0)))
+    for t, b in zip(grads, before):
+        assert (np.abs(f64(t) - f64(b) * c) <= np.abs(f64(b) * c) * 2.0**-22).all()
+
+
+def test_tensor_calls_refuse(ops):
+    X = torch.zeros(8, 64, device="cuda", dtype=torch.bfloat16)
+    W = torch.zeros(2, 16, 64, device="cuda", dtype=torch.bfloat16)
+    off = torch.tensor([0, 4, 8], device="cuda")
+    bad = [
+        lambda: ops.grouped_linear(X, None, W), lambda: ops.grouped_linear(X, off.int(), W),
+        lambda: ops.grouped_linear(X, off[:2], W), lambda: ops.grouped_linear(X, off.cpu(), W),
+        lambda: ops.grouped_linear(X.half(), off, W), lambda: ops.grouped_linear(X.float(), off, W.float()),
+        lambda: ops.grouped_linear(X.t(), off, W), lambda: ops.grouped_linear(X[:, :32], off, W),
+        lambda: ops.grouped_linear(X, off, W, out=torch.zeros(8, 16, device="cuda")),
+        lambda: ops.grouped_linear(X, off, W, out=torch.zeros(8, 17, device="cuda", dtype=torch.bfloat16)),
+        lambda: ops.grouped_linear_dw(X, X, off, dtype=torch.float16), lambda: ops.grouped_linear_dw(X, X[:4], off),
+        lambda: ops.fp8_quant_act(X.int()), lambda: ops.fp8_quant_act(X, out=(X, X)),
+        lambda: ops.fp8_linear(X, off, W[0], off), lambda: ops.clip_grad_norm([X.int()], 1.0),
+        lambda: ops.clip_grad_norm([X], 1.0, out=[X[:4]]), lambda: ops.clip_grad_norm([X, W], 1.0, out=[X]),
+        lambda: ops.clip_grad_norm([X.t()], 1.0), lambda: ops.clip_grad_norm([X.cpu()], 1.0),
+        lambda: ops.clip_grad_norm([X], -1.0), lambda: ops.clip_grad_norm([X, X], 1.0),
+        lambda: ops.grouped_linear(X[:, 1:9].contiguous()[:, :7], off, W),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, RuntimeError)):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    torch.cuda.synchronize()
 
 
 # --------------------------------------------------------------------------- clipping
