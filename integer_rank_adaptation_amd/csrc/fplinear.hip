@@ -19,6 +19,7 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef short v4s __attribute__((ext_vector_type(4)));
+typedef uint32_t u4i __attribute__((ext_vector_type(4)));
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f2 __attribute__((ext_vector_type(2)));
@@ -84,6 +85,18 @@ template <int N>
 __device__ __forceinline__ void wait_loads() {
   static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+
+// At most N loads in flight, or N + MORE where `more` is not 0.  In one piece: a branch of the
+// compiler's would cut the stage loop into blocks, and it would then move matrix instructions
+// past the wait and spill.
+template <int N, int MORE>
+__device__ __forceinline__ void wait_vm_more(int more) {
+  static_assert(N >= 0 && N + MORE < 64, "vmcnt is 6 bits");
+  __asm__ volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lmore%=\n\ts_waitcnt vmcnt(%1)\n.Lmore%=:\n\ts_waitcnt vmcnt(%2)"
+                   :
+                   : "s"(__builtin_amdgcn_readfirstlane(more)), "n"(N), "n"(N + MORE)
+                   : "memory", "scc");
 }
 
 __device__ __forceinline__ int clamp_row(int64_t o, int T) { return o < 0 ? 0 : (o > T ? T : (int)o); }
@@ -595,6 +608,9 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
   for (int q = 0; q < C::READS; ++q) read(q, fa, fb, 0, f0);
   if (C::F8) read_scales(0, 0, sc);
 
+  const bool aligned = (int64_t)p.cols * (TO == T_FP32 ? 4 : 2) % 16 == 0;
+  constexpr int STORES = (TO == T_FP32 ? 4 : 2) * C::MT * C::NT;
+  int fresh = 0;  // the last tile's STORES stores may be in flight, newer than this tile's first two stages
   // The stages of a block's consecutive tiles are one stream: the first stages of the next
   // tile are loaded during the last ones of this tile, and while its epilogue runs.
   for (;;) {
@@ -622,9 +638,12 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
       // kt + ST, and the next stage's second operand has landed for all waves; behind the one
       // half a sub-step later the first operand has.  So the loads never run dry: half a stage
       // is in flight at either barrier (with one barrier for both operands the loads alone
-      // took 1.5 times the matrix cores' time; outputs still being stored are newer than the
-      // loads waited for).
-      wait_loads<C::AX + (C::ST - 2) * C::LOADS>();
+      // took 1.5 times the matrix cores' time).
+      wait_lgkm();
+      if (BIG)
+        wait_vm_more<C::AX + (C::ST - 2) * C::LOADS, BIG ? STORES : 0>(fresh);
+      else
+        wait_vm<C::AX + (C::ST - 2) * C::LOADS>();
       __builtin_amdgcn_s_barrier();
       __asm__ volatile("" ::: "memory");
       if (kt + C::ST == cur.stages) begin_tile(nxt);
@@ -633,7 +652,11 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
 #pragma unroll
       for (int q = 0; q < C::PRODUCTS; ++q) {
         if (q == HALF) {
-          wait_vm<C::BL + (C::ST - 2) * C::LOADS>();
+          if (BIG)
+            wait_vm_more<C::BL + (C::ST - 2) * C::LOADS, BIG ? STORES : 0>(fresh);
+          else
+            wait_vm<C::BL + (C::ST - 2) * C::LOADS>();
+          fresh = 0;
           __builtin_amdgcn_s_barrier();
           __asm__ volatile("" ::: "memory");
           if (C::F8) read_scales(kt + 1 < cur.stages ? kt + 1 : 0, ph, sn);
@@ -657,17 +680,23 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
 
     // ---- epilogue: lane l holds row l % 32 of a tile and columns 8 a + 4 (l / 32) + 0 .. 3 in
     // registers 4 a .. 4 a + 3.  16-bit outputs pass through LDS, one 32 x 32 tile at a time
-    // in a part of the wave's own, so that whole 64-byte row pieces are stored.
+    // in a part of the wave's own, so that whole 64-byte row pieces are stored.  Rows and
+    // columns past the end are stores past the buffer's, so a wave's stores are always STORES
+    // in number and the next tile's first stage need not wait for them.
     if (cur.live) {
       uint8_t* stg = lds + C::EPI + wid * 32 * C::EPI_ROW;
-      const int fr = lane & 31, h = lane >> 5;
+      // (a copy of the lane number that the compiler does not see through: it would compute the
+      // epilogue's addresses before the stage loop, which has no registers for them)
+      int el = lane;
+      __asm__ volatile("" : "+v"(el));
+      const int fr = el & 31, h = el >> 5;
       constexpr int EO = TO == T_FP32 ? 4 : 2;
       const int rows_left = (LAY == L_TN ? p.rows : cur.g.rows) - cur.m0 - wm * C::WM;
       const int64_t out_row = (LAY == L_TN ? (int64_t)cur.g.e * p.rows : (int64_t)cur.g.row0) + cur.m0 + wm * C::WM;
       const int c0 = cur.n0 + wn * C::WN;
       uint8_t* out = static_cast<uint8_t*>(p.C) + (out_row * p.cols + c0) * EO;
       const int64_t ldo = (int64_t)p.cols * EO;
-      const bool aligned = ldo % 16 == 0;
+      const __amdgpu_buffer_rsrc_t ro = make_rsrc(out, C::WM * ldo);
 #pragma unroll
       for (int i = 0; i < C::MT; ++i) {
         const int live = rows_left - 32 * i;
@@ -675,17 +704,16 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
         for (int j = 0; j < C::NT; ++j) {
           __builtin_amdgcn_sched_barrier(0);  // one tile's outputs at a time
           const int cols = p.cols - c0 - 32 * j;
-          uint8_t* o = out + (32 * i) * ldo + 32 * j * EO;
+          const uint32_t o = (uint32_t)((32 * i) * ldo) + 32 * j * EO;
           if (TO == T_FP32) {
-            if (fr < live) {
 #pragma unroll
-              for (int a = 0; a < 4; ++a) {
-                const int c = 8 * a + 4 * h;
-                float* y = reinterpret_cast<float*>(o + fr * ldo) + c;
-                if (c + 4 <= cols)  // columns are a multiple of 8 here: whole groups of four
-                  *reinterpret_cast<float4*>(y) = make_float4(acc[i][j][4 * a], acc[i][j][4 * a + 1],
-                                                              acc[i][j][4 * a + 2], acc[i][j][4 * a + 3]);
-              }
+            for (int a = 0; a < 4; ++a) {
+              const int c = 8 * a + 4 * h;
+              const float4 y = make_float4(acc[i][j][4 * a], acc[i][j][4 * a + 1], acc[i][j][4 * a + 2],
+                                           acc[i][j][4 * a + 3]);
+              // columns are a multiple of 8 here: whole groups of four
+              __builtin_amdgcn_raw_buffer_store_b128(
+                  __builtin_bit_cast(u4i, y), ro, fr < live && c < cols ? o + (uint32_t)(fr * ldo) + 4 * c : kOOB, 0, 0);
             }
           } else {
 #pragma unroll
@@ -697,15 +725,16 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
             if (aligned) {  // columns are a multiple of 8: whole 16-byte pieces
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                const int r = 16 * q + (lane >> 2), c = lane & 3;
-                const v4i v = *reinterpret_cast<const v4i*>(stg + r * C::EPI_ROW + 16 * c);
-                if (r < live && 8 * c < cols) *reinterpret_cast<v4i*>(o + r * ldo + 16 * c) = v;
+                const int r = 16 * q + (el >> 2), c = el & 3;
+                const u4i v = *reinterpret_cast<const u4i*>(stg + r * C::EPI_ROW + 16 * c);
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    v, ro, r < live && 8 * c < cols ? o + (uint32_t)(r * ldo) + 16 * c : kOOB, 0, 0);
               }
             } else {
 #pragma unroll 4
               for (int r = h; r < 32; r += 2) {
                 const uint16_t v = *reinterpret_cast<const uint16_t*>(stg + r * C::EPI_ROW + 2 * fr);
-                if (r < live && fr < cols) reinterpret_cast<uint16_t*>(o + r * ldo)[fr] = v;
+                if (r < live && fr < cols) reinterpret_cast<uint16_t*>(out + o + r * ldo)[fr] = v;
               }
             }
             __builtin_amdgcn_wave_barrier();
@@ -713,6 +742,7 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
         }
       }
     }
+    fresh = aligned && cur.live ? 1 : 0;
     ++round;
     if (tile_of(round) >= list) break;
     cur = nxt;
