@@ -94,7 +94,8 @@ enum {
 };
 
 /* Floating-point element types of the 8-bit floating-point and grouped layers and of the
- * gradient calls below. */
+ * gradient calls below.  An output of these calls that overlaps another of their tensors is
+ * refused (INTLORA_EINVAL), save for gradients that are clipped in place. */
 enum { INTLORA_BF16 = 0, INTLORA_FP16 = 1, INTLORA_FP32 = 2 };
 
 /* One pretrained layer.  r is the LoRA rank (1..128); w_bits the base code width
@@ -432,8 +433,8 @@ int intlora_grouped_linear_dw(int64_t M, int64_t E, int64_t d, int64_t n, int dt
  *   parts of the gradients add their sums before the second call.)
  *   out_i = RN(g c), c = RN32(min(1, max_norm / (sqrt(sumsq) + 1e-6))) -- a NaN sum gives NaN
  *   outputs and an infinite one zeros (NaN for infinite gradients); norm_out[0] =
- *   RN32(sqrt(sumsq)), or NULL.  out_i may be grads_i (in place); outputs must not otherwise
- *   overlap inputs or each other: INTLORA_EINVAL.  max_norm >= 0.
+ *   RN32(sqrt(sumsq)), or NULL.  out_i may be grads_i (in place); outputs and norm_out must not
+ *   otherwise overlap inputs, sumsq or each other: INTLORA_EINVAL.  max_norm >= 0.
  * Workspace of the sum: intlora_grad_ws_bytes (8 bytes per 16384 elements or part). */
 size_t intlora_grad_ws_bytes(int64_t count, const int64_t* numel);
 int intlora_grad_sumsq(int64_t count, const void* const* grads, const int64_t* numel, const int32_t* dtype,

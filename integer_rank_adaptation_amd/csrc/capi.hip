@@ -289,6 +289,27 @@ int check_offsets(int64_t E, const int64_t* offsets, const char* what) {
   return check_opt(offsets, "offsets");
 }
 
+// Bytes of one tensor of a call (NULL: an optional one that is left out).
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+
+// No output overlaps an input or another output: blocks would read what others have written.
+int check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins, const char* what) {
+  const auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+  };
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    bool bad = false;
+    for (const Span& i : ins) bad = bad || meet(*o, i);
+    for (const Span* q = outs.begin(); q != o; ++q) bad = bad || meet(*o, *q);
+    if (bad) return fail(INTLORA_EINVAL, "%s: an output overlaps another tensor of the call", what);
+  }
+  return INTLORA_OK;
+}
+
 int check_grouped(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype, const int64_t* offsets,
                   const char* what) {
   int s = check_dtype(dtype, false, what);
@@ -307,6 +328,11 @@ int run_grouped(const char* what, int direction, int64_t M, int64_t E, int64_t d
   int s = M == 0 ? INTLORA_OK : check_ptrs({tokens, other}, what);
   if (s) return s;
   if ((s = check_ptrs({out}, what))) return s;
+  const int64_t w = 2 * E * d * n, x = 2 * M * n, y = 2 * M * d;  // bytes; tokens, other, out:
+  const bool dw = direction == intlora::kGroupedDw, dx = direction == intlora::kGroupedDx;
+  if ((s = check_apart({{out, dw ? (out_dtype == INTLORA_FP32 ? 2 * w : w) : dx ? x : y}},
+                       {{tokens, dx || dw ? y : x}, {other, dw ? x : w}, {offsets, 8 * (E + 1)}}, what)))
+    return s;
   if ((s = ensure_device())) return s;
   return launch_status(intlora::launch_grouped(direction, M, E, d, n, dtype, out_dtype, tokens, offsets, other, out,
                                                static_cast<hipStream_t>(stream)),
@@ -320,6 +346,12 @@ int fp8_linear(const char* what, int64_t M, int64_t E, int64_t d, int64_t n, con
   if (n % 16 != 0) return fail(INTLORA_ESHAPE, "%s needs n a multiple of 16 (got %lld)", what, (long long)n);
   if (M == 0 || d == 0) return ok();
   if ((s = check_ptrs({xq, sx, wq, sw, Y}, what))) return s;
+  const int64_t row = intlora::fp8_scale_stride(n);
+  if ((s = check_apart({{Y, 2 * M * d}},
+                       {{xq, M * n}, {sx, M * row}, {wq, E * d * n}, {sw, E * ((d + 127) / 128) * row},
+                        {offsets, 8 * (E + 1)}},
+                       what)))
+    return s;
   if ((s = ensure_device())) return s;
   return launch_status(intlora::launch_fp8_linear(M, E, d, n, xq, sx, offsets, wq, sw, Y,
                                                   static_cast<hipStream_t>(stream)),
@@ -346,19 +378,19 @@ int check_grads(int64_t count, const void* const* grads, const int64_t* numel, c
   return INTLORA_OK;
 }
 
-// Outputs present, aligned, and disjoint from every other tensor of the call: otherwise two
-// blocks would write the same element, or one would read what another has scaled.
+// Outputs present, aligned, and disjoint from every other tensor of the call (the sum that
+// every block reads and the norm that one writes among them): otherwise two blocks would write
+// the same element, or one would read what another has scaled.
 int check_clip_outputs(int64_t count, const void* const* grads, void* const* out, const int64_t* numel,
-                       const int32_t* dtype) {
-  if (count == 0) return INTLORA_OK;
-  if (!out) return fail(INTLORA_EINVAL, "grad_clip: NULL host array");
+                       const int32_t* dtype, const double* sumsq, const float* norm_out) {
+  if (count > 0 && !out) return fail(INTLORA_EINVAL, "grad_clip: NULL host array");
   struct Range {
     uintptr_t lo, hi;
     int64_t tensor;
   };
-  std::unique_ptr<Range[]> mem(new (std::nothrow) Range[2 * (size_t)count]);
+  std::unique_ptr<Range[]> mem(new (std::nothrow) Range[2 * ((size_t)count + 1)]);
   if (!mem) return fail(INTLORA_EINVAL, "grad_clip: no host memory for %lld tensors", (long long)count);
-  Range *w = mem.get(), *r = w + count;  // written; read by an output elsewhere
+  Range *w = mem.get(), *r = w + count + 1;  // written; read by an output elsewhere
   int64_t nw = 0, nr = 0;
   bool sw = true, sr = true;  // (lists that were allocated in order need no sort)
   for (int64_t i = 0; i < count; ++i) {
@@ -374,19 +406,27 @@ int check_clip_outputs(int64_t count, const void* const* grads, void* const* out
     sr = sr && (nr == 0 || r[nr - 1].lo <= g);
     r[nr++] = Range{g, g + bytes, i};
   }
+  const auto last = [](Range* a, int64_t& k, bool& sorted, const void* p, size_t bytes) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    sorted = sorted && (k == 0 || a[k - 1].lo <= lo);
+    a[k++] = Range{lo, lo + bytes, -1};
+  };
+  last(r, nr, sr, sumsq, sizeof *sumsq);
+  if (norm_out) last(w, nw, sw, norm_out, sizeof *norm_out);
   const auto before = [](const Range& a, const Range& b) { return a.lo < b.lo; };
   if (!sw) std::sort(w, w + nw, before);
   if (!sr) std::sort(r, r + nr, before);
-  int64_t bad = -1;
-  for (int64_t k = 1; k < nw && bad < 0; ++k)
-    if (w[k].lo < w[k - 1].hi) bad = w[k].tensor;
-  for (int64_t k = 0, j = 0; k < nr && bad < 0; ++k) {  // the outputs do not overlap each other here
+  const Range* bad = nullptr;
+  for (int64_t k = 1; k < nw && !bad; ++k)
+    if (w[k].lo < w[k - 1].hi) bad = &w[k];
+  for (int64_t k = 0, j = 0; k < nr && !bad; ++k) {  // the outputs do not overlap each other here
     while (j < nw && w[j].hi <= r[k].lo) ++j;
-    if (j < nw && w[j].lo < r[k].hi) bad = r[k].tensor;
+    if (j < nw && w[j].lo < r[k].hi) bad = &r[k];
   }
-  if (bad >= 0)
+  if (bad && bad->tensor < 0) return fail(INTLORA_EINVAL, "grad_clip: sumsq or norm_out overlaps another tensor");
+  if (bad)
     return fail(INTLORA_EINVAL, "grad_clip: the output or input of tensor %lld overlaps another output",
-                (long long)bad);
+                (long long)bad->tensor);
   return INTLORA_OK;
 }
 
@@ -779,6 +819,9 @@ int intlora_fp8_quant_act(int64_t M, int64_t n, int dtype, const void* X, uint8_
   if (M * ((n + 127) / 128) >= kMaxDim) return fail(INTLORA_ESHAPE, "fp8_quant_act: too many blocks");
   if (M == 0) return ok();
   if ((s = check_ptrs({X, xq, sx}, "fp8_quant_act"))) return s;
+  if ((s = check_apart({{xq, M * n}, {sx, M * intlora::fp8_scale_stride(n)}},
+                       {{X, M * n * (dtype == INTLORA_FP32 ? 4 : 2)}}, "fp8_quant_act")))
+    return s;
   if ((s = ensure_device())) return s;
   return launch_status(intlora::launch_fp8_quant_act(M, n, dtype, X, xq, sx, static_cast<hipStream_t>(stream)),
                        "fp8_quant_act");
@@ -798,6 +841,13 @@ int intlora_fp8_quant_weight(int64_t E, int64_t d, int64_t n, int dtype, const v
   if (d == 0) return ok();
   if ((s = check_ptrs({W, wq, sw}, "fp8_quant_weight"))) return s;
   if ((s = check_opt(wq_t, "wq_t")) || (s = check_opt(sw_t, "sw_t"))) return s;
+  const int64_t numel = E * d * n;
+  if ((s = check_apart({{wq, numel},
+                        {sw, E * ((d + 127) / 128) * intlora::fp8_scale_stride(n)},
+                        {wq_t, numel},
+                        {sw_t, E * ((n + 127) / 128) * intlora::fp8_scale_stride(d)}},
+                       {{W, numel * (dtype == INTLORA_FP32 ? 4 : 2)}}, "fp8_quant_weight")))
+    return s;
   if ((s = ensure_device())) return s;
   return launch_status(intlora::launch_fp8_quant_weight(E, d, n, dtype, W, wq, sw, wq_t, sw_t,
                                                         static_cast<hipStream_t>(stream)),
@@ -868,7 +918,7 @@ int intlora_grad_clip(int64_t count, const void* const* grads, void* const* out,
   if (s) return s;
   if (!(max_norm >= 0.0)) return fail(INTLORA_EINVAL, "grad_clip: max_norm must be >= 0 (got %g)", max_norm);
   if ((s = check_ptrs({sumsq}, "grad_clip")) || (s = check_opt(norm_out, "norm_out"))) return s;
-  if ((s = check_clip_outputs(count, grads, out, numel, dtype))) return s;
+  if ((s = check_clip_outputs(count, grads, out, numel, dtype, sumsq, norm_out))) return s;
   if ((s = ensure_device())) return s;
   return launch_status(intlora::launch_grad_clip(count, grads, out, numel, dtype, sumsq, max_norm, norm_out,
                                                  static_cast<hipStream_t>(stream)),

@@ -406,6 +406,13 @@ def _host(ctype, code, values):
     return (ctype * len(a)).from_buffer(a) if a else (ctype * 0)()
 
 
+def _tensors(name, ts):
+    """A list of them: an iterator could be gone over only once."""
+    if isinstance(ts, torch.Tensor):
+        raise ValueError(f"{name}: expected a list of tensors")
+    return list(ts)
+
+
 def _pointers(name, ts, dev):
     if ts and (set(map(torch.Tensor.get_device, ts)) != {dev} or not all(map(torch.Tensor.is_contiguous, ts))):
         raise ValueError(f"{name}: expected contiguous tensors on the current device")
@@ -439,6 +446,7 @@ def _sumsq(ptrs, numel, types, dev):
 def _clip(ptrs, numel, types, grads, sumsq, max_norm, out, dev):
     outs = ptrs
     if out is not None:
+        out = _tensors("out", out)
         outs = _pointers("out", out, dev)
         if len(out) != len(grads) or bytes(_types("out", out)) != bytes(types) or bytes(_numels(out)) != bytes(numel):
             raise ValueError("out: expected tensors of the gradients' sizes and types")
@@ -452,19 +460,19 @@ def clip_grad_norm(grads, max_norm, out=None):
     being the 2-norm over all of them, in place or into `out` (tensors of the same sizes and
     types), and returns the norm as a device tensor [1] (fp32); nothing waits for the GPU.
     Ranks that each hold a part call grad_sumsq, add their sums and call grad_clip."""
-    dev = torch.cuda.current_device()
+    dev, grads = torch.cuda.current_device(), _tensors("grads", grads)
     a = _pointers("grads", grads, dev), _numels(grads), _types("grads", grads)
     return _clip(*a, grads, _sumsq(*a, dev), max_norm, out, dev)
 
 
 def grad_sumsq(grads):
     """The sum of all squared gradients, a device tensor [1] (fp64)."""
-    dev = torch.cuda.current_device()
+    dev, grads = torch.cuda.current_device(), _tensors("grads", grads)
     return _sumsq(_pointers("grads", grads, dev), _numels(grads), _types("grads", grads), dev)
 
 
 def grad_clip(grads, sumsq, max_norm, out=None):
     """The second half of clip_grad_norm, from a sum of squares (fp64 [1]) over all ranks."""
-    dev = torch.cuda.current_device()
+    dev, grads = torch.cuda.current_device(), _tensors("grads", grads)
     _want("sumsq", sumsq, (1,), (torch.float64,), dev)
     return _clip(_pointers("grads", grads, dev), _numels(grads), _types("grads", grads), grads, sumsq, max_norm, out, dev)

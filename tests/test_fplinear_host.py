@@ -149,6 +149,43 @@ def test_clip_refusals(lib):
     assert b"overlaps" in lib.intlora_last_error()
 
 
+def test_outputs_may_not_overlap(lib):
+    x, s, w, v, y, off = (0x1000000 * k for k in range(1, 7))
+    M, E, d, n = 8, 2, 32, 64
+    # (one byte of overlap at either end is out of reach: pointers are multiples of 16)
+    for bad in (x, x + M * n - 16, x - 16, s, w + E * d * n - 16, v, off):
+        assert lib.intlora_fp8_grouped_linear_fwd(M, E, d, n, x, s, off, w, v, bad, None) == EINVAL
+    for bad in (x, w + d * n - 16):
+        assert lib.intlora_fp8_linear_fwd(M, d, n, x, s, w, v, bad, None) == EINVAL
+    for f, rows, cols in ((lib.intlora_grouped_linear_fwd, n, d), (lib.intlora_grouped_linear_dx, d, n)):
+        for bad in (x, x + 2 * M * rows - 16, x - 2 * M * cols + 16, w + 2 * E * d * n - 16, off):
+            assert f(M, E, d, n, 0, x, off, w, bad, None) == EINVAL
+    dw = lib.intlora_grouped_linear_dw
+    for bad in (x, w + 2 * M * n - 16, w - 4 * E * d * n + 16):
+        assert dw(M, E, d, n, 0, 2, x, w, off, bad, None) == EINVAL
+    assert b"overlaps" in lib.intlora_last_error()
+    assert lib.intlora_fp8_quant_act(M, n, 0, x, x, s, None) == EINVAL
+    assert lib.intlora_fp8_quant_act(M, n, 0, x, y, x + 2 * M * n - 16, None) == EINVAL
+    assert lib.intlora_fp8_quant_act(M, n, 2, x, y, x + 4 * M * n - 16, None) == EINVAL
+    assert lib.intlora_fp8_quant_act(M, n, 0, x, y, y + 16, None) == EINVAL
+    for wq, sw, wt, st in ((x, s, None, None), (w, x, None, None), (w, s, w, v), (w, s, v, s), (w, s, v, x + 16)):
+        assert lib.intlora_fp8_quant_weight(E, d, n, 0, x, wq, sw, wt, st, None) == EINVAL
+
+
+def test_clip_sum_and_norm_may_not_overlap(lib):
+    def call(sumsq, norm, grads=(0x100000, 0x200000), out=(0x300000, 0x400000)):
+        k, numel = len(grads), (ctypes.c_int64 * 2)(64, 64)
+        g, o, t = (ctypes.c_void_p * k)(*grads), (ctypes.c_void_p * k)(*out), (ctypes.c_int32 * 2)(2, 0)
+        return lib.intlora_grad_clip(k, g, o, numel, t, sumsq, 1.0, norm, None)
+
+    assert call(0x500000, 0x500000) == EINVAL             # the sum itself
+    assert call(0x300000 + 240, 0x500000) == EINVAL       # a sum that a block overwrites
+    assert call(0x500000, 0x400000) == EINVAL             # a norm inside an output
+    assert call(0x500000, 0x200000 + 112) == EINVAL       # ... inside an input
+    assert b"overlaps" in lib.intlora_last_error()
+    assert call(0x100000, 0x600000, out=(0x100000, 0x200000)) == EINVAL  # in place
+
+
 def test_tensor_calls_refuse_host_tensors_and_wrong_types():
     x = torch.zeros(4, 64)
     for call in (lambda: ops.fp8_quant_act(x), lambda: ops.fp8_quant_weight(x), lambda: ops.fp8_quant_act(x[0]),

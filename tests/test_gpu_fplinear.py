@@ -613,3 +613,28 @@ def test_clip_empty_and_nonfinite(ops):
     big = [torch.full((1000,), 1e30, device="cuda")]  # squares beyond binary32
     n = ops.clip_grad_norm(big, 1.0)
     assert abs(float(n) / (1e30 * 1000 ** 0.5) - 1) < 1e-6 and abs(float(big[0][3]) * 1000 ** 0.5 - 1) < 1e-6
+
+
+def test_clip_takes_iterators_and_refuses_a_tensor(ops):
+    """Generators of parameters' gradients are gone over several times inside."""
+    gs = [torch.full((100,), 3.0, device="cuda"), torch.full((25, 3), 4.0, device="cuda", dtype=torch.bfloat16)]
+    want = float(ops.clip_grad_norm([g.clone() for g in gs], 1e9))
+    assert abs(want - (900 + 1200) ** 0.5) < 1e-5
+    out = [torch.zeros_like(g) for g in gs]
+    assert float(ops.clip_grad_norm((g for g in gs), 0.5, out=(o for o in out))) == want
+    assert abs(float(out[0][0]) - 3.0 * 0.5 / want) < 1e-6 and float(gs[0][0]) == 3.0
+    assert float(ops.grad_clip((g for g in gs), ops.grad_sumsq(g for g in gs), 0.5)) == want
+    assert torch.equal(gs[0], out[0]) and torch.equal(gs[1], out[1])
+    for call in (lambda: ops.clip_grad_norm(gs[1], 1.0), lambda: ops.grad_sumsq(gs[1]),
+                 lambda: ops.clip_grad_norm(gs, 1.0, out=gs[1])):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_products_refuse_overlapping_outputs(ops):
+    X = torch.zeros(64, 64, device="cuda", dtype=torch.bfloat16)
+    W = torch.zeros(1, 64, 64, device="cuda", dtype=torch.bfloat16)
+    for call in (lambda: ops.grouped_linear(X, None, W, out=X), lambda: ops.grouped_linear(X, None, W, out=W[0]),
+                 lambda: ops.grouped_linear_dx(X, None, W, out=X), lambda: ops.grouped_linear_dw(X, W[0], None, out=W)):
+        with pytest.raises(RuntimeError, match="overlaps"):
+            call()
