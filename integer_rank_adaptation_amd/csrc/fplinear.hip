@@ -237,14 +237,15 @@ __device__ __forceinline__ int xcd_slot(int b, int n) {
 // A block computes BM x BN outputs at a time, each wave WM x WN of them in tiles of 32 x 32.
 // The contraction goes in stages of 128 bytes of a row (64 16-bit or 128 8-bit elements)
 // through a ring of ST LDS buffers filled by direct loads; a stage is two sub-steps of 64
-// bytes.
-template <int TY_, int LAY_, int BM_, int BN_, int WM_, int WN_, int ST_>
+// bytes.  With KS > 1 the block has KS such sets of waves with a ring each, which take the
+// stages in turn; their sums meet in LDS.
+template <int TY_, int LAY_, int BM_, int BN_, int WM_, int WN_, int ST_, int KS_ = 1>
 struct Tile {
-  static constexpr int TY = TY_, LAY = LAY_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_;
+  static constexpr int TY = TY_, LAY = LAY_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_, KS = KS_;
   static constexpr bool F8 = TY == T_FP8;
   static constexpr int EB = F8 ? 1 : 2;        // bytes per element
   static constexpr int BK = 128 / EB;          // elements per stage
-  static constexpr int WAVES_N = BN / WN, WAVES = BM / WM * WAVES_N, THREADS = 64 * WAVES;
+  static constexpr int WAVES_N = BN / WN, WAVES = BM / WM * WAVES_N, THREADS = 64 * WAVES * KS;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   // 8-bit: the scale dwords of a stage, BM rows', then the weight blocks' (64 per load; the
   // waves past the rows' all bring the latter)
@@ -255,12 +256,13 @@ struct Tile {
   static constexpr int READS = 2 * (MT + NT);                // LDS fragment reads per sub-step
   static constexpr int PRODUCTS = MT * NT * (F8 ? 1 : 2);    // matrix instructions per sub-step
   static constexpr int EPI_ROW = 32 * 2 + 16;                // epilogue staging: 32 rows of 32 16-bit outputs, padded
-  static constexpr int EPI = ST * STAGE, GROUPS = EPI + WAVES * 32 * EPI_ROW;
-  static constexpr int LDS = GROUPS + WAVES * 768;
+  static constexpr int RING = ST * STAGE, EPI = KS * RING, GROUPS = EPI + WAVES * 32 * EPI_ROW;
+  static constexpr int LDS = GROUPS + WAVES * KS * 768;
   static constexpr bool TA = LAY == L_TN, TB = LAY != L_NT;  // operands stored [contraction, columns]
   static_assert(AL * 1024 * WAVES == A_BYTES && BL * 1024 * WAVES == B_BYTES, "whole loads");
   static_assert(!F8 || WAVES > BM / 64, "waves for the rows' scales and the weights'");
   static_assert(LDS <= 160 * 1024, "LDS of a compute unit");
+  static_assert((KS - 1) * 4096 * MT * NT * WAVES <= EPI, "room for the sums");
 };
 
 // An operand tile of C rows / columns in LDS.  Row-contiguous operands (TR = 0) lie as rows
@@ -371,10 +373,11 @@ struct Stream {
 };
 
 template <class C, int TO>
-__global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 : 2) k_gemm(const GemmArgs p) {
+__global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::THREADS / 256 : 2) k_gemm(const GemmArgs p) {
   constexpr int TY = C::TY, LAY = C::LAY, BM = C::BM, BN = C::BN;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kg = C::KS > 1 ? wave / C::WAVES : 0, wid = wave - kg * C::WAVES;  // its set, and its number there
   const int wm = wid / C::WAVES_N, wn = wid % C::WAVES_N;
   constexpr bool BIG = BM == kBig;
   // ---- the launch's list: large tiles [0, whole), or the small tiles that the others
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
   const int units_m = (p.rows + um - 1) / um;  // TN
   Groups gr;
   gr.offsets = p.offsets;
-  gr.at = reinterpret_cast<int*>(lds + C::GROUPS + wid * 768);
+  gr.at = reinterpret_cast<int*>(lds + C::GROUPS + wave * 768);
   gr.E = p.E;
   gr.T = p.T;
   gr.bm = um;
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
       return;
     }
     w.kdim = LAY == L_TN ? w.g.rows : p.kdim;
-    const int k = (w.kdim + C::BK - 1) / C::BK;
+    const int k = (w.kdim + C::KS * C::BK - 1) / (C::KS * C::BK);
     // a stream that goes on in the next tile is at most one tile ahead; stages past the end
     // read zeros
     w.stages = BIG && k < C::ST ? C::ST : (k < 1 ? 1 : k);
@@ -479,7 +482,8 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
   // (a wave's loads are consecutive)
   const uint32_t ra = OA::row(lane, lda), rb = OB::row(lane, ldb);
   const int ca = OA::chunk(lane), cb = OB::chunk(lane);
-  const uint32_t fa = OA::frag(lane, wm * C::WM), fb = OB::frag(lane, wn * C::WN) + C::A_BYTES;
+  const uint32_t ring = kg * C::RING;
+  const uint32_t fa = ring + OA::frag(lane, wm * C::WM), fb = ring + OB::frag(lane, wn * C::WN) + C::A_BYTES;
   // 8-bit: the first BM / 64 waves bring 64 rows' scale dwords each, the others the weight blocks'
   const uint32_t so = (uint32_t)((wid < BM / 64 ? lane : lane & (BN / 128 > 1 ? 1 : 0)) * p.lds);
 
@@ -492,14 +496,14 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
   uint32_t va[2], vb[2];  // lane offsets of even and odd loads
   auto begin_tile = [&](const Work& w) {
     const int ga = wid * C::AL * OA::ROWS, gb = wid * C::BL * OB::ROWS;  // the wave's first row
-    ls.pa = w.pa + (int64_t)ga * lda;
-    ls.pb = w.pb + (int64_t)gb * ldb;
+    ls.pa = w.pa + (int64_t)ga * lda + kg * da;
+    ls.pb = w.pb + (int64_t)gb * ldb + kg * db;
     ls.ps = w.ps;
-    ls.na = w.na - ga * (int)lda;
-    ls.nb = w.nb - gb * (int)ldb;
+    ls.na = w.na - ga * (int)lda - 128 * kg;
+    ls.nb = w.nb - gb * (int)ldb - 128 * kg;
     ls.ns = w.ns;
-    ls.k = 0;
-    ls.left = w.kdim;
+    ls.k = kg;
+    ls.left = w.kdim - kg * C::BK;
     ls.xa = w.m0 * C::EB;
     ls.xb = w.n0 * C::EB;
   };
@@ -522,12 +526,12 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
       const int at = (ls.k >> 2) * 4;
       dss = make_desc(ls.ps + at, left > 0 ? ls.ns - at : 0);
     }
-    ls.pa += da;
-    ls.pb += db;
-    ls.na -= 128;
-    ls.nb -= 128;
-    ls.left -= C::BK;
-    ++ls.k;
+    ls.pa += C::KS * da;
+    ls.pb += C::KS * db;
+    ls.na -= C::KS * 128;
+    ls.nb -= C::KS * 128;
+    ls.left -= C::KS * C::BK;
+    ls.k += C::KS;
   };
   auto issue_b = [&](int q, uint32_t S) {  // load number q of the stage's second operand
     direct_load16(dsb, S + C::A_BYTES + (wid * C::BL + q) * 1024, vb[q & 1] + q * OB::ROWS * ldb);
@@ -555,8 +559,8 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
       f.a[x - C::NT][ks] = OA::read(lds, sa, x - C::NT, sub, ks);
   };
   auto read_scales = [&](int kt, int start, Scales& s) {
-    const uint32_t at = start + C::A_BYTES + C::B_BYTES;
-    const int sh = 8 * (kt & 3);
+    const uint32_t at = ring + start + C::A_BYTES + C::B_BYTES;
+    const int sh = 8 * ((C::KS * kt + kg) & 3);
     s.w = (int)((uint32_t)read_word(lds, at + 4 * (BM + (wn * C::WN) / 128)) >> sh);
 #pragma unroll
     for (int i = 0; i < C::MT; ++i)
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
   constexpr int RB = (2 * C::NT + HALF - 1) / HALF, RA = (2 * C::MT + HALF - 1) / HALF;
   constexpr int IB = (C::BL + HALF - 1) / HALF, IA = (C::AX + HALF - 1) / HALF;
 
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;  // LDS address of the buffers
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds + ring;  // LDS address of the buffers
   const int step = gridDim.x;
   const int slot = xcd_slot(blockIdx.x, step);
   auto tile_of = [&](int round) { return round * step + (sorted && (round & 1) ? step - 1 - slot : slot); };
@@ -676,6 +680,37 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::WAVES / 4 
         __builtin_amdgcn_sched_barrier(0);
       }
       sc = sn;
+    }
+
+    if (C::KS > 1) {  // the other sets' sums go to the first, which adds them in order and stores
+      wait_loads<0>();  // (zeros past the last stage still land in the rings)
+      __builtin_amdgcn_s_barrier();
+      __asm__ volatile("" ::: "memory");
+      constexpr int PIECES = 4 * C::MT * C::NT;  // 16 bytes of each lane
+      float4* sums = reinterpret_cast<float4*>(lds) + wid * (64 * PIECES) + lane;
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const v16f& t = acc[i / (4 * C::NT)][i / 4 % C::NT];
+        const int a = 4 * (i & 3);
+        if (kg > 0) sums[((kg - 1) * C::WAVES * PIECES + i) * 64] = make_float4(t[a], t[a + 1], t[a + 2], t[a + 3]);
+      }
+      wait_lgkm();
+      __builtin_amdgcn_s_barrier();
+      __asm__ volatile("" ::: "memory");
+      if (kg > 0) return;  // (no barrier follows: one tile per block)
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        v16f& t = acc[i / (4 * C::NT)][i / 4 % C::NT];
+        const int a = 4 * (i & 3);
+#pragma unroll
+        for (int g = 0; g < C::KS - 1; ++g) {
+          const float4 o = sums[(g * C::WAVES * PIECES + i) * 64];
+          t[a] += o.x;
+          t[a + 1] += o.y;
+          t[a + 2] += o.z;
+          t[a + 3] += o.w;
+        }
+      }
     }
 
     // ---- epilogue: lane l holds row l % 32 of a tile and columns 8 a + 4 (l / 32) + 0 .. 3 in
@@ -1018,8 +1053,6 @@ hipError_t launch_few(const GemmArgs& a, hipStream_t st) {
 // a group that is not a kernel's has no tiles there.
 constexpr int kFew = 16;
 
-
-
 int device_cus() {
   static thread_local int known_dev = -1, cus = 0;
   int dev = 0;
@@ -1047,11 +1080,15 @@ hipError_t run_gemm(GemmArgs a, hipStream_t st) {
   if (LAY == L_NT) {
     // Few rows: 16 to a group on average, or 32 in all, or so little work that tiles would
     // leave most compute units idle (4096 x 4096 in 8 bits: 64 rows 10 us against 23, 128 rows
-    // 15 against 23; 14336 x 4096, 64 rows: 27 against 25).
+    // 15 against 23; 14336 x 4096, 64 rows: 27 against 25).  With at most 128 rows in all a
+    // group of many rows goes there too, 16 rows at a time, which saves the second launch (8 bits,
+    // 128 rows in 8 groups of 4096 x 2048: 25 us against 36; all of them in one group of
+    // 14336 x 4096: 56 against 37).  With more rows the limit stays at 32 (1024 rows in 64
+    // groups of 4096 x 2048: 124 us, with a limit of 64 141).
     const bool little = (a.T + 32 * groups - 1) / (32 * groups) * tiles(128) * 2 <= a.cus;
     if (little || a.T <= kFew * groups || a.T <= 2 * kFew) {
       GemmArgs f = a;
-      const int limit = little ? 8 * kFew : 2 * kFew;
+      const int limit = little || a.T <= 8 * kFew ? 8 * kFew : 2 * kFew;
       f.most = a.T < limit ? a.T : limit;
       const hipError_t e = launch_few<TY>(f, st);
       if (e != hipSuccess || a.T <= limit) return e;
@@ -1059,28 +1096,34 @@ hipError_t run_gemm(GemmArgs a, hipStream_t st) {
     }
   }
   const int64_t units = tiles(kBig);
-  // Small tiles: with four stages in flight where compute units get one of them each at most,
-  // else two blocks per unit with two stages each.
+  // Small tiles.  A block alone on its compute unit waits for each stage's chain of barrier, LDS
+  // reads and products, so where there is one block to a unit at most, sets of waves take the
+  // stages in turn (1024 x 1024 outputs, contraction 4096: 64 x 64 tiles with 1, 2, 4 sets 29, 20
+  // and 19 us in bf16, 19, 13.5 and 12.6 in 8 bits; 2048^3 in 128 x 128 tiles with 1, 2 sets 25.1
+  // and 23.4).  Else two blocks per unit with two stages in flight each.
   using Small4 = Tile<TY, LAY, 128, 128, 64, 64, 4>;
+  using SmallK = Tile<TY, LAY, 128, 128, 64, 64, 2, 2>;
   using Small2 = Tile<TY, LAY, 128, 128, 64, 64, 2>;
   // They alone: where large tiles would not fill a round, or be mostly empty (groups that
   // average less than a large tile's rows).
   if (units * 256 < (int64_t)kTailShare * a.cus || (LAY != L_TN && (int64_t)a.T < kBig * groups)) {
     a.direct = 1;
     const int64_t n = tiles(128), n64 = tiles(64);
-    if (n64 <= a.cus) return launch_gemm<Tile<TY, LAY, 64, 64, 32, 64, 8>, TO>(a, n64, st);
-    if (n64 <= 2 * a.cus) return launch_gemm<Tile<TY, LAY, 64, 64, 32, 64, 4>, TO>(a, n64, st);
-    return 4 * n <= 5 * a.cus ? launch_gemm<Small4, TO>(a, n, st) : launch_gemm<Small2, TO>(a, n, st);
+    if (n64 <= a.cus) return launch_gemm<Tile<TY, LAY, 64, 64, 32, 64, 2, 4>, TO>(a, n64, st);
+    if (n64 <= 2 * a.cus) return launch_gemm<Tile<TY, LAY, 64, 64, 32, 64, 2, 2>, TO>(a, n64, st);
+    return 4 * n <= 5 * a.cus ? launch_gemm<SmallK, TO>(a, n, st) : launch_gemm<Small2, TO>(a, n, st);
   }
   const hipError_t e =
       launch_gemm<Tile<TY, LAY, kBig, kBig, 64, 128, 2>, TO>(a, units < a.cus ? units : a.cus, st);
   if (e != hipSuccess) return e;
-  // what is left over: less than kTailShare of a round
+  // What is left over, less than kTailShare of a round: at most one small tile per compute unit.
+  // All units load at once there, so four stages in flight beat two (dX of 8192 x 4096 x 2048 in
+  // 8 groups 158 us against 165) and two sets of waves (166 against 170).
   const bool sure = LAY == L_TN || a.offsets == nullptr;
   int64_t rest = ((int64_t)kTailShare * a.cus - 1) / 256;
   if (units < rest) rest = units;
   if (sure) rest = units % a.cus <= rest ? units % a.cus : 0;
-  return rest == 0 ? hipSuccess : launch_gemm<Small2, TO>(a, 4 * rest, st);
+  return rest == 0 ? hipSuccess : launch_gemm<Small4, TO>(a, 4 * rest, st);
 }
 
 // ------------------------------------------------------------------------ quantizers

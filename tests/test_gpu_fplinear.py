@@ -393,6 +393,22 @@ def test_grouped_tile_schedules(ops, rows, d, n):
     check(ops.grouped_linear_dw(dYd, Xd, offd, dtype=torch.float32), dw, mag, max(rows), "dW")
 
 
+@pytest.mark.parametrize("rows", [[90, 0, 3, 1, 0, 0, 20, 14], [0, 0, 128, 0, 0, 0, 0, 0], [33, 17, 16, 15, 31, 1, 14, 0]])
+def test_groups_of_many_rows_in_a_small_batch(ops, rows):
+    """At most 128 rows in all: every group goes 16 or 32 rows at a time, however many it has."""
+    d, n, M = 4104, 80, sum(rows)
+    off = offsets_of(rows)
+    X, W = randn(M, (M, n), 1.0, torch.bfloat16), randn(5, (8, d, n), 0.05, torch.bfloat16)
+    want, mag = ref.grouped(X.double().numpy(), off.tolist(), W.double().numpy())
+    check(ops.grouped_linear(X.cuda(), off.cuda(), W.cuda()), want, mag, n, "forward")
+    (xq, sx), w = ops.fp8_quant_act(X.cuda()), ops.fp8_quant_weight(W.cuda())
+    x = ref.dequantize(codes_of(xq), sx.cpu().numpy(), 1)
+    wd = np.stack([ref.dequantize(codes_of(w["wq"][e]), w["sw"][e].cpu().numpy(), 128) for e in range(8)])
+    want, mag = ref.grouped(x, off.tolist(), wd)
+    extra = np.concatenate([aligned(x[a:b], wd[e]) for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:]))])
+    check(ops.fp8_grouped_linear(xq, sx, off.cuda(), w["wq"], w["sw"]), want, mag, n, extra=extra)
+
+
 @pytest.mark.parametrize("M,d,n", [(4300, 4096, 64), (2100, 2304, 400), (1200, 1283, 272)])
 def test_fp8_tile_schedules(ops, M, d, n):
     X, W = randn(M, (M, n)), randn(d, (d, n), 0.02)
