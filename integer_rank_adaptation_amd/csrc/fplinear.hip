@@ -338,17 +338,24 @@ struct GemmArgs {
   int lds;                // scale bytes per row
   int cus;                // blocks of the large tiles' launch
   int direct;             // no large tiles: the small ones are counted by themselves
+  int rest_least, rest_most;  // small tiles of left-over large ones: their number if this launch is for them
 };
 
 constexpr int kBig = 256;        // the large tiles: kBig x kBig outputs, one block per compute unit
-constexpr int kTailShare = 65;  // a last round of at least this many large tiles (of 256) is not cut up
+// A last round of at least this many large tiles (of 256) is not cut up.  (4096 tokens, two
+// blocks of small tiles to a compute unit: half a round of large tiles takes 47 us with
+// contraction 2048, its small tiles 36; 160 of 256 54 and 56.)
+constexpr int kTailShare = 129;
+// dW behind whole rounds: its last tiles are the ones of the smallest groups and cost less than a
+// round (half a round of 640 tiles, 4 groups: 84 us, cut up 92; a quarter of one is cut up).
+constexpr int kTailShareDw = 65;
 
 // Large tiles that a full grid of `cus` blocks takes in whole rounds; the rest is cut into
 // small tiles, which fill the chip where a round of few large tiles would leave most
 // compute units idle.
-__device__ __forceinline__ int whole_rounds(int total, int cus) {
+__device__ __forceinline__ int whole_rounds(int total, int cus, int share) {
   const int rem = total % cus;
-  return rem * 256 >= kTailShare * cus ? total : total - rem;
+  return rem * 256 >= share * cus ? total : total - rem;
 }
 
 // One output tile: its place, and where its operands start.  na, nb: bytes from there to the
@@ -401,9 +408,10 @@ __global__ void __launch_bounds__(C::THREADS, C::LDS > 80 * 1024 ? C::THREADS / 
   // other round goes through the blocks backwards, which evens their loads out
   const bool sorted = LAY == L_TN && (BIG || cut) && p.E <= 64;
   if (sorted) gr.sort();
-  const int whole = BIG || cut ? whole_rounds(total, p.cus) : 0;
+  const int whole = BIG || cut ? whole_rounds(total, p.cus, LAY == L_TN ? kTailShareDw : kTailShare) : 0;
   constexpr int PER_M = kBig / BM, PER = PER_M * (kBig / BN);
-  const int list = BIG ? whole : cut ? (total - whole) * PER : total;
+  const int rest = total - whole;
+  const int list = BIG ? whole : !cut ? total : rest >= p.rest_least && rest <= p.rest_most ? rest * PER : 0;
 
   const uint32_t lda = (uint32_t)((LAY == L_TN ? p.rows : p.kdim) * C::EB);
   const uint32_t ldb = (uint32_t)((LAY == L_NT ? p.kdim : p.cols) * C::EB);
@@ -1111,19 +1119,32 @@ hipError_t run_gemm(GemmArgs a, hipStream_t st) {
     const int64_t n = tiles(128), n64 = tiles(64);
     if (n64 <= a.cus) return launch_gemm<Tile<TY, LAY, 64, 64, 32, 64, 2, 4>, TO>(a, n64, st);
     if (n64 <= 2 * a.cus) return launch_gemm<Tile<TY, LAY, 64, 64, 32, 64, 2, 2>, TO>(a, n64, st);
-    return 4 * n <= 5 * a.cus ? launch_gemm<SmallK, TO>(a, n, st) : launch_gemm<Small2, TO>(a, n, st);
+    return n <= a.cus ? launch_gemm<SmallK, TO>(a, n, st) : launch_gemm<Small2, TO>(a, n, st);
   }
   const hipError_t e =
       launch_gemm<Tile<TY, LAY, kBig, kBig, 64, 128, 2>, TO>(a, units < a.cus ? units : a.cus, st);
   if (e != hipSuccess) return e;
-  // What is left over, less than kTailShare of a round: at most one small tile per compute unit.
-  // All units load at once there, so four stages in flight beat two (dX of 8192 x 4096 x 2048 in
-  // 8 groups 158 us against 165) and two sets of waves (166 against 170).
+  // What is left over, less than whole_rounds' share of one.  Up to a quarter of a round is one small
+  // tile per compute unit at most, and all units load at once there: four stages in flight beat
+  // two (dX of 8192 x 4096 x 2048 in 8 groups 158 us against 165) and two sets of waves (166
+  // against 170).  More is two blocks to a unit (half a round, 4096 tokens, contraction 2048: 95 us
+  // against 105 with four stages and so one block).  Where only the device knows how much is left,
+  // both are launched and one of them finds no work (3 us).
   const bool sure = LAY == L_TN || a.offsets == nullptr;
-  int64_t rest = ((int64_t)kTailShare * a.cus - 1) / 256;
-  if (units < rest) rest = units;
-  if (sure) rest = units % a.cus <= rest ? units % a.cus : 0;
-  return rest == 0 ? hipSuccess : launch_gemm<Small4, TO>(a, 4 * rest, st);
+  const int64_t most = ((int64_t)(LAY == L_TN ? kTailShareDw : kTailShare) * a.cus - 1) / 256;
+  const int64_t quarter = a.cus / 4, left = units % a.cus;
+  if (sure && left > most) return hipSuccess;
+  const int64_t rest = sure ? left : units < most ? units : most;
+  if (rest > 0 && (!sure || rest <= quarter)) {
+    a.rest_least = 1;
+    a.rest_most = (int)quarter;
+    const hipError_t e4 = launch_gemm<Small4, TO>(a, 4 * (rest < quarter ? rest : quarter), st);
+    if (e4 != hipSuccess) return e4;
+  }
+  if (rest <= quarter) return hipSuccess;
+  a.rest_least = (int)quarter + 1;
+  a.rest_most = (int)most;
+  return launch_gemm<Small2, TO>(a, 4 * rest, st);
 }
 
 // ------------------------------------------------------------------------ quantizers

@@ -421,6 +421,14 @@ def test_fp8_tile_schedules(ops, M, d, n):
 
 
 # --------------------------------------------------------------------------- far offsets
+def test_last_rounds_up_to_half_full(ops):
+    """Large tiles that leave a quarter to a half of a round over (on 256 compute units), with
+    and without the host knowing how many."""
+    test_grouped_tile_schedules(ops, [2400, 0, 2600], 4608, 64)
+    test_grouped_tile_schedules(ops, [1100, 1300], 4608, 72)
+    test_fp8_tile_schedules(ops, 5000, 4608, 80)
+
+
 def test_weights_past_32_bits(ops):
     """The last of 70 experts lies past 4 GiB; few rows and tiled kernel, 8 bits."""
     E, d, n = 70, 8192, 8192
