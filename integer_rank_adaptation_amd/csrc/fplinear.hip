@@ -239,6 +239,13 @@ __device__ __forceinline__ int xcd_slot(int b, int n) {
 // through a ring of ST LDS buffers filled by direct loads; a stage is two sub-steps of 64
 // bytes.  With KS > 1 the block has KS such sets of waves with a ring each, which take the
 // stages in turn; their sums meet in LDS.
+//
+// Products of many rows are bound by the matrix cores and by the loads that feed them: a stage of
+// a 256 x 256 tile takes about 1.7 us, its matrix instructions alone 1.0 and its direct loads alone
+// 1.1 (64 KB per compute unit through L2).  256 x 256 x 8 waves because the bytes loaded per
+// product fall with the tile's side and the sums of 64 x 128 outputs are half of a wave's
+// registers.  8192^3: 8 bits 423 us (2.60 PFLOP/s), bf16 forward 821, dX 844, dW 834 us (1.34,
+// 1.30, 1.32 PFLOP/s); the matrix cores are busy 54 to 67 % of the time.
 template <int TY_, int LAY_, int BM_, int BN_, int WM_, int WN_, int ST_, int KS_ = 1>
 struct Tile {
   static constexpr int TY = TY_, LAY = LAY_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_, KS = KS_;
@@ -816,8 +823,11 @@ hipError_t launch_gemm(const GemmArgs& a, int64_t blocks, hipStream_t st) {
 // their sums meet in LDS in a fixed order (ks = 1: every wave has tiles of its own, and no
 // barrier).  Each wave keeps a ring of runs of its own in LDS, filled by direct loads of 4 rows
 // x 256 bytes.  The grid is persistent and the runs of a wave's consecutive tiles are one
-// stream, so the memory is kept busy across a tile's end.  (Fragments loaded straight into registers take 16 bytes from
-// each of 16 rows per 16 lanes: 16-token products then streamed 3 TB/s.)
+// stream, so the memory is kept busy across a tile's end.  (Fragments loaded straight into
+// registers take 16 bytes from each of 16 rows per 16 lanes: 16-token products then streamed
+// 3 TB/s.)  Bound by memory: 14336 x 4096 in 8 bits 14.2 us for 1 token (4.1 TB/s), 15.5 for 16,
+// 19.0 for 32; bf16 experts of 4096 x 2048, 16 tokens 25.1 us (4.7 TB/s); 4096 x 4096 in 8 bits,
+// 1 token 6.2 us, where launch and first loads count.
 template <int TY_, int TT_>
 struct Few {
   static constexpr int TY = TY_, TT = TT_;
@@ -1040,6 +1050,9 @@ hipError_t launch_few_tt(const GemmArgs& a, hipStream_t st) {
   }
   const int64_t groups = a.E < a.T ? a.E : a.T;
   const int64_t tiles = ((int64_t)a.cols + 15) / 16 * ((a.T + 16 * TT - 1) / (16 * TT) + groups - 1);
+  // All waves of a block on one tile, but fewer where a wave would have less than two runs of it
+  // and there are tiles enough without (64 experts of 2048 x 1024, 64 rows in 8 bits: 20 us, with
+  // all eight waves on a tile 31; 14336 x 1024, 16 rows: 6.9 against 7.3).
   int ks = C::WAVES;
   const int64_t runs = ((int64_t)a.kdim * (TY == T_FP8 ? 1 : 2) + 255) / 256;
   while (ks > 1 && runs < 2 * ks && tiles * ks >= 2 * (int64_t)a.cus * C::WAVES) ks /= 2;
@@ -1049,7 +1062,8 @@ hipError_t launch_few_tt(const GemmArgs& a, hipStream_t st) {
 }
 
 // 16 token rows at a time also where groups average half as many: one of 17 to 32 rows then
-// reads its weights twice (the second time from cache).
+// reads its weights twice, the second time from cache (512 rows in 64 groups of 2048 x 1024 in
+// bf16: 54 us, 32 at a time 72; 256 rows in 16 groups of 4096 x 2048: 68 and 60).
 template <int TY>
 hipError_t launch_few(const GemmArgs& a, hipStream_t st) {
   const int64_t groups = a.E < a.T ? a.E : a.T;
@@ -1108,7 +1122,9 @@ hipError_t run_gemm(GemmArgs a, hipStream_t st) {
   // reads and products, so where there is one block to a unit at most, sets of waves take the
   // stages in turn (1024 x 1024 outputs, contraction 4096: 64 x 64 tiles with 1, 2, 4 sets 29, 20
   // and 19 us in bf16, 19, 13.5 and 12.6 in 8 bits; 2048^3 in 128 x 128 tiles with 1, 2 sets 25.1
-  // and 23.4).  Else two blocks per unit with two stages in flight each.
+  // and 23.4).  Else two blocks per unit with two stages in flight each.  The 64 x 64 tiles as
+  // long as all of them are at work at once (8 bits, 512 of them, contraction 4096: 19 us, 128 x
+  // 128 22; 768 of them 31 and 23).
   using Small4 = Tile<TY, LAY, 128, 128, 64, 64, 4>;
   using SmallK = Tile<TY, LAY, 128, 128, 64, 64, 2, 2>;
   using Small2 = Tile<TY, LAY, 128, 128, 64, 64, 2>;
@@ -1238,7 +1254,8 @@ __global__ void __launch_bounds__(256) k_fp8_act(uint32_t units, uint32_t n, uin
 }
 
 // Weights: one block of 128 x 128 per workgroup, and, when asked for, the same codes
-// transposed (through LDS) for the input gradient's product.
+// transposed (through LDS) for the input gradient's product.  Bound by memory: 14336 x 4096 bf16
+// 32 us, 5.6 TB/s; with the transpose 39 us, 6.0 TB/s.
 template <int TI>
 __global__ void __launch_bounds__(256) k_fp8_weight(int d, int n, int lds, int lds_t, const void* __restrict__ W,
                                                     uint8_t* __restrict__ wq, uint8_t* __restrict__ sw,
