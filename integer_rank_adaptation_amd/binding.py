@@ -303,9 +303,10 @@ def intlora_grad_ws_bytes(numel) -> int:
     return int(lib().intlora_grad_ws_bytes(len(numel), numel))
 
 
-def intlora_grad_sumsq(grads, numel, dtype, sumsq, ws, stream=None):
-    """grads, numel, dtype: ctypes arrays of pointers, int64 and int32 (host)."""
-    wsb = 0 if ws is None else ws.numel() * ws.element_size()
+def intlora_grad_sumsq(grads, numel, dtype, sumsq, ws, stream=None, ws_bytes=None):
+    """grads, numel, dtype: ctypes arrays of pointers, int64 and int32 (host); ws: a tensor, or
+    an address and its ws_bytes."""
+    wsb = ws_bytes if ws_bytes is not None else 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib().intlora_grad_sumsq(len(numel), grads, numel, dtype, _ptr(sumsq), _ptr(ws), wsb, _stream(stream)),
            "intlora_grad_sumsq")
 

@@ -437,10 +437,11 @@ def _numels(ts):
 
 
 def _sumsq(ptrs, numel, types, dev):
-    ws = torch.empty(8 + B.intlora_grad_ws_bytes(numel) // 8, dtype=torch.float64, device=dev)  # the sum, then the parts
-    sumsq = ws[:1]
-    B.intlora_grad_sumsq(ptrs, numel, types, sumsq, ws[8:])
-    return sumsq
+    size = B.intlora_grad_ws_bytes(numel)
+    ws = torch.empty(8 + size // 8, dtype=torch.float64, device=dev)  # the sum, then the parts
+    at = ws.data_ptr()
+    B.intlora_grad_sumsq(ptrs, numel, types, at, at + 64, ws_bytes=size)
+    return ws
 
 
 def _clip(ptrs, numel, types, grads, sumsq, max_norm, out, dev):
@@ -448,7 +449,7 @@ def _clip(ptrs, numel, types, grads, sumsq, max_norm, out, dev):
     if out is not None:
         out = _tensors("out", out)
         outs = _pointers("out", out, dev)
-        if len(out) != len(grads) or bytes(_types("out", out)) != bytes(types) or bytes(_numels(out)) != bytes(numel):
+        if list(map(torch.Tensor.numel, out)) != list(numel) or list(map(_dtype, out)) != list(map(_dtype, grads)):
             raise ValueError("out: expected tensors of the gradients' sizes and types")
     norm = torch.empty(1, dtype=torch.float32, device=dev)
     B.intlora_grad_clip(ptrs, outs, numel, types, sumsq, max_norm, norm)
@@ -462,13 +463,14 @@ def clip_grad_norm(grads, max_norm, out=None):
     Ranks that each hold a part call grad_sumsq, add their sums and call grad_clip."""
     dev, grads = torch.cuda.current_device(), _tensors("grads", grads)
     a = _pointers("grads", grads, dev), _numels(grads), _types("grads", grads)
-    return _clip(*a, grads, _sumsq(*a, dev), max_norm, out, dev)
+    ws = _sumsq(*a, dev)
+    return _clip(*a, grads, ws.data_ptr(), max_norm, out, dev)
 
 
 def grad_sumsq(grads):
     """The sum of all squared gradients, a device tensor [1] (fp64)."""
     dev, grads = torch.cuda.current_device(), _tensors("grads", grads)
-    return _sumsq(_pointers("grads", grads, dev), _numels(grads), _types("grads", grads), dev)
+    return _sumsq(_pointers("grads", grads, dev), _numels(grads), _types("grads", grads), dev)[:1]
 
 
 def grad_clip(grads, sumsq, max_norm, out=None):

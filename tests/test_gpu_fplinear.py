@@ -421,6 +421,32 @@ def test_fp8_tile_schedules(ops, M, d, n):
 
 
 # --------------------------------------------------------------------------- far offsets
+def test_most_groups_and_no_rows(ops):
+    """4096 groups, most of them of no or few rows, one of many; and a call without a row."""
+    rng = np.random.default_rng(8)
+    rows = rng.choice([0, 0, 0, 1, 2, 5], 4096).tolist()
+    rows[4000], rows[4095] = 300, 17
+    d, n, M = 16, 48, sum(rows)
+    off = offsets_of(rows)
+    t = torch.bfloat16
+    X, W, dY = randn(1, (M, n), 1.0, t), randn(2, (4096, d, n), 0.05, t), randn(3, (M, d), 0.1, t)
+    x, w, dy = X.double().numpy(), W.double().numpy(), dY.double().numpy()
+    Xd, Wd, dYd, offd = X.cuda(), W.cuda(), dY.cuda(), off.cuda()
+    y, mag = ref.grouped(x, off.tolist(), w)
+    check(ops.grouped_linear(Xd, offd, Wd), y, mag, n, "forward")
+    dx, mag = ref.grouped(dy, off.tolist(), w.transpose(0, 2, 1))
+    check(ops.grouped_linear_dx(dYd, offd, Wd), dx, mag, d, "dX")
+    dw, mag, _ = ref.grouped_dw(dy, x, off.tolist())
+    check(ops.grouped_linear_dw(dYd, Xd, offd, dtype=torch.float32), dw, mag, max(rows), "dW")
+    none = torch.zeros(4097, dtype=torch.int64, device="cuda")
+    assert ops.grouped_linear(Xd[:0], none, Wd).shape == (0, d)
+    assert ops.grouped_linear_dx(dYd[:0], none, Wd).shape == (0, n)
+    out = torch.full((4096, d, n), 3.0, dtype=t, device="cuda")
+    assert not ops.grouped_linear_dw(dYd[:0], Xd[:0], none, out=out).any()
+    out.fill_(3.0)
+    assert not ops.grouped_linear_dw(dYd, Xd, none, out=out).any()
+
+
 def test_last_rounds_up_to_half_full(ops):
     """Large tiles that leave a quarter to a half of a round over (on 256 compute units), with
     and without the host knowing how many."""
