@@ -435,7 +435,8 @@ int intlora_grouped_linear_dw(int64_t M, int64_t E, int64_t d, int64_t n, int dt
  *   outputs and an infinite one zeros (NaN for infinite gradients); norm_out[0] =
  *   RN32(sqrt(sumsq)), or NULL.  out_i may be grads_i (in place); outputs and norm_out must not
  *   otherwise overlap inputs, sumsq or each other: INTLORA_EINVAL.  max_norm >= 0.
- * Workspace of the sum: intlora_grad_ws_bytes (8 bytes per 16384 elements or part). */
+ * Workspace of the sum: intlora_grad_ws_bytes (8 bytes per 16384 elements or part); it and sumsq
+ * must not overlap a gradient or each other: INTLORA_EINVAL. */
 size_t intlora_grad_ws_bytes(int64_t count, const int64_t* numel);
 int intlora_grad_sumsq(int64_t count, const void* const* grads, const int64_t* numel, const int32_t* dtype,
                        double* sumsq, void* ws, size_t ws_bytes, void* stream);

@@ -295,12 +295,13 @@ struct Span {
   int64_t bytes;
 };
 
+bool meet(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+
 // No output overlaps an input or another output: blocks would read what others have written.
 int check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins, const char* what) {
-  const auto meet = [](const Span& a, const Span& b) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.p && b.p && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
-  };
   for (const Span* o = outs.begin(); o != outs.end(); ++o) {
     bool bad = false;
     for (const Span& i : ins) bad = bad || meet(*o, i);
@@ -374,6 +375,21 @@ int check_grads(int64_t count, const void* const* grads, const int64_t* numel, c
     if (!grads[i]) return fail(INTLORA_EINVAL, "%s: tensor %lld is NULL", what, (long long)i);
     if (!aligned16(grads[i]))
       return fail(INTLORA_EALIGN, "%s: pointer %p of tensor %lld not 16-byte aligned", what, grads[i], (long long)i);
+  }
+  return INTLORA_OK;
+}
+
+// The sum and the workspace lie in no gradient (blocks write partial sums there while others
+// still read the gradients) and not in each other.
+int check_sumsq_outputs(int64_t count, const void* const* grads, const int64_t* numel, const int32_t* dtype,
+                        const double* sumsq, const void* ws, size_t ws_bytes) {
+  const Span sum{sumsq, sizeof *sumsq}, parts{ws, (int64_t)ws_bytes};
+  if (meet(sum, parts)) return fail(INTLORA_EINVAL, "grad_sumsq: sumsq overlaps the workspace");
+  for (int64_t i = 0; i < count; ++i) {
+    if (numel[i] == 0) continue;
+    const Span g{grads[i], numel[i] * (dtype[i] == INTLORA_FP32 ? 4 : 2)};
+    if (meet(sum, g) || meet(parts, g))
+      return fail(INTLORA_EINVAL, "grad_sumsq: sumsq or the workspace overlaps tensor %lld", (long long)i);
   }
   return INTLORA_OK;
 }
@@ -905,7 +921,9 @@ int intlora_grad_sumsq(int64_t count, const void* const* grads, const int64_t* n
   int s = check_grads(count, grads, numel, dtype, "grad_sumsq");
   if (s) return s;
   if ((s = check_ptrs({sumsq}, "grad_sumsq"))) return s;
-  if ((s = check_ws(ws, ws_bytes, intlora::grad_ws_bytes(count, numel)))) return s;
+  const size_t need = intlora::grad_ws_bytes(count, numel);
+  if ((s = check_ws(ws, ws_bytes, need))) return s;
+  if ((s = check_sumsq_outputs(count, grads, numel, dtype, sumsq, ws, need))) return s;
   if ((s = ensure_device())) return s;
   return launch_status(intlora::launch_grad_sumsq(count, grads, numel, dtype, sumsq, ws,
                                                   static_cast<hipStream_t>(stream)),
