@@ -295,9 +295,10 @@ struct Span {
   int64_t bytes;
 };
 
+// (A tensor without elements meets nothing, wherever its address points.)
 bool meet(const Span& a, const Span& b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.p && b.p && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
 }
 
 // No output overlaps an input or another output: blocks would read what others have written.
