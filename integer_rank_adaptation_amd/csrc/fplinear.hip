@@ -1326,15 +1326,25 @@ int fp8_scale_stride(int64_t n) { return (int)(4 * ((n + 511) / 512)); }
 
 hipError_t launch_fp8_quant_act(int64_t M, int64_t n, int dtype, const void* X, uint8_t* xq, uint8_t* sx,
                                 hipStream_t st) {
-  const uint32_t nb = (uint32_t)((n + 127) / 128), lds = (uint32_t)fp8_scale_stride(n), units = (uint32_t)(M * nb);
-  const dim3 grid((units + 15) / 16);
-  if (dtype == T_FP32)
-    k_fp8_act<T_FP32><<<grid, 256, 0, st>>>(units, (uint32_t)n, nb, lds, X, xq, sx);
-  else if (dtype == T_FP16)
-    k_fp8_act<T_FP16><<<grid, 256, 0, st>>>(units, (uint32_t)n, nb, lds, X, xq, sx);
-  else
-    k_fp8_act<T_BF16><<<grid, 256, 0, st>>>(units, (uint32_t)n, nb, lds, X, xq, sx);
-  return hipGetLastError();
+  const uint32_t nb = (uint32_t)((n + 127) / 128), lds = (uint32_t)fp8_scale_stride(n);
+  // A grid holds less than 2^32 work-items, so less than 2^28 blocks of 16 each: rows past those
+  // take another launch (from 2^28 rows of up to 128 columns on).
+  const int64_t most = ((int64_t(1) << 28) - 16) / nb, eb = dtype == T_FP32 ? 4 : 2;
+  for (int64_t row = 0; row < M; row += most) {
+    const uint32_t units = (uint32_t)((M - row < most ? M - row : most) * nb);
+    const dim3 grid((units + 15) / 16);
+    const uint8_t* x = static_cast<const uint8_t*>(X) + row * n * eb;
+    uint8_t *q = xq + row * n, *s = sx + row * lds;
+    if (dtype == T_FP32)
+      k_fp8_act<T_FP32><<<grid, 256, 0, st>>>(units, (uint32_t)n, nb, lds, x, q, s);
+    else if (dtype == T_FP16)
+      k_fp8_act<T_FP16><<<grid, 256, 0, st>>>(units, (uint32_t)n, nb, lds, x, q, s);
+    else
+      k_fp8_act<T_BF16><<<grid, 256, 0, st>>>(units, (uint32_t)n, nb, lds, x, q, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_fp8_quant_weight(int64_t E, int64_t d, int64_t n, int dtype, const void* W, uint8_t* wq,
