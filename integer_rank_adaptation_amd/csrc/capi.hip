@@ -277,7 +277,7 @@ int check_layer(int64_t M, int64_t E, int64_t d, int64_t n, const char* what) {
     return fail(INTLORA_ESHAPE, "%s: bad shape M=%lld d=%lld n=%lld (d, n <= 2^20)", what, (long long)M, (long long)d,
                 (long long)n);
   if (E < 1 || E > kMaxExperts) return fail(INTLORA_ESHAPE, "%s: E must be in [1, 4096] (got %lld)", what, (long long)E);
-  // blocks of the largest grid any of these calls makes (tiles of 64 x 64)
+  // tiles (64 x 64, more than any of these calls counts) are numbered in 32 bits
   const int64_t row_tiles = (M + 63) / 64 + E, dt = (d + 63) / 64, nt = (n + 63) / 64;
   if (row_tiles * (dt > nt ? dt : nt) >= kMaxDim - 256 || E * dt * nt >= kMaxDim - 256)
     return fail(INTLORA_ESHAPE, "%s: too many tiles", what);

@@ -349,6 +349,8 @@ struct GemmArgs {
 };
 
 constexpr int kBig = 256;        // the large tiles: kBig x kBig outputs, one block per compute unit
+// Blocks of 256 threads that a grid holds: less than 2^32 work-items.
+constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;
 // A last round of at least this many large tiles (of 256) is not cut up.  (4096 tokens, two
 // blocks of small tiles to a compute unit: half a round of large tiles takes 47 us with
 // contraction 2048, its small tiles 36; 160 of 256 54 and 56.)
@@ -1129,10 +1131,12 @@ hipError_t run_gemm(GemmArgs a, hipStream_t st) {
   using SmallK = Tile<TY, LAY, 128, 128, 64, 64, 2, 2>;
   using Small2 = Tile<TY, LAY, 128, 128, 64, 64, 2>;
   // They alone: where large tiles would not fill a round, or be mostly empty (groups that
-  // average less than a large tile's rows).
-  if (units * 256 < (int64_t)kTailShare * a.cus || (LAY != L_TN && (int64_t)a.T < kBig * groups)) {
+  // average less than a large tile's rows).  The large tiles' blocks are persistent, so they also
+  // take what would be more small tiles than a grid holds (thousands of groups of 2^19 outputs).
+  const int64_t n = tiles(128);
+  if (units * 256 < (int64_t)kTailShare * a.cus || (LAY != L_TN && (int64_t)a.T < kBig * groups && n <= kMaxBlocks)) {
     a.direct = 1;
-    const int64_t n = tiles(128), n64 = tiles(64);
+    const int64_t n64 = tiles(64);
     if (n64 <= a.cus) return launch_gemm<Tile<TY, LAY, 64, 64, 32, 64, 2, 4>, TO>(a, n64, st);
     if (n64 <= 2 * a.cus) return launch_gemm<Tile<TY, LAY, 64, 64, 32, 64, 2, 2>, TO>(a, n64, st);
     return n <= a.cus ? launch_gemm<SmallK, TO>(a, n, st) : launch_gemm<Small2, TO>(a, n, st);

@@ -42,3 +42,35 @@ def test_quantizer_of_more_rows_than_one_grid(ops):
     for (_, a), (b, _) in zip(live, live[1:]):
         assert int(codes[a:b].max()) == 0
         assert int(sx[a:b].min()) == 127 and int(sx[a:b].max()) == 127
+
+
+def test_more_small_tiles_than_one_grid(ops):
+    """4096 groups that average one row, of 520448 columns: tiles of 128 x 128 would be more than
+    2^24 blocks of 256 threads.  Three groups have rows; the input gradient (short contraction)
+    and the forward product on the same weights read the other way round."""
+    E, n, d = 4096, 520448, 8
+    rows = {0: 3, 2000: 290, 4095: 3803}
+    M = sum(rows.values())
+    off, at = torch.zeros(E + 1, dtype=torch.int64), 0
+    for e in range(E):
+        at += rows.get(e, 0)
+        off[e + 1] = at
+    assert (M // 128 + E - 1) * (n // 128) >= 1 << 24
+    W = torch.zeros((E, d, n), dtype=torch.bfloat16, device="cuda")
+    for e in rows:
+        W[e] = randn(e, (d, n), 0.05).cuda()
+    dY = randn(7, (M, d))
+    offd = off.cuda()
+    cols = np.unique(np.concatenate([np.arange(300), n // 2 + np.arange(-130, 130), n - 1 - np.arange(300)]))
+    pick = torch.from_numpy(cols).cuda()
+    dX = ops.grouped_linear_dx(dY.cuda(), offd, W)
+    Y = ops.grouped_linear(dY.cuda(), offd, W.view(E, n, d))
+    for e in rows:
+        a, b = int(off[e]), int(off[e + 1])
+        g = dY[a:b].double().numpy()
+        for out, w in ((dX, W[e][:, pick]), (Y, W.view(E, n, d)[e][pick].t())):
+            w = w.cpu().double().numpy()
+            want, mag = g @ w, np.abs(g) @ np.abs(w)
+            acc = (d + 16) * 2.0**-23 * mag  # d terms in binary32, any order; then one rounding to bf16
+            got = out[a:b][:, pick].cpu().double().numpy()
+            assert (np.abs(got - want) <= acc + 2.0**-8 * (np.abs(want) + acc)).all()
