@@ -1111,12 +1111,15 @@ hipError_t run_gemm(GemmArgs a, hipStream_t st) {
     // groups of 4096 x 2048: 124 us, with a limit of 64 141).
     const bool little = (a.T + 32 * groups - 1) / (32 * groups) * tiles(128) * 2 <= a.cus;
     if (little || a.T <= kFew * groups || a.T <= 2 * kFew) {
-      GemmArgs f = a;
       const int limit = little || a.T <= 8 * kFew ? 8 * kFew : 2 * kFew;
-      f.most = a.T < limit ? a.T : limit;
-      const hipError_t e = launch_few<TY>(f, st);
-      if (e != hipSuccess || a.T <= limit) return e;
-      a.least = limit + 1;
+      // (without offsets the one group's rows are known: it is either kernel's alone)
+      if (a.offsets != nullptr || a.T <= limit) {
+        GemmArgs f = a;
+        f.most = a.T < limit ? a.T : limit;
+        const hipError_t e = launch_few<TY>(f, st);
+        if (e != hipSuccess || a.T <= limit) return e;
+        a.least = limit + 1;
+      }
     }
   }
   const int64_t units = tiles(kBig);
