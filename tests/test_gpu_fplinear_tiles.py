@@ -101,3 +101,15 @@ def test_fp8_grouped_tiles(ops, rows, d):  # noqa: F811
     wd = [values(w["wq"][e], w["sw"][e], 128) for e in range(E)]
     _check_groups(Y, off.tolist(), x, wd, n, True)
     assert (Y[:lead] == 7).all() and (Y[M - tail:] == 7).all()
+
+
+@pytest.mark.parametrize("rows,d,n", [([3, 0, 20, 9], 272, 400), ([300, 0, 150, 33], 1040, 272), ([1500, 900], 1104, 2064)])
+def test_fp8_grouped_input_gradient(ops, rows, d, n):  # noqa: F811
+    """dX of every group from the transposed codes of its weight [E, n, d]."""
+    E, M = len(rows), sum(rows)
+    off = offsets_of(rows)
+    w = ops.fp8_quant_weight(torch.stack([spread(e + 50, d, n, 128) for e in range(E)]).cuda(), transpose=True)
+    dq, sd = ops.fp8_quant_act(spread(M, M, d, 1).cuda())
+    dX = ops.fp8_grouped_linear(dq, sd, off.cuda(), w["wq_t"], w["sw_t"])
+    wd = [values(w["wq"][e], w["sw"][e], 128).t().contiguous() for e in range(E)]
+    _check_groups(dX, off.tolist(), values(dq, sd, 1), wd, d, True)
