@@ -113,3 +113,36 @@ def test_fp8_grouped_input_gradient(ops, rows, d, n):  # noqa: F811
     dX = ops.fp8_grouped_linear(dq, sd, off.cuda(), w["wq_t"], w["sw_t"])
     wd = [values(w["wq"][e], w["sw"][e], 128).t().contiguous() for e in range(E)]
     _check_groups(dX, off.tolist(), values(dq, sd, 1), wd, d, True)
+
+
+# --------------------------------------------------------------------------- 16 bits
+# rows, d, n: large tiles where there are 4096 columns; of the weight gradient, without a cut
+# round and with one; 128 x 128
+STEPS = [([2100, 0, 2300, 41], 4096, 1096), ([700, 300, 900, 280], 2304, 2312), ([700, 300, 900, 280], 2296, 2040),
+         ([1500, 900], 1544, 1096)]
+
+
+@pytest.mark.parametrize("rows,d,n", STEPS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_grouped_step_on_large_tiles(ops, dtype, rows, d, n):  # noqa: F811
+    """Both types in all directions, the weight gradient in its inputs' type too."""
+    M, E = sum(rows), len(rows)
+    off = offsets_of(rows)
+    X, dY = randn(M, (M, n), 1.0, dtype).cuda(), randn(n, (M, d), 0.1, dtype).cuda()
+    W = randn(d, (E, d, n), 0.05, dtype).cuda()
+    offd, o = off.cuda(), off.tolist()
+    x, dy, w = X.double(), dY.double(), W.double()
+    Y, dX = ops.grouped_linear(X, offd, W), ops.grouped_linear_dx(dY, offd, W)
+    Wt = W.transpose(1, 2).contiguous()
+    Z, dZ = ops.grouped_linear(dY, offd, Wt), ops.grouped_linear_dx(X, offd, Wt)  # the wide side as columns
+    dW = [ops.grouped_linear_dw(dY, X, offd, dtype=t) for t in (dtype, torch.float32)]
+    dWt = ops.grouped_linear_dw(X, dY, offd)
+    for e in range(E):
+        r = slice(o[e], o[e + 1])
+        we, wt = w[e], w[e].t().contiguous()
+        for got, a, b, k, what in ((Y, x, we, n, "Y"), (dX, dy, wt, d, "dX"), (Z, dy, wt, d, "Z"), (dZ, x, we, n, "dZ")):
+            check(got[r], a[r], b, k, what)
+        dye, xe = dy[r].t().contiguous(), x[r].t().contiguous()
+        for got in dW:
+            check(got[e], dye, xe, rows[e], "dW")
+        check(dWt[e], xe, dye, rows[e], "dW of W^T")
