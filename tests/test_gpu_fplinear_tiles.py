@@ -146,3 +146,119 @@ def test_grouped_step_on_large_tiles(ops, dtype, rows, d, n):  # noqa: F811
         for got in dW:
             check(got[e], dye, xe, rows[e], "dW")
         check(dWt[e], xe, dye, rows[e], "dW of W^T")
+
+
+# --------------------------------------------------------------------------- what lies beside
+def _same_elsewhere(dirty, clean, rows):
+    keep = torch.ones(clean.shape[0], dtype=torch.bool, device="cuda")
+    keep[rows] = False
+    assert torch.isfinite(clean).all() and torch.equal(dirty[keep], clean[keep])
+
+
+@pytest.mark.parametrize("M,d", EVERY_TILE)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_fp8_nonfinite_blocks_in_tiles(ops, M, d, bad):  # noqa: F811
+    """A token block that holds a NaN or infinity makes its row NaN and changes no other output;
+    a weight block its 128 outputs.  Bad blocks at a row's start follow the row before's tail."""
+    n = 208
+    X, W = randn(M, (M, n)).cuda(), randn(d, (d, n), 0.02).cuda()
+    w = ops.fp8_quant_weight(W)
+    Y = ops.fp8_linear(*ops.fp8_quant_act(X), w["wq"], w["sw"])
+    rows = torch.tensor([5, 63, 64, 130, 255, 256, M - 300, M - 1], device="cuda")
+    Xb = X.clone()
+    Xb[rows, torch.tensor([0, 3, 207, 127, 128, 0, 60, 200], device="cuda")] = bad
+    xq, sx = ops.fp8_quant_act(Xb)
+    assert (sx == 255).sum() == len(rows)
+    Yb = ops.fp8_linear(xq, sx, w["wq"], w["sw"])
+    assert torch.isnan(Yb[rows]).all()
+    _same_elsewhere(Yb, Y, rows)
+    Wb = W.clone()
+    Wb[300, 5] = Wb[d - 1, 207] = bad
+    w = ops.fp8_quant_weight(Wb)
+    cols = torch.cat([torch.arange(256, 384), torch.arange((d - 1) // 128 * 128, d)]).cuda()
+    Yb = ops.fp8_linear(*ops.fp8_quant_act(X), w["wq"], w["sw"])
+    assert torch.isnan(Yb[:, cols]).all()
+    _same_elsewhere(Yb.t(), Y.t(), cols)
+
+
+# tiles of the products: 64 x 64 and 128 x 128 in sets, 128 x 128, large ones and their cuts
+BESIDE = [([300, 150, 400], 1096), ([600, 300, 600], 1504), ([500, 200, 500], 4096), ([2100, 196, 2100], 4096)]
+
+
+@pytest.mark.parametrize("rows,d", BESIDE)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_nan_of_one_group_in_tiles(ops, dtype, rows, d):  # noqa: F811
+    """NaN tokens and infinite weights of the middle group change no output of the others, although
+    tiles reach over the groups' borders and the ends of rows (72 columns: half a stage)."""
+    n, M = 72, sum(rows)
+    off = offsets_of(rows)
+    mid = torch.arange(int(off[1]), int(off[2]), device="cuda")
+    X, dY = randn(1, (M, n), 1.0, dtype).cuda(), randn(2, (M, d), 0.1, dtype).cuda()
+    W = randn(3, (3, d, n), 0.05, dtype).cuda()
+    Wt = W.transpose(1, 2).contiguous()
+    offd = off.cuda()
+
+    def run(x, dy, w, wt):
+        return [ops.grouped_linear(x, offd, w), ops.grouped_linear_dx(x, offd, wt), ops.grouped_linear(dy, offd, wt),
+                ops.grouped_linear_dx(dy, offd, w)], [ops.grouped_linear_dw(dy, x, offd), ops.grouped_linear_dw(x, dy, offd)]
+
+    clean, clean_dw = run(X, dY, W, Wt)
+    Xb, dYb, Wb = X.clone(), dY.clone(), W.clone()
+    Xb[mid], dYb[mid], Wb[1] = float("nan"), float("inf"), float("inf")
+    dirty, dirty_dw = run(Xb, dYb, Wb, Wb.transpose(1, 2).contiguous())
+    for a, b in zip(dirty, clean):
+        _same_elsewhere(a, b, mid)
+        assert not torch.isfinite(a[mid]).any()
+    for a, b in zip(dirty_dw, clean_dw):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2]) and torch.isnan(a[1]).all()
+
+
+def _wild_offsets(seed, E, M):
+    """Offsets that ascend on the whole, with entries far outside [0, M] and below their predecessors."""
+    g = rng(seed)
+    off = np.sort(g.integers(0, M + 1, E + 1)).astype(np.int64)
+    off[0] = -(1 << 40)
+    at = g.permutation(np.arange(1, E))
+    k = max(1, E // 6)
+    off[at[:k]] -= g.integers(1, M, k)          # descending, some below 0
+    off[at[k:2 * k]] = -(1 << 62)
+    off[E] = 1 << 62
+    if E > 8:
+        off[E // 2] = min(M, int(off[E // 2 - 1]) + M // 8)
+    return off
+
+
+@pytest.mark.parametrize("M,E,d", [(700, 3, 1096), (1500, 4, 4096), (4396, 3, 4096), (3000, 70, 1032), (18000, 70, 520),
+                                   (9000, 200, 520)])
+def test_bad_offsets_in_tiles(ops, M, E, d):  # noqa: F811
+    """Whatever the offsets hold, rows count as the definition says and no other row is touched."""
+    n, t = 40, torch.bfloat16
+    X, dY = randn(1, (M, n), 1.0, t).cuda(), randn(2, (M, d), 0.1, t).cuda()
+    W = randn(3, (E, d, n), 0.05, t).cuda()
+    (xq, sx), q = ops.fp8_quant_act(torch.nn.functional.pad(X, (0, 8))), ops.fp8_quant_weight(torch.nn.functional.pad(W, (0, 8)))
+    x, dy, w = X.double(), dY.double(), W.double()
+    x8, w8 = values(xq, sx, 1), [values(q["wq"][e], q["sw"][e], 128) for e in range(E)]
+    for seed in (1, 2):
+        off = _wild_offsets(seed, E, M)
+        b = ref.boundaries(off, M)
+        o = torch.from_numpy(off).cuda()
+        if seed == 2:  # rows in front of the first group and behind the last
+            b = ref.boundaries([50, *(off[1:-1] // 2), off[-2] // 2], M)
+            o = torch.tensor([50, *(off[1:-1] // 2), off[-2] // 2], device="cuda")
+        outs = [torch.full((M, c), 7.0, dtype=t, device="cuda") for c in (d, n, n, d, d)]
+        Wt = W.transpose(1, 2).contiguous()
+        ops.grouped_linear(X, o, W, out=outs[0])
+        ops.grouped_linear(dY, o, Wt, out=outs[1])
+        ops.grouped_linear_dx(dY, o, W, out=outs[2])
+        ops.grouped_linear_dx(X, o, Wt, out=outs[3])
+        ops.fp8_grouped_linear(xq, sx, o, q["wq"], q["sw"], out=outs[4])
+        dW = ops.grouped_linear_dw(dY, X, o, dtype=torch.float32)
+        for out in outs:
+            assert (out[:b[0]] == 7).all() and (out[b[-1]:] == 7).all()
+        for e in range(E):
+            r = slice(b[e], b[e + 1])
+            we, wt = w[e], w[e].t().contiguous()
+            for out, a, c, k in zip(outs, (x, dy, dy, x), (we, wt, wt, we), (n, d, d, n)):
+                check(out[r], a[r], c, k, f"group {e}")
+            check(outs[4][r], x8[r], w8[e], 48, f"8 bits, group {e}", True)
+            check(dW[e], dy[r].t().contiguous(), x[r].t().contiguous(), b[e + 1] - b[e], f"dW {e}")
