@@ -431,8 +431,9 @@ int intlora_grouped_linear_dw(int64_t M, int64_t E, int64_t d, int64_t n, int dt
  * INTLORA_BF16 / _FP16 / _FP32 each), read before the call returns; count <= 65536.
  *   sumsq[0] = sum of g^2 over all tensors, in binary64 in a fixed order.  (Ranks that hold
  *   parts of the gradients add their sums before the second call.)
- *   out_i = RN(g c), c = RN32(min(1, max_norm / (sqrt(sumsq) + 1e-6))) -- a NaN sum gives NaN
- *   outputs and an infinite one zeros (NaN for infinite gradients); norm_out[0] =
+ *   out_i = RN32(g c) for binary32 gradients and RN16(RN32(g c)) for 16-bit ones (the product is
+ *   binary32 and then rounded to the type), c = RN32(min(1, max_norm / (sqrt(sumsq) + 1e-6))) --
+ *   a NaN sum gives NaN outputs and an infinite one zeros (NaN for infinite gradients); norm_out[0] =
  *   RN32(sqrt(sumsq)), or NULL.  out_i may be grads_i (in place); outputs and norm_out must not
  *   otherwise overlap inputs, sumsq or each other: INTLORA_EINVAL.  max_norm >= 0.
  * Workspace of the sum: intlora_grad_ws_bytes (8 bytes per 16384 elements or part); it and sumsq

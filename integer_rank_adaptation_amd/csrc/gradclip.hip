@@ -1,7 +1,10 @@
 // Global 2-norm of a list of gradients, and the gradients scaled to it, for gfx950.
 //
 //   s = sum over all tensors of g^2 (binary64),  norm = sqrt(s),
-//   c = min(1, max_norm / (norm + 1e-6)),        g' = RN(g c).
+//   c = RN32(min(1, max_norm / (norm + 1e-6))),  g' = RN32(g c), rounded once more for 16 bits
+//
+// (the rounding to binary32 moves a 16-bit result by at most 2^-24 of its value besides its own
+// half step; one rounding of the 32- to 35-bit product would take binary64 or a correction step).
 //
 // Both passes are bound by memory.  The tensors' addresses travel in the kernel arguments
 // (kPerLaunch tensors per launch), so a call needs no table in device memory, no copy from
