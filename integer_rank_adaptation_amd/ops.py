@@ -349,7 +349,8 @@ def fp8_linear(xq, sx, wq, sw, out=None):
 
 def fp8_grouped_linear(xq, sx, offsets, wq, sw, out=None):
     """As fp8_linear with one weight per group of rows: wq [E, d, n], rows offsets[e] ..
-    offsets[e + 1] - 1 take weight e.  Rows in no group are left as they are in `out`."""
+    offsets[e + 1] - 1 take weight e.  Rows in no group are left as they are in `out`; without
+    `out` they are not initialised."""
     E = _dims("wq", wq, 3)[0]
     dev = torch.cuda.current_device()
     M, d, n, (x, s, w, v) = _fp8_operands(xq, sx, wq, sw, (E,), dev)
@@ -360,7 +361,8 @@ def fp8_grouped_linear(xq, sx, offsets, wq, sw, out=None):
 
 def grouped_linear(X, offsets, W, out=None):
     """Y [M, d] of X [M, n] and W [E, d, n] (bf16 or fp16): rows offsets[e] .. offsets[e + 1] - 1
-    are multiplied by W[e]^T.  Rows in no group are left as they are in `out`."""
+    are multiplied by W[e]^T.  Rows in no group are left as they are in `out`; without `out` they
+    are not initialised."""
     M, n = _dims("X", X, 2)
     E, d, _ = _dims("W", W, 3)
     dev = torch.cuda.current_device()
@@ -371,7 +373,9 @@ def grouped_linear(X, offsets, W, out=None):
 
 
 def grouped_linear_dx(dY, offsets, W, out=None):
-    """The gradient of grouped_linear's X: dX [M, n] of dY [M, d] and W [E, d, n]."""
+    """The gradient of grouped_linear's X: dX [M, n] of dY [M, d] and W [E, d, n].  Rows in no
+    group are left as they are in `out` (their gradient is zero: clear them there); without
+    `out` they are not initialised."""
     M, d = _dims("dY", dY, 2)
     E, _, n = _dims("W", W, 3)
     dev = torch.cuda.current_device()
@@ -460,6 +464,7 @@ def clip_grad_norm(grads, max_norm, out=None):
     """Scales a list of gradients (bf16, fp16, fp32) by min(1, max_norm / (norm + 1e-6)), norm
     being the 2-norm over all of them, in place or into `out` (tensors of the same sizes and
     types), and returns the norm as a device tensor [1] (fp32); nothing waits for the GPU.
+    Tensors are contiguous, on the current device, and start at multiples of 16 bytes.
     Ranks that each hold a part call grad_sumsq, add their sums and call grad_clip."""
     dev, grads = torch.cuda.current_device(), _tensors("grads", grads)
     a = _pointers("grads", grads, dev), _numels(grads), _types("grads", grads)
