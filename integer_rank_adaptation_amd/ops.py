@@ -3,9 +3,8 @@ memory only) and run one IntLoRA step through libintlora.so.  No arithmetic of t
 method happens here."""
 from __future__ import annotations
 
-import array
 import ctypes
-import operator
+import importlib
 
 import torch
 
@@ -403,41 +402,26 @@ def grouped_linear_dw(dY, X, offsets, dtype=None, out=None):
 
 
 # ---------------------------------------------------------------- gradient norm, clipping
-# (lists of hundreds of tensors: the checks go over the whole list at a time)
-def _host(ctype, code, values):
-    """A C array of the values (array.array converts them in half of ctypes' time)."""
-    a = array.array(code, values)
-    return (ctype * len(a)).from_buffer(a) if a else (ctype * 0)()
+_tensor_list = None
 
 
-def _tensors(name, ts):
-    """A list of them: an iterator could be gone over only once."""
+def _read(name, ts, dev):
+    """Addresses, element counts and types of contiguous bf16, fp16 or fp32 tensors on device
+    `dev` as C arrays, read in one pass in compiled code."""
+    global _tensor_list
     if isinstance(ts, torch.Tensor):
         raise ValueError(f"{name}: expected a list of tensors")
-    return list(ts)
-
-
-def _pointers(name, ts, dev):
-    if ts and (set(map(torch.Tensor.get_device, ts)) != {dev} or not all(map(torch.Tensor.is_contiguous, ts))):
-        raise ValueError(f"{name}: expected contiguous tensors on the current device")
-    return _host(ctypes.c_void_p, "Q", map(torch.Tensor.data_ptr, ts))
-
-
-_dtype = operator.attrgetter("dtype")
-
-
-def _types(name, ts):
-    try:
-        one = set(map(_dtype, ts))
-        if len(one) == 1:
-            return _host(ctypes.c_int32, "i", [_FLOAT[one.pop()]] * len(ts))
-        return _host(ctypes.c_int32, "i", map(_FLOAT.__getitem__, map(_dtype, ts)))
-    except KeyError as e:
-        raise ValueError(f"{name}: expected bf16, fp16 or fp32 tensors, got {e.args[0]}") from None
-
-
-def _numels(ts):
-    return _host(ctypes.c_int64, "q", map(torch.Tensor.numel, ts))
+    if _tensor_list is None:
+        try:
+            _tensor_list = importlib.import_module("._tensor_list", __package__)
+        except ImportError as e:
+            raise RuntimeError(f"_tensor_list.so does not load ({e}): build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+    ts = list(ts)
+    n = len(ts)
+    ptrs, numel, types = _tensor_list.read(name, ts, dev)
+    return ((ctypes.c_void_p * n).from_buffer_copy(ptrs), (ctypes.c_int64 * n).from_buffer_copy(numel),
+            (ctypes.c_int32 * n).from_buffer_copy(types))
 
 
 def _sumsq(ptrs, numel, types, dev):
@@ -448,12 +432,11 @@ def _sumsq(ptrs, numel, types, dev):
     return ws
 
 
-def _clip(ptrs, numel, types, grads, sumsq, max_norm, out, dev):
+def _clip(ptrs, numel, types, sumsq, max_norm, out, dev):
     outs = ptrs
     if out is not None:
-        out = _tensors("out", out)
-        outs = _pointers("out", out, dev)
-        if list(map(torch.Tensor.numel, out)) != list(numel) or list(map(_dtype, out)) != list(map(_dtype, grads)):
+        outs, n, t = _read("out", out, dev)
+        if bytes(n) != bytes(numel) or bytes(t) != bytes(types):
             raise ValueError("out: expected tensors of the gradients' sizes and types")
     norm = torch.empty(1, dtype=torch.float32, device=dev)
     B.intlora_grad_clip(ptrs, outs, numel, types, sumsq, max_norm, norm)
@@ -466,20 +449,20 @@ def clip_grad_norm(grads, max_norm, out=None):
     types), and returns the norm as a device tensor [1] (fp32); nothing waits for the GPU.
     Tensors are contiguous, on the current device, and start at multiples of 16 bytes.
     Ranks that each hold a part call grad_sumsq, add their sums and call grad_clip."""
-    dev, grads = torch.cuda.current_device(), _tensors("grads", grads)
-    a = _pointers("grads", grads, dev), _numels(grads), _types("grads", grads)
+    dev = torch.cuda.current_device()
+    a = _read("grads", grads, dev)
     ws = _sumsq(*a, dev)
-    return _clip(*a, grads, ws.data_ptr(), max_norm, out, dev)
+    return _clip(*a, ws.data_ptr(), max_norm, out, dev)
 
 
 def grad_sumsq(grads):
     """The sum of all squared gradients, a device tensor [1] (fp64)."""
-    dev, grads = torch.cuda.current_device(), _tensors("grads", grads)
-    return _sumsq(_pointers("grads", grads, dev), _numels(grads), _types("grads", grads), dev)[:1]
+    dev = torch.cuda.current_device()
+    return _sumsq(*_read("grads", grads, dev), dev)[:1]
 
 
 def grad_clip(grads, sumsq, max_norm, out=None):
     """The second half of clip_grad_norm, from a sum of squares (fp64 [1]) over all ranks."""
-    dev, grads = torch.cuda.current_device(), _tensors("grads", grads)
-    _want("sumsq", sumsq, (1,), (torch.float64,), dev)
-    return _clip(_pointers("grads", grads, dev), _numels(grads), _types("grads", grads), grads, sumsq, max_norm, out, dev)
+    dev = torch.cuda.current_device()
+    a = _read("grads", grads, dev)
+    return _clip(*a, _want("sumsq", sumsq, (1,), (torch.float64,), dev), max_norm, out, dev)
