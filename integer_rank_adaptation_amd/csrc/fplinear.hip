@@ -244,8 +244,8 @@ __device__ __forceinline__ int xcd_slot(int b, int n) {
 // a 256 x 256 tile takes about 1.7 us, its matrix instructions alone 1.0 and its direct loads alone
 // 1.1 (64 KB per compute unit through L2).  256 x 256 x 8 waves because the bytes loaded per
 // product fall with the tile's side and the sums of 64 x 128 outputs are half of a wave's
-// registers.  8192^3: 8 bits 423 us (2.60 PFLOP/s), bf16 forward 821, dX 844, dW 834 us (1.34,
-// 1.30, 1.32 PFLOP/s); the matrix cores are busy 54 to 67 % of the time.
+// registers.  8192^3: 8 bits 433 us (2.54 PFLOP/s), bf16 forward 836, dX 867, dW 857 us (1.32,
+// 1.27, 1.28 PFLOP/s); the matrix cores are busy 54 to 67 % of the time.
 template <int TY_, int LAY_, int BM_, int BN_, int WM_, int WN_, int ST_, int KS_ = 1>
 struct Tile {
   static constexpr int TY = TY_, LAY = LAY_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_, KS = KS_;
@@ -827,9 +827,9 @@ hipError_t launch_gemm(const GemmArgs& a, int64_t blocks, hipStream_t st) {
 // x 256 bytes.  The grid is persistent and the runs of a wave's consecutive tiles are one
 // stream, so the memory is kept busy across a tile's end.  (Fragments loaded straight into
 // registers take 16 bytes from each of 16 rows per 16 lanes: 16-token products then streamed
-// 3 TB/s.)  Bound by memory: 14336 x 4096 in 8 bits 14.2 us for 1 token (4.1 TB/s), 15.5 for 16,
-// 19.0 for 32; bf16 experts of 4096 x 2048, 16 tokens 25.1 us (4.7 TB/s); 4096 x 4096 in 8 bits,
-// 1 token 6.2 us, where launch and first loads count.
+// 3 TB/s.)  Bound by memory: 14336 x 4096 in 8 bits 13.1 us for 1 token (4.5 TB/s), 13.4 for 16,
+// 15.2 for 32; eight bf16 experts of 4096 x 2048, 2 tokens each 25.4 us (5.3 TB/s); 4096 x 4096 in
+// 8 bits, 1 token 6.3 us, where launch and first loads count.
 template <int TY_, int TT_>
 struct Few {
   static constexpr int TY = TY_, TT = TT_;
@@ -1053,8 +1053,8 @@ hipError_t launch_few_tt(const GemmArgs& a, hipStream_t st) {
   const int64_t groups = a.E < a.T ? a.E : a.T;
   const int64_t tiles = ((int64_t)a.cols + 15) / 16 * ((a.T + 16 * TT - 1) / (16 * TT) + groups - 1);
   // All waves of a block on one tile, but fewer where a wave would have less than two runs of it
-  // and there are tiles enough without (64 experts of 2048 x 1024, 64 rows in 8 bits: 20 us, with
-  // all eight waves on a tile 31; 14336 x 1024, 16 rows: 6.9 against 7.3).
+  // and there are tiles enough without (64 experts of 2048 x 1024, a row each in 8 bits: 29 us,
+  // with all eight waves on a tile 48; 14336 x 1024, 16 rows: 8.6 against 9.5).
   int ks = C::WAVES;
   const int64_t runs = ((int64_t)a.kdim * (TY == T_FP8 ? 1 : 2) + 255) / 256;
   while (ks > 1 && runs < 2 * ks && tiles * ks >= 2 * (int64_t)a.cus * C::WAVES) ks /= 2;
@@ -1152,7 +1152,7 @@ hipError_t run_gemm(GemmArgs a, hipStream_t st) {
   // two (dX of 8192 x 4096 x 2048 in 8 groups 158 us against 165) and two sets of waves (166
   // against 170).  More is two blocks to a unit (half a round, 4096 tokens, contraction 2048: 95 us
   // against 105 with four stages and so one block).  Where only the device knows how much is left,
-  // both are launched and one of them finds no work (3 us).
+  // both are launched and one of them finds no work (4.5 to 4.8 us).
   const bool sure = LAY == L_TN || a.offsets == nullptr;
   const int64_t most = ((int64_t)(LAY == L_TN ? kTailShareDw : kTailShare) * a.cus - 1) / 256;
   const int64_t quarter = a.cus / 4, left = units % a.cus;
@@ -1236,7 +1236,7 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], uint32_t byte) {
 
 // Activations: 16 lanes take one block of 1 x 128 (8 elements each); the largest magnitude
 // goes round the 16 lanes as integer bits, so a NaN wins.  Bound by memory: 8192 x 14336 bf16
-// 65 us, 5.4 TB/s (two or four blocks per 16 lanes with their loads together: the same or
+// 64 us, 5.5 TB/s (two or four blocks per 16 lanes with their loads together: the same or
 // slower, and 0.3 to 1.4 us more at 64 x 4096).
 template <int TI>
 __global__ void __launch_bounds__(256) k_fp8_act(uint32_t units, uint32_t n, uint32_t nb, uint32_t lds,
@@ -1262,7 +1262,7 @@ __global__ void __launch_bounds__(256) k_fp8_act(uint32_t units, uint32_t n, uin
 
 // Weights: one block of 128 x 128 per workgroup, and, when asked for, the same codes
 // transposed (through LDS) for the input gradient's product.  Bound by memory: 14336 x 4096 bf16
-// 32 us, 5.6 TB/s; with the transpose 39 us, 6.0 TB/s.
+// 35 us, 5.0 TB/s; with the transpose 44 us, 5.3 TB/s.
 template <int TI>
 __global__ void __launch_bounds__(256) k_fp8_weight(int d, int n, int lds, int lds_t, const void* __restrict__ W,
                                                     uint8_t* __restrict__ wq, uint8_t* __restrict__ sw,

@@ -117,7 +117,7 @@ __device__ __forceinline__ double wave_sum(double s) {
   return s;
 }
 
-// 168 M elements of fp32 in 448 tensors: 4 launches of 38 us, 4.4 TB/s (part of it from the
+// 168 M elements of fp32 in 448 tensors: 4 launches of 37 us, 4.5 TB/s (part of it from the
 // last-level cache); the scaling pass 62 us each, 5.4 TB/s read and written.
 __global__ void __launch_bounds__(kThreads) k_grad_sumsq(const Table t, double* __restrict__ partial) {
   __shared__ double w[4];
@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(kThreads) k_grad_sumsq(const Table t, double* 
 }
 
 // Small lists: one block takes all chunks, in order, and writes the sum itself, one launch less
-// (a call on 16 chunks 16.0 us, of 17, in two launches, 18.4; on 24 chunks 20.0; alone this kernel
-// takes 6.1 us for 12 tensors of 56 k elements, the other two 4.2 and 1.8).
+// (a call on 8 chunks 13.2 us, on 16 16.0, on 17, in two launches, 16.2; alone this kernel takes 6.0
+// us for 12 tensors of 56 k elements, the other two 4.2 and 1.8).
 __global__ void __launch_bounds__(1024) k_grad_sumsq_small(const Table t, double* __restrict__ sumsq) {
   __shared__ double w[16];
   const int sub = threadIdx.x >> 8;  // four chunks at a time
