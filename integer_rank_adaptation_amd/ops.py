@@ -405,19 +405,24 @@ def grouped_linear_dw(dY, X, offsets, dtype=None, out=None):
 _tensor_list = None
 
 
-def _read(name, ts, dev):
-    """Addresses, element counts and types of contiguous bf16, fp16 or fp32 tensors on device
-    `dev` as C arrays, read in one pass in compiled code."""
-    global _tensor_list
+def _tensors(name, ts):
+    """A list of them.  The call holds it until its kernels are enqueued: what an iterator made on
+    the way may have no other owner, and its memory could become the workspace."""
     if isinstance(ts, torch.Tensor):
         raise ValueError(f"{name}: expected a list of tensors")
+    return list(ts)
+
+
+def _read(name, ts, dev):
+    """Addresses, element counts and types of a list of contiguous bf16, fp16 or fp32 tensors on
+    device `dev` as C arrays, read in one pass in compiled code."""
+    global _tensor_list
     if _tensor_list is None:
         try:
             _tensor_list = importlib.import_module("._tensor_list", __package__)
         except ImportError as e:
             raise RuntimeError(f"_tensor_list.so does not load ({e}): build it first "
                                "(python -c 'import __graft_entry__ as g; g.build()')") from e
-    ts = list(ts)
     n = len(ts)
     ptrs, numel, types = _tensor_list.read(name, ts, dev)
     return ((ctypes.c_void_p * n).from_buffer_copy(ptrs), (ctypes.c_int64 * n).from_buffer_copy(numel),
@@ -435,6 +440,7 @@ def _sumsq(ptrs, numel, types, dev):
 def _clip(ptrs, numel, types, sumsq, max_norm, out, dev):
     outs = ptrs
     if out is not None:
+        out = _tensors("out", out)
         outs, n, t = _read("out", out, dev)
         if bytes(n) != bytes(numel) or bytes(t) != bytes(types):
             raise ValueError("out: expected tensors of the gradients' sizes and types")
@@ -449,7 +455,7 @@ def clip_grad_norm(grads, max_norm, out=None):
     types), and returns the norm as a device tensor [1] (fp32); nothing waits for the GPU.
     Tensors are contiguous, on the current device, and start at multiples of 16 bytes.
     Ranks that each hold a part call grad_sumsq, add their sums and call grad_clip."""
-    dev = torch.cuda.current_device()
+    dev, grads = torch.cuda.current_device(), _tensors("grads", grads)
     a = _read("grads", grads, dev)
     ws = _sumsq(*a, dev)
     return _clip(*a, ws.data_ptr(), max_norm, out, dev)
@@ -457,12 +463,12 @@ def clip_grad_norm(grads, max_norm, out=None):
 
 def grad_sumsq(grads):
     """The sum of all squared gradients, a device tensor [1] (fp64)."""
-    dev = torch.cuda.current_device()
+    dev, grads = torch.cuda.current_device(), _tensors("grads", grads)
     return _sumsq(*_read("grads", grads, dev), dev)[:1]
 
 
 def grad_clip(grads, sumsq, max_norm, out=None):
     """The second half of clip_grad_norm, from a sum of squares (fp64 [1]) over all ranks."""
-    dev = torch.cuda.current_device()
+    dev, grads = torch.cuda.current_device(), _tensors("grads", grads)
     a = _read("grads", grads, dev)
     return _clip(*a, _want("sumsq", sumsq, (1,), (torch.float64,), dev), max_norm, out, dev)

@@ -1,6 +1,7 @@
 """Lists of gradients are read in one compiled pass (CPU: the host tensors' device is -1; GPU: the
 calls on top of it)."""
 import ctypes
+import weakref
 
 import pytest
 import torch
@@ -32,7 +33,7 @@ def test_addresses_sizes_and_types():
     ptrs, numel, types = ops._read("grads", ts, -1)
     assert list(numel) == [t.numel() for t in ts] and list(types) == [CODES[t.dtype] for t in ts]
     assert [p or 0 for p in ptrs] == [t.data_ptr() for t in ts]
-    assert isinstance(ptrs, ctypes.Array) and ops._read("grads", iter(ts), -1)[1][:] == numel[:]
+    assert isinstance(ptrs, ctypes.Array) and ops._tensors("grads", iter(ts)) == ts
     assert [len(a) for a in ops._read("grads", [], -1)] == [0, 0, 0]
 
 
@@ -57,10 +58,47 @@ def test_refusals(bad, error, text):
         with pytest.raises(error, match=text):
             ops._read("grads", ts, -1)
     with pytest.raises(ValueError, match="grads: expected a list"):
-        ops._read("grads", torch.zeros(2, 2), -1)
+        ops._tensors("grads", torch.zeros(2, 2))
     for t in (torch.zeros(2), torch.zeros(2, device="meta")):  # on no GPU
         with pytest.raises(ValueError, match="out: expected contiguous tensors on the current device"):
             ops._read("out", [t], 0)
+
+
+def test_tensors_of_an_iterator_live_until_the_call_is_enqueued(monkeypatch):
+    """Tensors that only the iterator made: their memory may not go back (and become the
+    workspace) before the kernels that read them are enqueued."""
+    made, seen = [], []
+
+    def temporaries():
+        for i in range(3):
+            t = torch.ones(4 + i)
+            made.append(weakref.ref(t))
+            yield t
+
+    def sumsq(ptrs, numel, types, dev):
+        seen.append([r() is not None for r in made])
+        return torch.zeros(1, dtype=torch.float64)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    monkeypatch.setattr(ops, "_sumsq", sumsq)
+    ops.grad_sumsq(temporaries())
+    monkeypatch.setattr(ops, "_clip", lambda *a: seen.append([r() is not None for r in made]))
+    ops.clip_grad_norm(temporaries(), 1.0)
+    assert seen == [[True] * 3, [False] * 3 + [True] * 3, [False] * 3 + [True] * 3]
+
+
+@pytest.mark.gpu
+def test_temporary_gradients_and_outputs():
+    gs = [torch.full((1 << 16,), float(i + 1), device="cuda") for i in range(8)]
+    total = (1 << 16) * sum((2.0 * (i + 1)) ** 2 for i in range(8))
+    out = [torch.zeros_like(g) for g in gs]
+    for _ in range(3):
+        norm = ops.clip_grad_norm((2 * g for g in gs), 1.0, out=(o.view(-1) for o in out))
+        s = ops.grad_sumsq(2 * g for g in gs)
+        assert float(s) == total and abs(float(norm) - total**0.5) <= total**0.5 * 2.0**-23
+        for i, o in enumerate(out):
+            want = 2.0 * (i + 1) / (total**0.5 + 1e-6)  # the factor and the product are rounded to binary32
+            assert (o.double() - want).abs().max() <= want * 2.0**-23 * 1.001
 
 
 @pytest.mark.gpu
