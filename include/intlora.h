@@ -425,6 +425,32 @@ int intlora_grouped_linear_dx(int64_t M, int64_t E, int64_t d, int64_t n, int dt
 int intlora_grouped_linear_dw(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype, const void* dY,
                               const void* X, const int64_t* offsets, void* dW, void* stream);
 
+/* Low-rank adapters of many requests beside a shared layer, kept apart from its weight (where a
+ * merge would need a weight per adapter).  Row t of a batch belongs to adapter a = index[t] of L
+ * (int32 on the device; rows whose entry is outside [0, L) have none).  A: L x d x r, B: L x r x n,
+ * X, base, Y of one type (dtype INTLORA_BF16 / _FP16), scale: [L] fp32.
+ *   Y[t, :] = base[t, :] + scale_a A_a (B_a X[t, :]),  Y[t, :] = base[t, :] without an adapter.
+ * base: M x d, the output of any layer (intlora_linear_fwd, intlora_fp8_linear_fwd, ...), or NULL
+ * (zeros); Y may be base (in place), and then rows without an adapter are not touched.  Sums are
+ * binary32 in an order fixed by the sizes; the term B_a x keeps at least 16 significant bits on
+ * the way; one rounding at the end.  Rows of one adapter may lie anywhere; where they follow each
+ * other its factors are read once per 32 rows.  r in [1, 128], d and n multiples of 8 and
+ * <= 2^20, L <= 4096, M < 2^31.  Workspace (of both calls): intlora_adapters_ws_bytes. */
+size_t intlora_adapters_ws_bytes(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, int grads);
+int intlora_adapters_fwd(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, int dtype, const void* base,
+                         const void* X, const int32_t* index, const void* A, const void* B, const float* scale, void* Y,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradients, with dH[t, :] = scale_a A_a^T dY[t, :]:
+ *   dX[t, :] = base[t, :] + B_a^T dH[t, :] (base: the shared layer's dX, or NULL; may be dX; dX may be
+ *   NULL), dA_a = scale_a sum_t dY[t, :] (B_a X[t, :])^T, dB_a = sum_t dH[t, :] X[t, :]^T, both zeros
+ *   for an adapter without rows, in dtype or (out_dtype) INTLORA_FP32.
+ * The same conventions; B_a x and dH keep binary32's 24 bits in dA and dB. */
+int intlora_adapters_grad(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, int dtype, int out_dtype,
+                          const void* dY, const void* X, const int32_t* index, const void* A, const void* B,
+                          const float* scale, const void* base, void* dX, void* dA, void* dB, void* ws, size_t ws_bytes,
+                          void* stream);
+
 /* Global gradient norm and clipping over a list of tensors (the next call after
  * intlora_ste_backward has filled dA and dB of every layer).  grads, out, numel and dtype are
  * HOST arrays of `count` entries (device pointers, 16-byte aligned; element counts >= 0;

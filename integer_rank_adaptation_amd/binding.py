@@ -84,6 +84,11 @@ _SIG = {
     "intlora_grouped_linear_fwd": (_INT, [_I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P]),
     "intlora_grouped_linear_dx": (_INT, [_I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P]),
     "intlora_grouped_linear_dw": (_INT, [_I64, _I64, _I64, _I64, _INT, _INT, _P, _P, _P, _P, _P]),
+    "intlora_adapters_ws_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I64, _INT]),
+    "intlora_adapters_fwd": (_INT, [_I64, _I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _P, _P, _P,
+                                    ctypes.c_size_t, _P]),
+    "intlora_adapters_grad": (_INT, [_I64, _I64, _I64, _I64, _I64, _INT, _INT, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                     _P, ctypes.c_size_t, _P]),
     "intlora_grad_ws_bytes": (ctypes.c_size_t, [_I64, _P]),
     "intlora_grad_sumsq": (_INT, [_I64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "intlora_grad_clip": (_INT, [_I64, _P, _P, _P, _P, _P, ctypes.c_double, _P, _P]),
@@ -296,6 +301,29 @@ def intlora_grouped_linear_dw(M: int, E: int, d: int, n: int, dtype: int, out_dt
                               stream=None):
     _check(lib().intlora_grouped_linear_dw(M, E, d, n, dtype, out_dtype, _ptr(dY), _ptr(X), _ptr(offsets), _ptr(dW),
                                            _stream(stream)), "intlora_grouped_linear_dw")
+
+
+def intlora_adapters_ws_bytes(M: int, L: int, d: int, n: int, r: int, grads: bool) -> int:
+    return int(lib().intlora_adapters_ws_bytes(M, L, d, n, r, int(grads)))
+
+
+def _ws(ws, ws_bytes):
+    """Address and size of a workspace: a tensor, or an address and its bytes."""
+    return _ptr(ws), ws_bytes if ws_bytes is not None else 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def intlora_adapters_fwd(M: int, L: int, d: int, n: int, r: int, dtype: int, base, X, index, A, B, scale, Y, ws,
+                         stream=None, ws_bytes=None):
+    _check(lib().intlora_adapters_fwd(M, L, d, n, r, dtype, _ptr(base), _ptr(X), _ptr(index), _ptr(A), _ptr(B),
+                                      _ptr(scale), _ptr(Y), *_ws(ws, ws_bytes), _stream(stream)),
+           "intlora_adapters_fwd")
+
+
+def intlora_adapters_grad(M: int, L: int, d: int, n: int, r: int, dtype: int, out_dtype: int, dY, X, index, A, B,
+                          scale, base, dX, dA, dB, ws, stream=None, ws_bytes=None):
+    _check(lib().intlora_adapters_grad(M, L, d, n, r, dtype, out_dtype, _ptr(dY), _ptr(X), _ptr(index), _ptr(A),
+                                       _ptr(B), _ptr(scale), _ptr(base), _ptr(dX), _ptr(dA), _ptr(dB),
+                                       *_ws(ws, ws_bytes), _stream(stream)), "intlora_adapters_grad")
 
 
 def intlora_grad_ws_bytes(numel) -> int:

@@ -360,6 +360,24 @@ int fp8_linear(const char* what, int64_t M, int64_t E, int64_t d, int64_t n, con
                        what);
 }
 
+constexpr int64_t kMaxAdapters = 4096;
+
+int check_adapters(const intlora::AdapterArgs& a, const char* what) {
+  int s = check_dtype(a.dtype, false, what);
+  if (s) return s;
+  if (a.out_dtype != a.dtype && a.out_dtype != INTLORA_FP32)
+    return fail(INTLORA_EINVAL, "%s: out_dtype must be dtype or INTLORA_FP32 (got %d)", what, a.out_dtype);
+  if (a.r < 1 || a.r > 128) return fail(INTLORA_EINVAL, "%s: rank r must be in [1, 128] (got %lld)", what, (long long)a.r);
+  if (a.L < 1 || a.L > kMaxAdapters)
+    return fail(INTLORA_ESHAPE, "%s: L must be in [1, 4096] (got %lld)", what, (long long)a.L);
+  if (a.M < 0 || a.M >= kMaxDim - 256 || a.d < 8 || a.d > kMaxFeatures || a.n < 8 || a.n > kMaxFeatures ||
+      a.d % 8 != 0 || a.n % 8 != 0)
+    return fail(INTLORA_ESHAPE, "%s: bad shape M=%lld d=%lld n=%lld (d, n multiples of 8, <= 2^20)", what,
+                (long long)a.M, (long long)a.d, (long long)a.n);
+  if (!intlora::adapters_fit(a.M, a.d, a.n, a.r)) return fail(INTLORA_ESHAPE, "%s: too many tiles", what);
+  return INTLORA_OK;
+}
+
 int check_grads(int64_t count, const void* const* grads, const int64_t* numel, const int32_t* dtype,
                 const char* what) {
   if (count < 0 || count > kMaxGrads)
@@ -907,6 +925,62 @@ int intlora_grouped_linear_dw(int64_t M, int64_t E, int64_t d, int64_t n, int dt
   if (d == 0) return ok();
   return run_grouped("grouped_linear_dw", intlora::kGroupedDw, M, E, d, n, dtype, out_dtype, dY, offsets, X, dW,
                      stream);
+}
+
+size_t intlora_adapters_ws_bytes(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, int grads) {
+  intlora::AdapterArgs a{};
+  a.M = M, a.L = L, a.d = d, a.n = n, a.r = r;
+  if (check_adapters(a, "adapters_ws_bytes")) return 0;
+  ok();
+  return intlora::adapters_ws_bytes(M, L, d, n, r, grads != 0);
+}
+
+int intlora_adapters_fwd(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, int dtype, const void* base,
+                         const void* X, const int32_t* index, const void* A, const void* B, const float* scale, void* Y,
+                         void* ws, size_t ws_bytes, void* stream) {
+  intlora::AdapterArgs a{};
+  a.M = M, a.L = L, a.d = d, a.n = n, a.r = r;
+  a.dtype = a.out_dtype = dtype;
+  a.X = X, a.A = A, a.B = B, a.index = index, a.scale = scale, a.base = base, a.Y = Y;
+  int s = check_adapters(a, "adapters_fwd");
+  if (s) return s;
+  if (M == 0) return ok();
+  if ((s = check_ptrs({X, index, A, B, scale, Y}, "adapters_fwd")) || (s = check_opt(base, "base"))) return s;
+  const size_t need = intlora::adapters_ws_bytes(M, L, d, n, r, false);
+  if ((s = check_ws(ws, ws_bytes, need))) return s;
+  if ((s = check_apart({{Y, 2 * M * d}, {ws, (int64_t)need}},
+                       {{base == Y ? nullptr : base, 2 * M * d}, {X, 2 * M * n}, {index, 4 * M}, {A, 2 * L * d * r},
+                        {B, 2 * L * r * n}, {scale, 4 * L}},
+                       "adapters_fwd")))
+    return s;
+  if ((s = ensure_device())) return s;
+  return launch_status(intlora::launch_adapters(a, ws, static_cast<hipStream_t>(stream)), "adapters_fwd");
+}
+
+int intlora_adapters_grad(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, int dtype, int out_dtype,
+                          const void* dY, const void* X, const int32_t* index, const void* A, const void* B,
+                          const float* scale, const void* base, void* dX, void* dA, void* dB, void* ws, size_t ws_bytes,
+                          void* stream) {
+  intlora::AdapterArgs a{};
+  a.M = M, a.L = L, a.d = d, a.n = n, a.r = r;
+  a.dtype = dtype, a.out_dtype = out_dtype;
+  a.X = X, a.dY = dY, a.A = A, a.B = B, a.index = index, a.scale = scale, a.base = base, a.Y = dX, a.dA = dA, a.dB = dB;
+  int s = check_adapters(a, "adapters_grad");
+  if (s) return s;
+  if (base && !dX) return fail(INTLORA_EINVAL, "adapters_grad: base without dX");
+  if (M > 0 && (s = check_ptrs({dY, X, index}, "adapters_grad"))) return s;  // without a row the gradients are zeros
+  if ((s = check_ptrs({A, B, scale, dA, dB}, "adapters_grad"))) return s;
+  if ((s = check_opt(base, "base")) || (s = check_opt(dX, "dX"))) return s;
+  const size_t need = intlora::adapters_ws_bytes(M, L, d, n, r, true);
+  if ((s = check_ws(ws, ws_bytes, need))) return s;
+  const int64_t eb = out_dtype == INTLORA_FP32 ? 4 : 2;
+  if ((s = check_apart({{dX, 2 * M * n}, {dA, eb * L * d * r}, {dB, eb * L * r * n}, {ws, (int64_t)need}},
+                       {{base == dX ? nullptr : base, 2 * M * n}, {dY, 2 * M * d}, {X, 2 * M * n}, {index, 4 * M},
+                        {A, 2 * L * d * r}, {B, 2 * L * r * n}, {scale, 4 * L}},
+                       "adapters_grad")))
+    return s;
+  if ((s = ensure_device())) return s;
+  return launch_status(intlora::launch_adapters_grad(a, ws, static_cast<hipStream_t>(stream)), "adapters_grad");
 }
 
 size_t intlora_grad_ws_bytes(int64_t count, const int64_t* numel) {

@@ -98,6 +98,21 @@ hipError_t launch_fp8_linear(int64_t M, int64_t E, int64_t d, int64_t n, const u
 // tokens: X (forward) or dY; other: W (forward, dX) or X (dW); out: Y, dX or dW.
 hipError_t launch_grouped(int direction, int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype,
                           const void* tokens, const int64_t* offsets, const void* other, void* out, hipStream_t st);
+// Adapters of many requests (adapters.hip).
+struct AdapterArgs {
+  int64_t M, L, d, n, r;
+  int dtype, out_dtype;  // out_dtype: of dA and dB
+  const void *X, *dY, *A, *B;
+  const int32_t* index;
+  const float* scale;
+  const void* base;  // of Y, NULL: zeros
+  void* Y;           // the output, or dX (NULL: not wanted)
+  void *dA, *dB;
+};
+bool adapters_fit(int64_t M, int64_t d, int64_t n, int64_t r);
+size_t adapters_ws_bytes(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads);
+hipError_t launch_adapters(const AdapterArgs& p, void* ws, hipStream_t st);
+hipError_t launch_adapters_grad(const AdapterArgs& p, void* ws, hipStream_t st);
 // Gradient norm and clipping (gradclip.hip); src, dst, numel, dtype are host arrays.
 size_t grad_ws_bytes(int64_t count, const int64_t* numel);
 hipError_t launch_grad_sumsq(int64_t count, const void* const* src, const int64_t* numel, const int32_t* dtype,

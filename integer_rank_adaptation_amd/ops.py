@@ -401,6 +401,62 @@ def grouped_linear_dw(dY, X, offsets, dtype=None, out=None):
     return dW
 
 
+# ---------------------------------------------------------------- adapters of many requests
+def _adapters(tokens, other, index, A, B, scale, dev):
+    """Sizes and addresses of an adapters call; tokens: X [M, n], other: dY [M, d] or None."""
+    L, d, r = _dims("A", A, 3)
+    n = _dims("B", B, 3)[2]
+    M, dt = _dims("X", tokens, 2)[0], tokens.dtype
+    p = [_want("X", tokens, (M, n), _HALF, dev), _want("index", index, (M,), (torch.int32,), dev),
+         _want("A", A, (L, d, r), (dt,), dev), _want("B", B, (L, r, n), (dt,), dev),
+         _want("scale", scale, (L,), (torch.float32,), dev)]
+    if other is not None:
+        p.insert(0, _want("dY", other, (M, d), (dt,), dev))
+    return M, L, d, n, r, p
+
+
+def _adapters_ws(M, L, d, n, r, grads, like):
+    size = B.intlora_adapters_ws_bytes(M, L, d, n, r, grads)
+    return torch.empty(max(size, 16), dtype=torch.uint8, device=like.device), size
+
+
+def adapters_linear(base, X, index, A, B_, scale, out=None):
+    """Y [M, d] = base [M, d] + the low-rank term scale_a A_a (B_a x_t) of each row's own adapter
+    a = index[t] (int32 [M]; rows with an entry outside [0, L) have none and keep base's values).
+    X [M, n], A [L, d, r], B [L, r, n] and base of one type (bf16 or fp16), scale [L] fp32; base:
+    the output of any layer, or None for the term alone.  out=base adds in place."""
+    dev = torch.cuda.current_device()
+    M, L, d, n, r, (x, i, a, b, s) = _adapters(X, None, index, A, B_, scale, dev)
+    p = None if base is None else _want("base", base, (M, d), (X.dtype,), dev)
+    Y, y = _output(out, (M, d), X.dtype, X, dev)
+    ws, size = _adapters_ws(M, L, d, n, r, False, X)
+    B.intlora_adapters_fwd(M, L, d, n, r, _FLOAT[X.dtype], p, x, i, a, b, s, y, ws.data_ptr(), ws_bytes=size)
+    return Y
+
+
+def adapters_linear_grad(dY, X, index, A, B_, scale, base=None, dtype=None, need_dx=True, out=None):
+    """The gradients of adapters_linear: (dX [M, n], dA [L, d, r], dB [L, r, n]) of dY [M, d], dX
+    with `base` (the shared layer's input gradient) added, or None without need_dx; dA and dB in
+    X's type or in fp32 (dtype), zeros for adapters without rows.  out: three tensors (the first
+    may be base, or None without need_dx)."""
+    dev = torch.cuda.current_device()
+    M, L, d, n, r, (g, x, i, a, b, s) = _adapters(X, dY, index, A, B_, scale, dev)
+    dtype = dtype or (X.dtype if out is None else out[1].dtype)
+    if dtype not in (X.dtype, torch.float32):
+        raise ValueError(f"dtype: expected {X.dtype} or torch.float32, got {dtype}")
+    if base is not None and not need_dx:
+        raise ValueError("base: without dX there is nothing to add it to")
+    p = None if base is None else _want("base", base, (M, n), (X.dtype,), dev)
+    o = (None, None, None) if out is None else out
+    dX, dx = _output(o[0], (M, n), X.dtype, X, dev) if need_dx else (None, None)
+    dA, da = _output(o[1], (L, d, r), dtype, X, dev)
+    dB, db = _output(o[2], (L, r, n), dtype, X, dev)
+    ws, size = _adapters_ws(M, L, d, n, r, True, X)
+    B.intlora_adapters_grad(M, L, d, n, r, _FLOAT[X.dtype], _FLOAT[dtype], g, x, i, a, b, s, p, dx, da, db,
+                            ws.data_ptr(), ws_bytes=size)
+    return dX, dA, dB
+
+
 # ---------------------------------------------------------------- gradient norm, clipping
 _tensor_list = None
 
