@@ -425,6 +425,37 @@ int intlora_grouped_linear_dx(int64_t M, int64_t E, int64_t d, int64_t n, int dt
 int intlora_grouped_linear_dw(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype, const void* dY,
                               const void* X, const int64_t* offsets, void* dW, void* stream);
 
+/* The weight gradient from X as intlora_fp8_quant_act saved it (xq, sx): dW as above of dY and of
+ * the numbers the codes stand for, in dY's type (exact where X had that type; a code past fp16's
+ * largest number counts as that).  n a multiple of 16.  Workspace: 2 M n bytes. */
+int intlora_grouped_linear_dw_fp8(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype, const void* dY,
+                                  const uint8_t* xq, const uint8_t* sx, const int64_t* offsets, void* dW, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* The numbers of intlora_fp8_quant_act's codes (M x n, dtype): code x 2^(byte - 127), rounded to
+ * the type; a code past fp16's largest number gives that number, the byte 255 NaN. */
+int intlora_fp8_dequant_act(int64_t M, int64_t n, int dtype, const uint8_t* xq, const uint8_t* sx, void* X,
+                            void* stream);
+
+/* Gated feed-forward layer (bf16 / fp16), dense or grouped by expert as above: W holds the gate's f
+ * rows and then the up projection's f rows of n columns, E x 2 f x n, and
+ *   [G | U][t, :] = W_e X[t, :],  H[t, :] = act(G[t, :]) U[t, :]
+ * in one pass: act INTLORA_SILU, g / (1 + e^-g), or INTLORA_GELU, g P(g) with the normal
+ * distribution function P.  H: M x f, formed from the binary32 sums with one rounding; GU: M x 2 f,
+ * both projections for the backward pass, or NULL.  f and n multiples of 8.  The down projection
+ * is intlora_grouped_linear_fwd on H. */
+enum { INTLORA_SILU = 0, INTLORA_GELU = 1 };
+int intlora_gated_linear_fwd(int64_t M, int64_t E, int64_t f, int64_t n, int dtype, int act, const void* X,
+                             const int64_t* offsets, const void* W, void* H, void* GU, void* stream);
+
+/* Its backward up to the products: dGU [M, 2 f] = [dH U act'(G) | dH act(G)], and H again (NULL: not
+ * wanted) for the down projection's weight gradient, of dH [M, f] and GU: 16-bit with sGU = NULL,
+ * or codes of M x 2 f numbers with their scale bytes sGU as intlora_fp8_quant_act makes them.  All
+ * M rows; binary32 inside.  Then dX = intlora_grouped_linear_dx(dGU, W) and dW =
+ * intlora_grouped_linear_dw(dGU, X) with d = 2 f. */
+int intlora_gated_linear_dgu(int64_t M, int64_t f, int dtype, int act, const void* dH, const void* GU,
+                             const uint8_t* sGU, void* dGU, void* H, void* stream);
+
 /* Low-rank adapters of many requests beside a shared layer, kept apart from its weight (where a
  * merge would need a weight per adapter).  Row t of a batch belongs to adapter a = index[t] of L
  * (int32 on the device; rows whose entry is outside [0, L) have none).  A: L x d x r, B: L x r x n,

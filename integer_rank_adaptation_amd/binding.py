@@ -21,6 +21,7 @@ INTLORA_AUX_LAPLACE, INTLORA_AUX_GAUSS, INTLORA_AUX_CAUCHY, INTLORA_AUX_STUDENT_
 INTLORA_OP_STATS_UMINMAX, INTLORA_OP_MERGE_MUL, INTLORA_OP_MERGE_SHIFT, INTLORA_OP_LINEAR, INTLORA_OP_BASE_QUANT = 1, 2, 3, 4, 5
 INTLORA_OP_MERGE_PTQ, INTLORA_OP_STE_BACKWARD = 6, 7
 INTLORA_BF16, INTLORA_FP16, INTLORA_FP32 = 0, 1, 2
+INTLORA_SILU, INTLORA_GELU = 0, 1
 
 
 class IntLoraError(RuntimeError):
@@ -84,6 +85,11 @@ _SIG = {
     "intlora_grouped_linear_fwd": (_INT, [_I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P]),
     "intlora_grouped_linear_dx": (_INT, [_I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P]),
     "intlora_grouped_linear_dw": (_INT, [_I64, _I64, _I64, _I64, _INT, _INT, _P, _P, _P, _P, _P]),
+    "intlora_grouped_linear_dw_fp8": (_INT, [_I64, _I64, _I64, _I64, _INT, _INT, _P, _P, _P, _P, _P, _P,
+                                             ctypes.c_size_t, _P]),
+    "intlora_fp8_dequant_act": (_INT, [_I64, _I64, _INT, _P, _P, _P, _P]),
+    "intlora_gated_linear_fwd": (_INT, [_I64, _I64, _I64, _I64, _INT, _INT, _P, _P, _P, _P, _P, _P]),
+    "intlora_gated_linear_dgu": (_INT, [_I64, _I64, _INT, _INT, _P, _P, _P, _P, _P, _P]),
     "intlora_adapters_ws_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I64, _INT]),
     "intlora_adapters_fwd": (_INT, [_I64, _I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _P, _P, _P,
                                     ctypes.c_size_t, _P]),
@@ -303,13 +309,36 @@ def intlora_grouped_linear_dw(M: int, E: int, d: int, n: int, dtype: int, out_dt
                                            _stream(stream)), "intlora_grouped_linear_dw")
 
 
-def intlora_adapters_ws_bytes(M: int, L: int, d: int, n: int, r: int, grads: bool) -> int:
-    return int(lib().intlora_adapters_ws_bytes(M, L, d, n, r, int(grads)))
-
-
 def _ws(ws, ws_bytes):
     """Address and size of a workspace: a tensor, or an address and its bytes."""
     return _ptr(ws), ws_bytes if ws_bytes is not None else 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def intlora_grouped_linear_dw_fp8(M: int, E: int, d: int, n: int, dtype: int, out_dtype: int, dY, xq, sx, offsets, dW,
+                                  ws, stream=None, ws_bytes=None):
+    _check(lib().intlora_grouped_linear_dw_fp8(M, E, d, n, dtype, out_dtype, _ptr(dY), _ptr(xq), _ptr(sx),
+                                               _ptr(offsets), _ptr(dW), *_ws(ws, ws_bytes), _stream(stream)),
+           "intlora_grouped_linear_dw_fp8")
+
+
+def intlora_fp8_dequant_act(M: int, n: int, dtype: int, xq, sx, X, stream=None):
+    _check(lib().intlora_fp8_dequant_act(M, n, dtype, _ptr(xq), _ptr(sx), _ptr(X), _stream(stream)),
+           "intlora_fp8_dequant_act")
+
+
+def intlora_gated_linear_fwd(M: int, E: int, f: int, n: int, dtype: int, act: int, X, offsets, W, H, GU=None,
+                             stream=None):
+    _check(lib().intlora_gated_linear_fwd(M, E, f, n, dtype, act, _ptr(X), _ptr(offsets), _ptr(W), _ptr(H), _ptr(GU),
+                                          _stream(stream)), "intlora_gated_linear_fwd")
+
+
+def intlora_gated_linear_dgu(M: int, f: int, dtype: int, act: int, dH, GU, sGU, dGU, H=None, stream=None):
+    _check(lib().intlora_gated_linear_dgu(M, f, dtype, act, _ptr(dH), _ptr(GU), _ptr(sGU), _ptr(dGU), _ptr(H),
+                                          _stream(stream)), "intlora_gated_linear_dgu")
+
+
+def intlora_adapters_ws_bytes(M: int, L: int, d: int, n: int, r: int, grads: bool) -> int:
+    return int(lib().intlora_adapters_ws_bytes(M, L, d, n, r, int(grads)))
 
 
 def intlora_adapters_fwd(M: int, L: int, d: int, n: int, r: int, dtype: int, base, X, index, A, B, scale, Y, ws,

@@ -17,7 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libintlora.so")
 TENSOR_LIST = os.path.join(HERE, "_tensor_list.so")
-SOURCES = ["capi.hip", "merge.hip", "linear.hip", "ste.hip", "fplinear.hip", "adapters.hip", "gradclip.hip"]
+SOURCES = ["capi.hip", "merge.hip", "linear.hip", "ste.hip", "fplinear.hip", "gated.hip", "adapters.hip", "gradclip.hip"]
 
 # -ffp-contract=off: no implicit multiply-add fusion (every fp32 step is the IEEE
 # operation written); packed fp32 instructions are disabled for all device code.

@@ -360,6 +360,11 @@ int fp8_linear(const char* what, int64_t M, int64_t E, int64_t d, int64_t n, con
                        what);
 }
 
+int check_act(int act, const char* what) {
+  if (act == INTLORA_SILU || act == INTLORA_GELU) return INTLORA_OK;
+  return fail(INTLORA_EINVAL, "%s: act must be INTLORA_SILU or INTLORA_GELU (got %d)", what, act);
+}
+
 constexpr int64_t kMaxAdapters = 4096;
 
 int check_adapters(const intlora::AdapterArgs& a, const char* what) {
@@ -925,6 +930,85 @@ int intlora_grouped_linear_dw(int64_t M, int64_t E, int64_t d, int64_t n, int dt
   if (d == 0) return ok();
   return run_grouped("grouped_linear_dw", intlora::kGroupedDw, M, E, d, n, dtype, out_dtype, dY, offsets, X, dW,
                      stream);
+}
+
+int intlora_grouped_linear_dw_fp8(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype, const void* dY,
+                                  const uint8_t* xq, const uint8_t* sx, const int64_t* offsets, void* dW, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  const char* what = "grouped_linear_dw_fp8";
+  int s = check_grouped(M, E, d, n, dtype, out_dtype, offsets, what);
+  if (s) return s;
+  if (n % 16 != 0) return fail(INTLORA_ESHAPE, "%s needs n a multiple of 16 (got %lld)", what, (long long)n);
+  if (d == 0) return ok();
+  if (M > 0 && (s = check_ptrs({dY, xq, sx}, what))) return s;
+  if ((s = check_ptrs({dW}, what))) return s;
+  if ((s = check_ws(ws, ws_bytes, (size_t)(2 * M * n)))) return s;
+  if ((s = check_apart({{dW, E * d * n * (out_dtype == INTLORA_FP32 ? 4 : 2)}, {ws, 2 * M * n}},
+                       {{dY, 2 * M * d}, {xq, M * n}, {sx, M * intlora::fp8_scale_stride(n)}, {offsets, 8 * (E + 1)}},
+                       what)))
+    return s;
+  if ((s = ensure_device())) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (M > 0 && (s = launch_status(intlora::launch_fp8_restore(M, n, dtype, xq, sx, ws, st), what))) return s;
+  return launch_status(intlora::launch_grouped(intlora::kGroupedDw, M, E, d, n, dtype, out_dtype, dY, offsets, ws, dW,
+                                               st),
+                       what);
+}
+
+int intlora_fp8_dequant_act(int64_t M, int64_t n, int dtype, const uint8_t* xq, const uint8_t* sx, void* X,
+                            void* stream) {
+  int s = check_dtype(dtype, true, "fp8_dequant_act");
+  if (s) return s;
+  if (M < 0 || M >= kMaxDim || n < 1 || n > kMaxFeatures || n % 16 != 0 || M * (n / 16) >= (int64_t(1) << 32) - 256)
+    return fail(INTLORA_ESHAPE, "fp8_dequant_act needs n a multiple of 16 and <= 2^20, M n < 2^36 (got M=%lld n=%lld)",
+                (long long)M, (long long)n);
+  if (M == 0) return ok();
+  if ((s = check_ptrs({xq, sx, X}, "fp8_dequant_act"))) return s;
+  if ((s = check_apart({{X, M * n * (dtype == INTLORA_FP32 ? 4 : 2)}},
+                       {{xq, M * n}, {sx, M * intlora::fp8_scale_stride(n)}}, "fp8_dequant_act")))
+    return s;
+  if ((s = ensure_device())) return s;
+  return launch_status(intlora::launch_fp8_restore(M, n, dtype, xq, sx, X, static_cast<hipStream_t>(stream)),
+                       "fp8_dequant_act");
+}
+
+int intlora_gated_linear_fwd(int64_t M, int64_t E, int64_t f, int64_t n, int dtype, int act, const void* X,
+                             const int64_t* offsets, const void* W, void* H, void* GU, void* stream) {
+  const char* what = "gated_linear_fwd";
+  int s = check_act(act, what);
+  if (s) return s;
+  if (f > kMaxFeatures / 2) return fail(INTLORA_ESHAPE, "%s: f must be <= 2^19 (got %lld)", what, (long long)f);
+  if ((s = check_grouped(M, E, f < 0 ? f : 2 * f, n, dtype, dtype, offsets, what))) return s;
+  if (f % 8 != 0) return fail(INTLORA_ESHAPE, "%s needs f a multiple of 8 (got %lld)", what, (long long)f);
+  if (M == 0 || f == 0) return ok();
+  if ((s = check_ptrs({X, W, H}, what)) || (s = check_opt(GU, "GU"))) return s;
+  if ((s = check_apart({{H, 2 * M * f}, {GU, 4 * M * f}},
+                       {{X, 2 * M * n}, {W, 4 * E * f * n}, {offsets, 8 * (E + 1)}}, what)))
+    return s;
+  if ((s = ensure_device())) return s;
+  return launch_status(intlora::launch_gated(M, E, f, n, dtype, act, X, offsets, W, H, GU,
+                                             static_cast<hipStream_t>(stream)),
+                       what);
+}
+
+int intlora_gated_linear_dgu(int64_t M, int64_t f, int dtype, int act, const void* dH, const void* GU,
+                             const uint8_t* sGU, void* dGU, void* H, void* stream) {
+  const char* what = "gated_linear_dgu";
+  int s = check_act(act, what);
+  if (s) return s;
+  if ((s = check_dtype(dtype, false, what))) return s;
+  if (M < 0 || M >= kMaxDim || f < 8 || f > kMaxFeatures / 2 || f % 8 != 0 || M * (f / 8) >= (int64_t(1) << 32) - 256)
+    return fail(INTLORA_ESHAPE, "%s needs f a multiple of 8 and <= 2^19, M f < 2^35 (got M=%lld f=%lld)", what,
+                (long long)M, (long long)f);
+  if (M == 0) return ok();
+  if ((s = check_ptrs({dH, GU, dGU}, what)) || (s = check_opt(sGU, "sGU")) || (s = check_opt(H, "H"))) return s;
+  if ((s = check_apart({{dGU, 4 * M * f}, {H, 2 * M * f}},
+                       {{dH, 2 * M * f}, {GU, (sGU ? 2 : 4) * M * f}, {sGU, M * intlora::fp8_scale_stride(2 * f)}}, what)))
+    return s;
+  if ((s = ensure_device())) return s;
+  return launch_status(intlora::launch_gated_dgu(M, f, dtype, act, dH, GU, sGU, dGU, H,
+                                                 static_cast<hipStream_t>(stream)),
+                       what);
 }
 
 size_t intlora_adapters_ws_bytes(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, int grads) {

@@ -98,6 +98,14 @@ hipError_t launch_fp8_linear(int64_t M, int64_t E, int64_t d, int64_t n, const u
 // tokens: X (forward) or dY; other: W (forward, dX) or X (dW); out: Y, dX or dW.
 hipError_t launch_grouped(int direction, int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype,
                           const void* tokens, const int64_t* offsets, const void* other, void* out, hipStream_t st);
+// Gated layers and saved activations (gated.hip).  act: INTLORA_SILU / _GELU; GU: [G | U], NULL
+// where it is not wanted; sGU: scale bytes of GU's codes, NULL where GU is 16-bit.
+hipError_t launch_gated(int64_t M, int64_t E, int64_t f, int64_t n, int dtype, int act, const void* X,
+                        const int64_t* offsets, const void* W, void* H, void* GU, hipStream_t st);
+hipError_t launch_gated_dgu(int64_t M, int64_t f, int dtype, int act, const void* dH, const void* GU, const uint8_t* sGU,
+                            void* dGU, void* H, hipStream_t st);
+hipError_t launch_fp8_restore(int64_t M, int64_t n, int dtype, const uint8_t* xq, const uint8_t* sx, void* X,
+                              hipStream_t st);
 // Adapters of many requests (adapters.hip).
 struct AdapterArgs {
   int64_t M, L, d, n, r;

@@ -387,18 +387,89 @@ def grouped_linear_dx(dY, offsets, W, out=None):
 def grouped_linear_dw(dY, X, offsets, dtype=None, out=None):
     """The gradient of grouped_linear's W: dW [E, d, n] of dY [M, d] and X [M, n], in their type
     or in fp32 (dtype).  With offsets = None one group of all rows: dW [1, d, n], whose fp32
-    form is the G of ste_backward."""
+    form is the G of ste_backward.  X may be the pair (xq, sx) that fp8_quant_act saved of it."""
     M, d = _dims("dY", dY, 2)
+    saved = not isinstance(X, torch.Tensor)
+    if saved:
+        X, sx = X
     n = _dims("X", X, 2)[1]
     dev = torch.cuda.current_device()
-    y, x = _want("dY", dY, (M, d), _HALF, dev), _want("X", X, (M, n), (dY.dtype,), dev)
+    y, x = _want("dY", dY, (M, d), _HALF, dev), _want("X", X, (M, n), _E4M3 if saved else (dY.dtype,), dev)
     E = 1 if offsets is None else offsets.numel() - 1
     dtype = dtype or (dY.dtype if out is None else out.dtype)
     if dtype not in (dY.dtype, torch.float32):
         raise ValueError(f"dtype: expected {dY.dtype} or torch.float32, got {dtype}")
+    o = _offsets(offsets, E, dev)
     dW, w = _output(out, (E, d, n), dtype, dY, dev)
-    B.intlora_grouped_linear_dw(M, E, d, n, _FLOAT[dY.dtype], _FLOAT[dtype], y, x, _offsets(offsets, E, dev), w)
+    if saved:
+        s = _want("sx", sx, (M, fp8_scale_bytes(n)), _BYTES, dev)
+        ws = torch.empty((M, n), dtype=dY.dtype, device=dY.device)
+        B.intlora_grouped_linear_dw_fp8(M, E, d, n, _FLOAT[dY.dtype], _FLOAT[dtype], y, x, s, o, w, ws)
+    else:
+        B.intlora_grouped_linear_dw(M, E, d, n, _FLOAT[dY.dtype], _FLOAT[dtype], y, x, o, w)
     return dW
+
+
+def fp8_dequant_act(xq, sx, dtype, out=None):
+    """The numbers [M, n] (bf16, fp16 or fp32) of fp8_quant_act's codes and scale bytes."""
+    M, n = _dims("xq", xq, 2)
+    if dtype not in _FLOAT:
+        raise ValueError(f"dtype: expected {' or '.join(map(str, _FLOAT))}, got {dtype}")
+    dev = torch.cuda.current_device()
+    q, s = _want("xq", xq, (M, n), _E4M3, dev), _want("sx", sx, (M, fp8_scale_bytes(n)), _BYTES, dev)
+    X, x = _output(out, (M, n), dtype, xq, dev)
+    B.intlora_fp8_dequant_act(M, n, _FLOAT[dtype], q, s, x)
+    return X
+
+
+# ---------------------------------------------------------------- gated feed-forward layer
+_ACT = {"silu": B.INTLORA_SILU, "gelu": B.INTLORA_GELU}
+
+
+def _act(act):
+    if act not in _ACT:
+        raise ValueError(f"act: expected {' or '.join(_ACT)}, got {act!r}")
+    return _ACT[act]
+
+
+def gated_linear(X, offsets, W, act="silu", save=False, out=None):
+    """H [M, f] = act(G) * U with [G | U] = X W[e]^T for the rows of each group, X [M, n], W [E, 2f, n]
+    (bf16 or fp16; the gate's f rows first; offsets as grouped_linear, None with E = 1).  act:
+    "silu", or "gelu" by the normal distribution function.  With `save` also [G | U] as GU [M, 2f]
+    for gated_linear_dgu: (H, GU).  out: the tensor, or the pair.  Rows in no group are left as
+    they are in `out`; without `out` they are not initialised."""
+    M, n = _dims("X", X, 2)
+    E, d, _ = _dims("W", W, 3)
+    a, f, dt = _act(act), d // 2, X.dtype
+    dev = torch.cuda.current_device()
+    x, w = _want("X", X, (M, n), _HALF, dev), _want("W", W, (E, 2 * f, n), (dt,), dev)
+    o = _offsets(offsets, E, dev)
+    H, h = _output(out[0] if save and out is not None else out, (M, f), dt, X, dev)
+    GU, gu = _output(out[1] if out is not None else None, (M, 2 * f), dt, X, dev) if save else (None, None)
+    B.intlora_gated_linear_fwd(M, E, f, n, _FLOAT[dt], a, x, o, w, h, gu)
+    return (H, GU) if save else H
+
+
+def gated_linear_dgu(dH, GU, act="silu", save=True, out=None):
+    """The backward of act(G) * U: (dGU [M, 2f], H [M, f]) of dH [M, f] and of gated_linear's GU
+    [M, 2f], or of the pair (codes, scale bytes) that fp8_quant_act saved of it.  H is computed
+    again for the down projection's weight gradient (None without `save`).  grouped_linear_dx and
+    grouped_linear_dw take dGU on to the gradients of X and W.  out: the pair (H's ignored without
+    `save`).  All M rows, in groups or not."""
+    M, f = _dims("dH", dH, 2)
+    a, dt = _act(act), dH.dtype
+    dev = torch.cuda.current_device()
+    d = _want("dH", dH, (M, f), _HALF, dev)
+    s = None
+    if isinstance(GU, torch.Tensor):
+        g = _want("GU", GU, (M, 2 * f), (dt,), dev)
+    else:
+        q, sq = GU
+        g, s = _want("GU", q, (M, 2 * f), _E4M3, dev), _want("sGU", sq, (M, fp8_scale_bytes(2 * f)), _BYTES, dev)
+    dGU, o = _output(out[0] if out is not None else None, (M, 2 * f), dt, dH, dev)
+    H, h = _output(out[1] if out is not None else None, (M, f), dt, dH, dev) if save else (None, None)
+    B.intlora_gated_linear_dgu(M, f, _FLOAT[dt], a, d, g, s, o, h)
+    return dGU, H
 
 
 # ---------------------------------------------------------------- adapters of many requests
