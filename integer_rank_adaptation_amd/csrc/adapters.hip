@@ -94,42 +94,50 @@ struct Tile {
   }
 };
 
-struct DownArgs {
+// h = W_a x of one or two problems (h and dh: blockIdx.y).
+struct Down {
   const uint8_t* X;  // M x n
   const uint8_t* W;  // L x r x n
-  const int32_t* index;
   float* H;          // splits x M x rp
+  int n, splits;
+};
+struct DownArgs {
+  Down of[2];
+  const int32_t* index;
   int64_t M;
-  int L, n, r, rp;
-  int splits, per;   // columns per split (a multiple of 64)
-  int slots;         // 0: a wave takes all adapters of its tile in turn; else one wave per token of a tile of 16
+  int L, r, rp;
+  int slots;  // 0: a block takes all adapters of its tile in turn; else one block per token of a tile of 16
 };
 
-// h = W_a x.  A wave computes 16 TT tokens x 16 RT ranks over one split of the columns; lane l
-// holds token l % 16 and ranks 4 (l / 16) + 0 .. 3 of a tile.  Rows of other adapters read as zeros
-// and are not written.
+// A block computes 16 TT tokens x 16 RT ranks over one split of the columns: its eight waves take
+// runs of 64 columns in turn, and their sums meet in LDS, where each wave adds the eight parts of
+// a tile in order.  Lane l holds token l % 16 and ranks 4 (l / 16) + 0 .. 3 of a tile.  Rows of
+// other adapters read as zeros and are not written.
+constexpr int kDownWaves = 8;
+
 template <int TY, int TT, int RT>
-__global__ void __launch_bounds__(256) k_down(const DownArgs p) {
+__global__ void __launch_bounds__(64 * kDownWaves) k_down(const DownArgs p) {
+  constexpr int PASS = TT * RT > 8 ? 8 / TT : RT;  // rank tiles whose sums LDS holds at a time
+  __shared__ __attribute__((aligned(16))) float sums[kDownWaves][TT * PASS][256];
+  const Down& of = p.of[blockIdx.y];
   const int lane = threadIdx.x & 63, fr = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int groups = (p.rp + 16 * RT - 1) / (16 * RT);
-  const int per_tile = p.splits * groups * (p.slots ? p.slots : 1);
-  const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t tile = unit / per_tile;
-  int rest = (int)(unit - tile * per_tile);
-  const int64_t t0 = tile * 16 * TT;
+  const uint32_t per_tile = of.splits * groups * (p.slots ? p.slots : 1);
+  const int64_t tile = blockIdx.x / per_tile, t0 = tile * 16 * TT;
   if (t0 >= p.M) return;
-  const int split = rest % p.splits;
-  rest /= p.splits;
-  const int g0 = rest % groups * 16 * RT;
-  const int slot = rest / groups;
+  int rest = (int)(blockIdx.x - tile * per_tile);
+  const int split = rest % of.splits;
+  rest /= of.splits;
+  const int g0 = rest % groups * 16 * RT, slot = rest / groups;
   Tile<TT> tl;
   tl.read(p.index, t0, p.M, p.L);
   const int rows = p.M - t0 < 16 * TT ? (int)(p.M - t0) : 16 * TT;
-  const uint32_t ld = (uint32_t)p.n * 2;
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.X + t0 * ld, (int64_t)rows * ld);
-  const int k0 = split * p.per, k1 = k0 + p.per < p.n ? k0 + p.per : p.n;
+  const uint32_t ld = (uint32_t)of.n * 2;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(of.X + t0 * ld, (int64_t)rows * ld);
+  const int first = 64 * (wave + kDownWaves * split), step = 64 * kDownWaves * of.splits;
   for (int a = p.slots ? tl.leader(slot) : tl.first(); a >= 0; a = tl.first()) {
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.W + (int64_t)a * p.r * ld, (int64_t)p.r * ld);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(of.W + (int64_t)a * p.r * ld, (int64_t)p.r * ld);
     uint32_t ox[TT], ow[RT];
 #pragma unroll
     for (int i = 0; i < TT; ++i) ox[i] = tl.id[i] == a ? (16 * i + fr) * ld : kOOB;
@@ -140,35 +148,63 @@ __global__ void __launch_bounds__(256) k_down(const DownArgs p) {
     for (int i = 0; i < TT; ++i)
 #pragma unroll
       for (int j = 0; j < RT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    constexpr int U = TT * RT > 4 ? 2 : 4;
-    for (int k = k0; k < k1; k += 32 * U) {
-      v4i x[U][TT], w[U][RT];
+    // Two runs are in flight at a time (lane q: 16 bytes each at 8 q and 32 + 8 q of a run).  Runs past
+    // the last read zeros.
+    struct Run {
+      v4i x[2][TT], w[2][RT];
+    };
+    auto load = [&](int k, Run& f) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+      for (int u = 0; u < 2; ++u) {
         const int c = k + 32 * u + 8 * q;
-        const uint32_t o = c < k1 ? 2u * c : kOOB;
+        const uint32_t o = c < of.n ? 2u * c : kOOB;
 #pragma unroll
-        for (int i = 0; i < TT; ++i) x[u][i] = load16(rx, (ox[i] | o) & kOOB ? kOOB : ox[i] + o);
+        for (int i = 0; i < TT; ++i) f.x[u][i] = load16(rx, (ox[i] | o) & kOOB ? kOOB : ox[i] + o);
 #pragma unroll
-        for (int j = 0; j < RT; ++j) w[u][j] = load16(rw, (ow[j] | o) & kOOB ? kOOB : ow[j] + o);
+        for (int j = 0; j < RT; ++j) f.w[u][j] = load16(rw, (ow[j] | o) & kOOB ? kOOB : ow[j] + o);
       }
+    };
+    auto add = [&](const Run& f) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < TT; ++i)
 #pragma unroll
-          for (int j = 0; j < RT; ++j) acc[i][j] = mfma<TY>(w[u][j], x[u][i], acc[i][j]);
+          for (int j = 0; j < RT; ++j) acc[i][j] = mfma<TY>(f.w[u][j], f.x[u][i], acc[i][j]);
+    };
+    Run f0, f1;
+    load(first, f0);
+    for (int k = first; k < of.n; k += 2 * step) {
+      load(k + step, f1);
+      add(f0);
+      load(k + 2 * step, f0);
+      add(f1);
     }
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      if (tl.id[i] != a) continue;
-      float* h = p.H + (split * p.M + t0 + 16 * i + fr) * p.rp + g0 + 4 * q;
+    for (int g = 0; g < RT; g += PASS) {
+      if (g0 + 16 * g >= p.rp) break;
+      __syncthreads();
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
-        if (g0 + 16 * j < p.rp) *reinterpret_cast<v4f*>(h + 16 * j) = acc[i][j];
-      tl.id[i] = -1;
+      for (int i = 0; i < TT; ++i)
+#pragma unroll
+        for (int j = 0; j < PASS; ++j) *reinterpret_cast<v4f*>(&sums[wave][i * PASS + j][4 * lane]) = acc[i][g + j];
+      __syncthreads();
+#pragma unroll
+      for (int y = 0; y < TT * PASS; y += kDownWaves) {
+        const int z = y + wave, i = z / PASS, j = z % PASS;  // this wave's tile
+        if (z >= TT * PASS) break;
+        v4f s = *reinterpret_cast<const v4f*>(&sums[0][z][4 * lane]);
+#pragma unroll
+        for (int w = 1; w < kDownWaves; ++w) s += *reinterpret_cast<const v4f*>(&sums[w][z][4 * lane]);
+        const int id = TT == 1 || i == 0 ? tl.id[0] : tl.id[TT - 1];
+        if (id == a && g0 + 16 * (g + j) < p.rp)
+          *reinterpret_cast<v4f*>(of.H + (split * p.M + t0 + 16 * i + fr) * p.rp + g0 + 16 * (g + j) + 4 * q) = s;
+      }
     }
     if (p.slots) return;
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+      if (tl.id[i] == a) tl.id[i] = -1;
   }
 }
 
@@ -183,7 +219,7 @@ struct UpArgs {
   int L, d, r, ld, rp, splits;
   int ranks;            // numbers of a row of H that count
   int slots;            // as k_down
-  int chunk;            // output columns of a wave (a multiple of 64)
+  int chunk;            // output columns of a wave (a multiple of 32)
 };
 
 // Eight numbers of a weight row from number k on; zeros past the row's r.
@@ -199,9 +235,10 @@ __device__ __forceinline__ v4i row8(const uint16_t* __restrict__ row, int k, int
   return v4i{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
 }
 
-// Y = base + s_a W_a h.  A wave takes 16 TT tokens and 64 columns at a time.  Row m of the matrix
-// instruction's tile u is column 16 (m / 4) + 4 u + m % 4, so lane l ends up with columns
-// 16 (l / 16) + 0 .. 15 of token l % 16: whole 128-byte pieces of a row are read and written.
+// Y = base + s_a W_a h.  A wave takes 16 TT tokens and 32 columns at a time.  Row m of the matrix
+// instruction's tile u is column 8 (m / 4) + 4 u + m % 4, so lane l ends up with columns
+// 8 (l / 16) + 0 .. 7 of token l % 16, and a row is read and written in whole runs of 64 bytes.  The
+// next columns' weights are loaded while these are at work, the first ones before h is there.
 // KT: steps of 32 of the rank.
 template <int TY, int TT, int KT, bool WIDE>
 __global__ void __launch_bounds__(256) k_up(const UpArgs p) {
@@ -219,6 +256,21 @@ __global__ void __launch_bounds__(256) k_up(const UpArgs p) {
   all = tl;
   const int c0 = (int)block * p.chunk, c1 = c0 + p.chunk < p.d ? c0 + p.chunk : p.d;
   for (int a = p.slots ? tl.leader((int)(in - tile * slots)) : tl.first(); a >= 0; a = tl.first()) {
+    const uint16_t* W = reinterpret_cast<const uint16_t*>(p.W) + (int64_t)a * p.d * p.ld;
+    struct Cols {
+      v4i w[2][KT];
+    };
+    auto load = [&](int n0, Cols& f) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int row = n0 + 8 * (fr >> 2) + 4 * u + (fr & 3);
+#pragma unroll
+        for (int c = 0; c < KT; ++c)
+          f.w[u][c] = row8<WIDE>(W + (int64_t)row * p.ld, row < p.d ? 32 * c + 8 * q : p.r, p.r);
+      }
+    };
+    Cols cur;
+    load(c0, cur);
     const float s = p.scale[a];
     v4i hi[TT][KT], lo[TT][KT];
     float back[TT];
@@ -233,8 +285,9 @@ __global__ void __launch_bounds__(256) k_up(const UpArgs p) {
         const int k = 32 * c + 8 * q;
         if (!mine || k >= p.rp) continue;
         const float* h = p.H + (t0 + 16 * i + fr) * p.rp + k;
-        for (int z = 0; z < p.splits; ++z, h += p.M * p.rp) {
-          const float4 x = *reinterpret_cast<const float4*>(h), y = *reinterpret_cast<const float4*>(h + 4);
+#pragma unroll 4
+        for (int z = 0; z < p.splits; ++z) {
+          const float4 *o = reinterpret_cast<const float4*>(h + z * p.M * p.rp), x = o[0], y = o[1];
           v[c][0] += x.x, v[c][1] += x.y, v[c][2] += x.z, v[c][3] += x.w;
           v[c][4] += y.x, v[c][5] += y.y, v[c][6] += y.z, v[c][7] += y.w;
         }
@@ -281,154 +334,185 @@ __global__ void __launch_bounds__(256) k_up(const UpArgs p) {
           lo[i][c][e] = (int)b;
         }
     }
-    const uint16_t* W = reinterpret_cast<const uint16_t*>(p.W) + (int64_t)a * p.d * p.ld;
-    for (int n0 = c0; n0 < c1; n0 += 64) {
-      v4f acc[TT][4];
+    for (int n0 = c0; n0 < c1; n0 += 32) {
+      const int col = n0 + 8 * q;
+      u4i b[TT];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int row = n0 + 16 * (fr >> 2) + 4 * u + (fr & 3);
-        v4i w[KT];
+      for (int i = 0; i < TT; ++i) {
+        b[i] = u4i{0, 0, 0, 0};
+        if (p.base && tl.id[i] == a && col < p.d)
+          b[i] = *reinterpret_cast<const u4i*>(p.base + 2 * ((t0 + 16 * i + fr) * p.d + col));
+      }
+      Cols next;
+      load(n0 + 32 < c1 ? n0 + 32 : p.d, next);
+      v4f acc[TT][2];
 #pragma unroll
-        for (int c = 0; c < KT; ++c)
-          w[c] = row8<WIDE>(W + (int64_t)row * p.ld, row < p.d ? 32 * c + 8 * q : p.r, p.r);
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
           acc[i][u] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < KT; ++c) {
-            acc[i][u] = mfma<TY>(w[c], lo[i][c], acc[i][u]);
-            acc[i][u] = mfma<TY>(w[c], hi[i][c], acc[i][u]);
+            acc[i][u] = mfma<TY>(cur.w[u][c], lo[i][c], acc[i][u]);
+            acc[i][u] = mfma<TY>(cur.w[u][c], hi[i][c], acc[i][u]);
           }
         }
-      }
 #pragma unroll
       for (int i = 0; i < TT; ++i) {
-        const int64_t at = (t0 + 16 * i + fr) * p.d;
+        if (tl.id[i] != a || col >= p.d) continue;
+        u4i y;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {  // eight columns
-          const int col = n0 + 16 * q + 8 * g;
-          if (tl.id[i] != a || col >= p.d) continue;
-          u4i b = u4i{0, 0, 0, 0};
-          if (p.base) b = *reinterpret_cast<const u4i*>(p.base + 2 * (at + col));
-          u4i y;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const f2 f = unpack2<TY>(b[e]);
-            const v4f& t = acc[i][2 * g + e / 2];
-            y[e] = pack2<TY>(f.x + t[2 * (e & 1)] * back[i], f.y + t[2 * (e & 1) + 1] * back[i]);
-          }
-          *reinterpret_cast<u4i*>(p.Y + 2 * (at + col)) = y;
+        for (int e = 0; e < 4; ++e) {
+          const f2 f = unpack2<TY>(b[i][e]);
+          const v4f& t = acc[i][e / 2];
+          y[e] = pack2<TY>(f.x + t[2 * (e & 1)] * back[i], f.y + t[2 * (e & 1) + 1] * back[i]);
         }
+        *reinterpret_cast<u4i*>(p.Y + 2 * ((t0 + 16 * i + fr) * p.d + col)) = y;
       }
+      cur = next;
     }
+    if (p.slots) break;
 #pragma unroll
     for (int i = 0; i < TT; ++i)
       if (tl.id[i] == a) tl.id[i] = -1;
-    if (p.slots) break;
   }
   // Rows without an adapter: the base's (nothing to do in place).
   if (p.base == p.Y || (p.slots && in - tile * slots != 0)) return;
-  for (int n0 = c0; n0 < c1; n0 += 64)
+  for (int col = c0 + 8 * q; col < c1; col += 32)
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       const int64_t t = t0 + 16 * i + fr;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int col = n0 + 16 * q + 8 * g;
-        if (all.id[i] >= 0 || t >= p.M || col >= p.d) continue;
-        u4i b = u4i{0, 0, 0, 0};
-        if (p.base) b = *reinterpret_cast<const u4i*>(p.base + 2 * (t * p.d + col));
-        *reinterpret_cast<u4i*>(p.Y + 2 * (t * p.d + col)) = b;
-      }
+      if (all.id[i] >= 0 || t >= p.M) continue;
+      u4i b = u4i{0, 0, 0, 0};
+      if (p.base) b = *reinterpret_cast<const u4i*>(p.base + 2 * (t * p.d + col));
+      *reinterpret_cast<u4i*>(p.Y + 2 * (t * p.d + col)) = b;
     }
 }
 
-// out[a] (cols x ldo) = in[a] (rows x cols) transposed, zeros from column `rows` on.
-__global__ void __launch_bounds__(256) k_turn(const uint16_t* __restrict__ in, uint16_t* __restrict__ out, int rows,
-                                              int cols, int ldo) {
+// out[a] (cols x ldo) = in[a] (rows x cols) transposed, zeros from column `rows` on, of both factors.
+struct Turn {
+  const uint16_t* in;
+  uint16_t* out;
+  int rows, cols, ldo, tiles_x, tiles;  // tiles of 32 x 32: along the columns, in all
+};
+struct TurnArgs {
+  Turn of[2];
+};
+__global__ void __launch_bounds__(256) k_turn(const TurnArgs p) {
   __shared__ uint16_t t[32][34];
+  const bool second = (int)blockIdx.x >= p.of[0].tiles;
+  const Turn& w = p.of[second];
+  const int tile = blockIdx.x - (second ? p.of[0].tiles : 0);
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int64_t c0 = (int64_t)blockIdx.x * 32, r0 = (int64_t)blockIdx.y * 32;
-  in += (int64_t)blockIdx.z * rows * cols;
-  out += (int64_t)blockIdx.z * cols * ldo;
+  const int64_t c0 = (int64_t)(tile % w.tiles_x) * 32, r0 = (int64_t)(tile / w.tiles_x) * 32;
+  const uint16_t* in = w.in + (int64_t)blockIdx.y * w.rows * w.cols;
+  uint16_t* out = w.out + (int64_t)blockIdx.y * w.cols * w.ldo;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t r = r0 + y + 8 * i, c = c0 + x;
-    t[y + 8 * i][x] = r < rows && c < cols ? in[r * cols + c] : 0;
+    t[y + 8 * i][x] = r < w.rows && c < w.cols ? in[r * w.cols + c] : 0;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t r = c0 + y + 8 * i, c = r0 + x;
-    if (r < cols && c < ldo) out[r * ldo + c] = t[x][y + 8 * i];
+    if (r < w.cols && c < w.ldo) out[r * w.ldo + c] = t[x][y + 8 * i];
   }
 }
 
+struct Sum {
+  const uint8_t* P;  // M x F token rows (dY or X)
+  const float* H;    // splits x M x rp (h or dh)
+  void* out;         // L x F x r (dA) or L x r x F (dB)
+  int F, splits;
+};
 struct SumArgs {
-  const uint8_t* P;      // M x F token rows (dY or X)
-  const float* H;        // splits x M x rp (h or dh)
+  Sum of[2];             // dA, dB
   const int32_t* index;
   const float* scale;
-  void* out;             // L x F x r (ranks in the lanes) or L x r x F
   int64_t M;
-  int L, F, r, rp, splits;
+  int L, r, rp;
+  int blocks0;           // blocks of 64 columns of the first one
   int64_t per;           // tokens of a part
-  int64_t numel;         // of `out`: parts lie one after the other
+  int64_t numel[2];      // of the outputs: parts lie one after the other
 };
 
 // sum over an adapter's tokens of P_t h_t^T s_a.  A block takes 64 columns of P and all ranks: it
-// collects its adapter's tokens in order, 32 at a time, and each wave adds 16 columns x 16 RT ranks.
-// Both operands have the contraction (tokens) in rows and leave LDS through the transposing reads.
-// h goes as three bf16 numbers; fp16 rows of P as two (exact).
+// lists its adapter's tokens (of 2048 rows at a time, in order) and adds them T at a time, each
+// wave 16 columns x 16 RT ranks; the next ones are loaded meanwhile.  Both operands have the
+// contraction (tokens) in rows and leave LDS through the transposing reads.  h goes as three bf16
+// numbers; fp16 rows of P as two (exact).
+template <int TY, int RT>
+struct SumLds {
+  static constexpr int PP = TY == T_FP16 ? 2 : 1, T = RT == 8 ? 32 : 64;
+  static constexpr int PS = 64 + 8, HS = 16 * RT + 8;  // row strides (16-bit numbers)
+  static constexpr int kScan = 2048;
+  uint16_t p[PP][T * PS];
+  uint16_t h[3][T * HS];
+  int list[kScan + T];
+  int counts[4];
+};
+
 template <int TY, int TO, int RT, bool RANK_LANES>
-__global__ void __launch_bounds__(256) k_sums(const SumArgs p) {
-  constexpr int PP = TY == T_FP16 ? 2 : 1;
-  constexpr int PS = 64 + 8, HS = 16 * RT + 8;  // row strides (16-bit numbers)
-  __shared__ __attribute__((aligned(16))) uint16_t lp[PP][32 * PS];
-  __shared__ __attribute__((aligned(16))) uint16_t lh[3][32 * HS];
-  __shared__ int list[256 + 32];
-  __shared__ int counts[4];
+__device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64_t numel, int block, SumLds<TY, RT>& L) {
+  using S = SumLds<TY, RT>;
+  constexpr int PP = S::PP, T = S::T, PS = S::PS, HS = S::HS;
+  constexpr int NP = T / 32, NH = T * RT / 64;  // 16-byte loads of a thread
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, fr = lane & 15, q = lane >> 4;
-  const int a = blockIdx.y, f0 = blockIdx.x * 64;
+  const int a = blockIdx.y, f0 = block * 64;
   const float s = p.scale[a];
   const int64_t tb = blockIdx.z * p.per, te = tb + p.per < p.M ? tb + p.per : p.M;
   v4f acc[RT];
 #pragma unroll
   for (int j = 0; j < RT; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+  u4i pv[NP];
+  float4 hv[NH];
 
-  auto batch = [&](int64_t base, int from, int n) {  // tokens base + list[from .. from + n), n <= 32
-    __syncthreads();
-    {
-      const int row = tid >> 3, c = (tid & 7) * 8;
-      u4i v = u4i{0, 0, 0, 0};
-      if (row < n && f0 + c < p.F) v = *reinterpret_cast<const u4i*>(p.P + 2 * ((base + list[from + row]) * p.F + f0 + c));
+  // tokens tb + list[from .. from + n), n <= T: rows past n are zeros
+  auto fetch = [&](int from, int n) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int row = (tid >> 3) + 32 * i, c = (tid & 7) * 8;
+      pv[i] = u4i{0, 0, 0, 0};
+      if (row < n && f0 + c < of.F)
+        pv[i] = *reinterpret_cast<const u4i*>(of.P + 2 * ((tb + L.list[from + row]) * of.F + f0 + c));
+    }
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      const int at = tid + 256 * i, row = at / (4 * RT), c = at % (4 * RT) * 4;
+      hv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < n && c < p.rp) {
+        const float* src = of.H + (tb + L.list[from + row]) * p.rp + c;
+        for (int z = 0; z < of.splits; ++z) {
+          const float4 x = *reinterpret_cast<const float4*>(src + z * p.M * p.rp);
+          hv[i].x += x.x, hv[i].y += x.y, hv[i].z += x.z, hv[i].w += x.w;
+        }
+      }
+    }
+  };
+  auto store = [&]() {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int at = ((tid >> 3) + 32 * i) * PS + (tid & 7) * 8;
       if (TY == T_FP16) {
         u4i t, b;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const f2 x = unpack2<T_FP16>(v[e]);
+          const f2 x = unpack2<T_FP16>(pv[i][e]);
           const f2 y = f2{top_bf16(x.x), top_bf16(x.y)};
           t[e] = pack2<T_BF16>(y.x, y.y);
           b[e] = pack2<T_BF16>(finite(x.x) ? x.x - y.x : 0.f, finite(x.y) ? x.y - y.y : 0.f);
         }
-        *reinterpret_cast<u4i*>(&lp[0][row * PS + c]) = t;
-        *reinterpret_cast<u4i*>(&lp[PP - 1][row * PS + c]) = b;
+        *reinterpret_cast<u4i*>(&L.p[0][at]) = t;
+        *reinterpret_cast<u4i*>(&L.p[PP - 1][at]) = b;
       } else {
-        *reinterpret_cast<u4i*>(&lp[0][row * PS + c]) = v;
+        *reinterpret_cast<u4i*>(&L.p[0][at]) = pv[i];
       }
     }
-    for (int i = tid; i < 32 * 4 * RT; i += 256) {
-      const int row = i / (4 * RT), c = i % (4 * RT) * 4;
-      float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row < n && c < p.rp) {
-        const float* src = p.H + (base + list[from + row]) * p.rp + c;
-        for (int z = 0; z < p.splits; ++z, src += p.M * p.rp) {
-          const float4 x = *reinterpret_cast<const float4*>(src);
-          h.x += x.x, h.y += x.y, h.z += x.z, h.w += x.w;
-        }
-        h.x *= s, h.y *= s, h.z *= s, h.w *= s;
-      }
-      float v[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      const int at = tid + 256 * i, row = at / (4 * RT), c = at % (4 * RT) * 4;
+      float v[4] = {hv[i].x * s, hv[i].y * s, hv[i].z * s, hv[i].w * s};
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         float t[4];
@@ -437,52 +521,89 @@ __global__ void __launch_bounds__(256) k_sums(const SumArgs p) {
           t[e] = top_bf16(v[e]);
           v[e] = finite(v[e]) ? v[e] - t[e] : 0.f;
         }
-        *reinterpret_cast<uint2*>(&lh[k][row * HS + c]) = make_uint2(pack2<T_BF16>(t[0], t[1]), pack2<T_BF16>(t[2], t[3]));
+        *reinterpret_cast<uint2*>(&L.h[k][row * HS + c]) = make_uint2(pack2<T_BF16>(t[0], t[1]), pack2<T_BF16>(t[2], t[3]));
       }
     }
-    __syncthreads();
-    auto frag = [&](const uint16_t* m, int stride, int col) {  // rows 8 q .. 8 q + 7 of column col + fr
-      const uint16_t* at = m + (8 * q + (fr >> 2)) * stride + col + 4 * (fr & 3);
-      const int2 x = __builtin_bit_cast(int2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t)at));
-      const int2 y = __builtin_bit_cast(int2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t)(at + 4 * stride)));
-      return v4i{x.x, x.y, y.x, y.y};
-    };
-    v4i pf[PP];
+  };
+  auto frag = [&](const uint16_t* m, int stride, int row, int col) {  // rows row + 8 q + 0 .. 7 of column col + fr
+    const uint16_t* at = m + (row + 8 * q + (fr >> 2)) * stride + col + 4 * (fr & 3);
+    const int2 x = __builtin_bit_cast(int2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t)at));
+    const int2 y = __builtin_bit_cast(int2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t)(at + 4 * stride)));
+    return v4i{x.x, x.y, y.x, y.y};
+  };
+  auto add = [&]() {
 #pragma unroll
-    for (int k = 0; k < PP; ++k) pf[k] = frag(lp[k], PS, 16 * wave);
+    for (int t = 0; t < T; t += 32) {
+      v4i pf[PP];
 #pragma unroll
-    for (int j = 0; j < RT; ++j)
+      for (int k = 0; k < PP; ++k) pf[k] = frag(L.p[k], PS, t, 16 * wave);
 #pragma unroll
-      for (int k = 2; k >= 0; --k) {
-        const v4i h = frag(lh[k], HS, 16 * j);
+      for (int j = 0; j < RT; ++j)
 #pragma unroll
-        for (int z = PP - 1; z >= 0; --z)
-          acc[j] = RANK_LANES ? mfma<T_BF16>(pf[z], h, acc[j]) : mfma<T_BF16>(h, pf[z], acc[j]);
-      }
+        for (int k = 2; k >= 0; --k) {
+          const v4i h = frag(L.h[k], HS, t, 16 * j);
+#pragma unroll
+          for (int z = PP - 1; z >= 0; --z)
+            acc[j] = RANK_LANES ? mfma<T_BF16>(pf[z], h, acc[j]) : mfma<T_BF16>(h, pf[z], acc[j]);
+        }
+    }
+  };
+  auto run = [&](int n) {  // whole lots of T tokens of the list, or (n < T) its last ones
+    fetch(0, n);
+    for (int from = 0;;) {
+      __syncthreads();
+      store();
+      __syncthreads();
+      from += T;
+      const bool more = from + T <= n;
+      if (more) fetch(from, T);
+      add();
+      if (!more) break;
+    }
   };
 
-  int have = 0;  // collected, not yet added (positions in the list relative to tb)
-  for (int64_t t = tb; t < te; t += 256) {
-    const bool hit = t + tid < te && p.index[t + tid] == a;
-    const uint64_t m = __builtin_amdgcn_ballot_w64(hit);
-    __syncthreads();
-    if (lane == 0) counts[wave] = __builtin_popcountll(m);
-    __syncthreads();
-    int at = have, all = have;
-    for (int w = 0; w < 4; ++w) {
-      if (w < wave) at += counts[w];
-      all += counts[w];
+  int have = 0;  // listed, not yet added
+  for (int64_t t = tb; t < te; t += S::kScan) {
+    // eight rows in a row for each thread
+    const int64_t mine = t + 8 * tid;
+    uint32_t hits = 0;
+    if (mine + 8 <= te) {
+      const int4 x = *reinterpret_cast<const int4*>(p.index + mine), y = *reinterpret_cast<const int4*>(p.index + mine + 4);
+      hits = (x.x == a) | (x.y == a) << 1 | (x.z == a) << 2 | (x.w == a) << 3 | (y.x == a) << 4 | (y.y == a) << 5 |
+             (y.z == a) << 6 | (y.w == a) << 7;
+    } else {
+      for (int e = 0; e < 8; ++e)
+        if (mine + e < te && p.index[mine + e] == a) hits |= 1u << e;
     }
-    if (hit) list[at + __builtin_popcountll(m & ((1ull << lane) - 1))] = (int)(t - tb) + tid;
-    int from = 0;
-    for (; all - from >= 32; from += 32) batch(tb, from, 32);
-    have = all - from;
+    int at = __builtin_popcount(hits);
+    const int n = at;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+      const int o = __shfl_up(at, k);
+      if (lane >= k) at += o;
+    }
     __syncthreads();
-    const int keep = tid < have ? list[from + tid] : 0;
+    if (lane == 63) L.counts[wave] = at;
     __syncthreads();
-    if (tid < have) list[tid] = keep;
+    int all = have;
+    at += have - n;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) at += L.counts[w];
+      all += L.counts[w];
+    }
+    for (uint32_t m = hits; m; m &= m - 1) L.list[at++] = (int)(mine - tb) + __builtin_ctz(m);
+    __syncthreads();
+    const int whole = all / T * T;
+    if (whole) run(whole);
+    have = all - whole;
+    __syncthreads();
+    const int keep = tid < have ? L.list[whole + tid] : 0;
+    __syncthreads();
+    if (tid < have) L.list[tid] = keep;
   }
-  if (have > 0) batch(tb, 0, have);
+  __syncthreads();
+  if (have > 0) run(have);
 
   // lane l: column (rank) l % 16 of the tile, rows 4 (l / 16) + 0 .. 3
 #pragma unroll
@@ -490,85 +611,104 @@ __global__ void __launch_bounds__(256) k_sums(const SumArgs p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int f = f0 + 16 * wave + (RANK_LANES ? 4 * q + e : fr), k = 16 * j + (RANK_LANES ? fr : 4 * q + e);
-      if (f >= p.F || k >= p.r) continue;
-      const int64_t at = blockIdx.z * p.numel + (RANK_LANES ? ((int64_t)a * p.F + f) * p.r + k : ((int64_t)a * p.r + k) * p.F + f);
+      if (f >= of.F || k >= p.r) continue;
+      const int64_t at = blockIdx.z * numel + (RANK_LANES ? ((int64_t)a * of.F + f) * p.r + k : ((int64_t)a * p.r + k) * of.F + f);
       if (TO == T_FP32)
-        static_cast<float*>(p.out)[at] = acc[j][e];
+        static_cast<float*>(of.out)[at] = acc[j][e];
       else
-        static_cast<uint16_t*>(p.out)[at] = (uint16_t)pack2<TO>(acc[j][e], 0.f);
+        static_cast<uint16_t*>(of.out)[at] = (uint16_t)pack2<TO>(acc[j][e], 0.f);
     }
 }
 
-// out = the parts added in order; numel a multiple of 4.
+template <int TY, int TO, int RT>
+__global__ void __launch_bounds__(256) k_sums(const SumArgs p) {
+  __shared__ __attribute__((aligned(16))) SumLds<TY, RT> lds;
+  const int b = blockIdx.x;
+  if (b < p.blocks0)
+    sum_block<TY, TO, RT, true>(p, p.of[0], p.numel[0], b, lds);
+  else
+    sum_block<TY, TO, RT, false>(p, p.of[1], p.numel[1], b - p.blocks0, lds);
+}
+
+// out = the parts added in order, of both gradients; numbers of elements multiples of 4.
+struct PartsArgs {
+  const float* in[2];
+  void* out[2];
+  int64_t numel[2];
+};
 template <int TO>
-__global__ void __launch_bounds__(256) k_parts(const float* __restrict__ in, void* __restrict__ out, int64_t numel,
-                                               int parts) {
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < numel; i += (int64_t)gridDim.x * 1024) {
-    float4 s = *reinterpret_cast<const float4*>(in + i);
+__global__ void __launch_bounds__(256) k_parts(const PartsArgs p, int parts) {
+  const int64_t all = p.numel[0] + p.numel[1];
+  for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; at < all; at += (int64_t)gridDim.x * 1024) {
+    const int b = at >= p.numel[0];
+    const int64_t i = at - (b ? p.numel[0] : 0);
+    const float* in = p.in[b] + i;
+    float4 s = *reinterpret_cast<const float4*>(in);
     for (int z = 1; z < parts; ++z) {
-      const float4 x = *reinterpret_cast<const float4*>(in + z * numel + i);
+      const float4 x = *reinterpret_cast<const float4*>(in + z * p.numel[b]);
       s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
     }
     if (TO == T_FP32)
-      *reinterpret_cast<float4*>(static_cast<float*>(out) + i) = s;
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out[b]) + i) = s;
     else
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + i) = make_uint2(pack2<TO>(s.x, s.y), pack2<TO>(s.z, s.w));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out[b]) + i) = make_uint2(pack2<TO>(s.x, s.y), pack2<TO>(s.z, s.w));
   }
 }
 
-constexpr int64_t kSlotRows = 1024;  // up to here one wave per token of a tile
+constexpr int64_t kSlotRows = 1024;  // up to here one block (wave) per token of a tile
 
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// Splits of a k_down call over n columns, and the columns of each.
-struct Splits {
-  int count, per;
-};
-Splits down_splits(int64_t M, int64_t n, int64_t r) {
-  const int64_t tiles = (r + 15) / 16;
-  const int64_t waves = M <= kSlotRows ? M * tiles : (M + 31) / 32 * ((tiles + 3) / 4);
-  int64_t s = waves > 0 ? (2048 + waves - 1) / waves : 1;
-  const int64_t most = (n + 255) / 256;
-  s = s > 16 ? 16 : s;
+// Splits of k_down over n columns: where its blocks are fewer than the compute units, down to two
+// runs of 64 columns for each wave.
+int down_splits(int64_t M, int64_t n, int64_t r) {
+  const int64_t blocks = M <= kSlotRows ? M * ((r + 15) / 16) : (M + 31) / 32;
+  const int64_t most = n / (2 * 64 * kDownWaves);
+  int64_t s = blocks > 0 ? 256 / blocks : 1;
   s = s > most ? most : s;
-  const int64_t per = ((n + s - 1) / s + 63) / 64 * 64;
-  return {(int)((n + per - 1) / per), (int)per};
+  return (int)(s > 8 ? 8 : s < 1 ? 1 : s);
 }
 
-// Parts of the tokens of a k_sums call.
+// Parts of the tokens of k_sums, each a multiple of 8 rows.
 struct Parts {
   int count;
   int64_t per;
 };
-Parts sum_parts(int64_t M, int64_t L, int64_t F) {
-  const int64_t blocks = L * ((F + 63) / 64);
-  int64_t z = blocks >= 512 ? 1 : (512 + blocks - 1) / blocks;
+Parts sum_parts(int64_t M, int64_t L, int64_t d, int64_t n) {
+  const int64_t blocks = L * ((d + 63) / 64 + (n + 63) / 64);
+  int64_t z = (256 + blocks - 1) / blocks;
   const int64_t most = (M + 511) / 512;
-  z = z > 32 ? 32 : z;
-  z = z > most ? (most < 1 ? 1 : most) : z;
-  const int64_t per = M < 1 ? 256 : ((M + z - 1) / z + 255) / 256 * 256;
+  z = z > most ? most : z;
+  z = z < 1 ? 1 : z;
+  int64_t per = ((M + z - 1) / z + 7) / 8 * 8;
+  per = per < 8 ? 8 : per;
   const int64_t c = (M + per - 1) / per;
   return {(int)(c < 1 ? 1 : c), per};
 }
 
 template <int TY>
-hipError_t down(DownArgs a, const Splits& s, hipStream_t st) {
-  a.splits = s.count;
-  a.per = s.per;
+hipError_t down(DownArgs a, int problems, hipStream_t st) {
   const int rt = a.rp / 16;
   a.slots = a.M <= kSlotRows ? (a.M < 16 ? (int)a.M : 16) : 0;
-  const int tt = a.slots ? 1 : 2, per_wave = a.slots ? 1 : (rt >= 4 ? 4 : rt == 1 ? 1 : 2);
-  const int64_t units = (a.M + 16 * tt - 1) / (16 * tt) * s.count * ((rt + per_wave - 1) / per_wave) * (a.slots ? a.slots : 1);
-  const dim3 grid((unsigned)((units + 3) / 4));
+  const int tt = a.slots ? 1 : 2, per = a.slots ? 1 : rt > 4 ? 8 : rt > 2 ? 4 : rt;
+  int64_t blocks = 0;
+  for (int i = 0; i < problems; ++i) {
+    const int64_t b = (a.M + 16 * tt - 1) / (16 * tt) * a.of[i].splits * ((rt + per - 1) / per) * (a.slots ? a.slots : 1);
+    blocks = b > blocks ? b : blocks;
+  }
+  const dim3 grid((unsigned)blocks, (unsigned)problems);
+  const int threads = 64 * kDownWaves;
   if (a.slots)
-    k_down<TY, 1, 1><<<grid, 256, 0, st>>>(a);
-  else if (per_wave == 1)
-    k_down<TY, 2, 1><<<grid, 256, 0, st>>>(a);
-  else if (per_wave == 2)
-    k_down<TY, 2, 2><<<grid, 256, 0, st>>>(a);
+    k_down<TY, 1, 1><<<grid, threads, 0, st>>>(a);
+  else if (per == 1)
+    k_down<TY, 2, 1><<<grid, threads, 0, st>>>(a);
+  else if (per == 2)
+    k_down<TY, 2, 2><<<grid, threads, 0, st>>>(a);
+  else if (per == 4)
+    k_down<TY, 2, 4><<<grid, threads, 0, st>>>(a);
   else
-    k_down<TY, 2, 4><<<grid, 256, 0, st>>>(a);
+    k_down<TY, 2, 8><<<grid, threads, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -582,13 +722,18 @@ void up_kt(const UpArgs& a, dim3 grid, hipStream_t st) {
     k_up<TY, TT, 4, WIDE><<<grid, 256, 0, st>>>(a);
 }
 
+// Columns of a wave: at least 2048 waves where there are columns for them.
+int64_t up_chunk(int64_t tiles, int64_t d) {
+  int64_t chunk = 512;
+  while (chunk > 64 && tiles * ((d + chunk - 1) / chunk) < 2048) chunk /= 2;
+  return chunk;
+}
+
 template <int TY>
 hipError_t up(UpArgs a, hipStream_t st) {
   a.slots = a.M <= kSlotRows ? (a.M < 16 ? (int)a.M : 16) : 0;
   const int tt = a.slots ? 1 : 2;
-  const int64_t tiles = (a.M + 16 * tt - 1) / (16 * tt) * (a.slots ? a.slots : 1);
-  int64_t chunk = 512;
-  while (chunk > 64 && tiles * ((a.d + chunk - 1) / chunk) < 2048) chunk /= 2;
+  const int64_t tiles = (a.M + 16 * tt - 1) / (16 * tt) * (a.slots ? a.slots : 1), chunk = up_chunk(tiles, a.d);
   a.chunk = (int)chunk;
   const dim3 grid((unsigned)((tiles * ((a.d + chunk - 1) / chunk) + 3) / 4));
   const bool wide = a.r % 8 == 0 && a.ld % 8 == 0;
@@ -599,36 +744,42 @@ hipError_t up(UpArgs a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int TY, int TO, bool RANK_LANES>
+template <int TY, int TO>
 void sums_rt(const SumArgs& a, dim3 grid, hipStream_t st) {
   if (a.rp <= 16)
-    k_sums<TY, TO, 1, RANK_LANES><<<grid, 256, 0, st>>>(a);
+    k_sums<TY, TO, 1><<<grid, 256, 0, st>>>(a);
   else if (a.rp <= 32)
-    k_sums<TY, TO, 2, RANK_LANES><<<grid, 256, 0, st>>>(a);
+    k_sums<TY, TO, 2><<<grid, 256, 0, st>>>(a);
   else if (a.rp <= 64)
-    k_sums<TY, TO, 4, RANK_LANES><<<grid, 256, 0, st>>>(a);
+    k_sums<TY, TO, 4><<<grid, 256, 0, st>>>(a);
   else
-    k_sums<TY, TO, 8, RANK_LANES><<<grid, 256, 0, st>>>(a);
+    k_sums<TY, TO, 8><<<grid, 256, 0, st>>>(a);
 }
 
-template <int TY, bool RANK_LANES>
-hipError_t sums(SumArgs a, const Parts& z, int out_dtype, void* out, float* ws, hipStream_t st) {
+template <int TY>
+hipError_t sums(SumArgs a, const Parts& z, int out_dtype, float* ws, hipStream_t st) {
   a.per = z.per;
-  a.numel = (int64_t)a.L * a.F * a.r;
-  a.out = z.count > 1 ? ws : out;
-  const dim3 grid((unsigned)((a.F + 63) / 64), (unsigned)a.L, (unsigned)z.count);
+  PartsArgs q{};
+  for (int i = 0; i < 2; ++i) {
+    a.numel[i] = q.numel[i] = (int64_t)a.L * a.of[i].F * a.r;
+    q.out[i] = a.of[i].out;
+    if (z.count > 1) a.of[i].out = ws + (i ? z.count * a.numel[0] : 0);
+    q.in[i] = static_cast<const float*>(a.of[i].out);
+  }
+  a.blocks0 = (a.of[0].F + 63) / 64;
+  const dim3 grid((unsigned)(a.blocks0 + (a.of[1].F + 63) / 64), (unsigned)a.L, (unsigned)z.count);
   if (z.count > 1 || out_dtype == T_FP32)
-    sums_rt<TY, T_FP32, RANK_LANES>(a, grid, st);
+    sums_rt<TY, T_FP32>(a, grid, st);
   else
-    sums_rt<TY, TY, RANK_LANES>(a, grid, st);
-  hipError_t e = hipGetLastError();
+    sums_rt<TY, TY>(a, grid, st);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || z.count == 1) return e;
-  const int64_t want = (a.numel / 4 + 255) / 256;
+  const int64_t want = ((q.numel[0] + q.numel[1]) / 4 + 255) / 256;
   const unsigned blocks = (unsigned)(want < 2048 ? want : 2048);
   if (out_dtype == T_FP32)
-    k_parts<T_FP32><<<blocks, 256, 0, st>>>(ws, out, a.numel, z.count);
+    k_parts<T_FP32><<<blocks, 256, 0, st>>>(q, z.count);
   else
-    k_parts<TY><<<blocks, 256, 0, st>>>(ws, out, a.numel, z.count);
+    k_parts<TY><<<blocks, 256, 0, st>>>(q, z.count);
   return hipGetLastError();
 }
 
@@ -639,101 +790,88 @@ struct Ws {
 Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   Ws w{};
   const int64_t rp = round16(r);
-  int64_t at = up256(4 * M * rp * down_splits(M, n, r).count);
+  int64_t at = up256(4 * M * rp * down_splits(M, n, r));
   if (grads) {
     w.dh = at;
-    at += up256(4 * M * rp * down_splits(M, d, r).count);
+    at += up256(4 * M * rp * down_splits(M, d, r));
     w.at = at;
     at += up256(2 * L * r * d);
     w.bt = at;
     at += up256(2 * L * n * rp);
     w.parts = at;
-    const int64_t za = sum_parts(M, L, d).count, zb = sum_parts(M, L, n).count;
-    const int64_t pa = za > 1 ? 4 * za * L * d * r : 0, pb = zb > 1 ? 4 * zb * L * n * r : 0;
-    at += up256(pa > pb ? pa : pb);
+    const int64_t z = sum_parts(M, L, d, n).count;
+    at += z > 1 ? up256(4 * z * L * r * (d + n)) : 0;
   }
   w.bytes = at;
   return w;
 }
 
+DownArgs down_args(const AdapterArgs& p) {
+  DownArgs a{};
+  a.index = p.index;
+  a.M = p.M;
+  a.L = (int)p.L;
+  a.r = (int)p.r;
+  a.rp = (int)round16(p.r);
+  return a;
+}
+
+UpArgs up_args(const AdapterArgs& p) {
+  UpArgs a{};
+  a.index = p.index;
+  a.scale = p.scale;
+  a.base = static_cast<const uint8_t*>(p.base);
+  a.Y = static_cast<uint8_t*>(p.Y);
+  a.M = p.M;
+  a.L = (int)p.L;
+  a.rp = (int)round16(p.r);
+  a.ranks = (int)p.r;
+  return a;
+}
+
 template <int TY>
 hipError_t fwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
-  const Splits s = down_splits(p.M, p.n, p.r);
-  const int rp = (int)round16(p.r);
-  DownArgs x{};
-  x.X = static_cast<const uint8_t*>(p.X);
-  x.W = static_cast<const uint8_t*>(p.B);
-  x.index = p.index;
-  x.H = reinterpret_cast<float*>(ws);
-  x.M = p.M;
-  x.L = (int)p.L;
-  x.n = (int)p.n;
-  x.r = (int)p.r;
-  x.rp = rp;
-  hipError_t e = down<TY>(x, s, st);
+  float* h = reinterpret_cast<float*>(ws);
+  const int s = down_splits(p.M, p.n, p.r);
+  DownArgs x = down_args(p);
+  x.of[0] = Down{static_cast<const uint8_t*>(p.X), static_cast<const uint8_t*>(p.B), h, (int)p.n, s};
+  const hipError_t e = down<TY>(x, 1, st);
   if (e != hipSuccess) return e;
-  UpArgs y{};
-  y.H = x.H;
+  UpArgs y = up_args(p);
+  y.H = h;
+  y.splits = s;
   y.W = static_cast<const uint8_t*>(p.A);
-  y.index = p.index;
-  y.scale = p.scale;
-  y.base = static_cast<const uint8_t*>(p.base);
-  y.Y = static_cast<uint8_t*>(p.Y);
-  y.M = p.M;
-  y.L = (int)p.L;
   y.d = (int)p.d;
   y.r = y.ld = (int)p.r;
-  y.rp = rp;
-  y.ranks = (int)p.r;
-  y.splits = s.count;
   return up<TY>(y, st);
 }
 
 template <int TY>
 hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   const Ws w = carve(p.M, p.L, p.d, p.n, p.r, true);
-  const int rp = (int)round16(p.r);
-  const int L = (int)p.L, d = (int)p.d, n = (int)p.n, r = (int)p.r;
-  float *h = reinterpret_cast<float*>(ws), *dh = reinterpret_cast<float*>(ws + w.dh),
-        *parts = reinterpret_cast<float*>(ws + w.parts);
+  const int rp = (int)round16(p.r), L = (int)p.L, d = (int)p.d, n = (int)p.n, r = (int)p.r;
+  float *h = reinterpret_cast<float*>(ws), *dh = reinterpret_cast<float*>(ws + w.dh);
   uint16_t *at = reinterpret_cast<uint16_t*>(ws + w.at), *bt = reinterpret_cast<uint16_t*>(ws + w.bt);
+  const uint8_t *X = static_cast<const uint8_t*>(p.X), *dY = static_cast<const uint8_t*>(p.dY);
+  const int sh = down_splits(p.M, n, r), sd = down_splits(p.M, d, r);
   hipError_t e;
-  const Splits sh = down_splits(p.M, n, r), sd = down_splits(p.M, d, r);
   if (p.M > 0) {
-    k_turn<<<dim3((r + 31) / 32, (d + 31) / 32, L), 256, 0, st>>>(static_cast<const uint16_t*>(p.A), at, d, r, d);
+    TurnArgs t{};
+    t.of[0] = Turn{static_cast<const uint16_t*>(p.A), at, d, r, d, (r + 31) / 32, (r + 31) / 32 * ((d + 31) / 32)};
+    t.of[1] = Turn{static_cast<const uint16_t*>(p.B), bt, r, n, rp, (n + 31) / 32, (n + 31) / 32 * ((rp + 31) / 32)};
+    k_turn<<<dim3(t.of[0].tiles + (p.Y ? t.of[1].tiles : 0), L), 256, 0, st>>>(t);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    DownArgs x{};
-    x.index = p.index;
-    x.M = p.M;
-    x.L = L;
-    x.r = r;
-    x.rp = rp;
-    x.X = static_cast<const uint8_t*>(p.X);
-    x.W = static_cast<const uint8_t*>(p.B);
-    x.H = h;
-    x.n = n;
-    if ((e = down<TY>(x, sh, st)) != hipSuccess) return e;
-    x.X = static_cast<const uint8_t*>(p.dY);
-    x.W = reinterpret_cast<const uint8_t*>(at);
-    x.H = dh;
-    x.n = d;
-    if ((e = down<TY>(x, sd, st)) != hipSuccess) return e;
+    DownArgs x = down_args(p);
+    x.of[0] = Down{X, static_cast<const uint8_t*>(p.B), h, n, sh};
+    x.of[1] = Down{dY, reinterpret_cast<const uint8_t*>(at), dh, d, sd};
+    if ((e = down<TY>(x, 2, st)) != hipSuccess) return e;
     if (p.Y) {
-      k_turn<<<dim3((n + 31) / 32, (rp + 31) / 32, L), 256, 0, st>>>(static_cast<const uint16_t*>(p.B), bt, r, n, rp);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-      UpArgs y{};
+      UpArgs y = up_args(p);
       y.H = dh;
+      y.splits = sd;
       y.W = reinterpret_cast<const uint8_t*>(bt);
-      y.index = p.index;
-      y.scale = p.scale;
-      y.base = static_cast<const uint8_t*>(p.base);
-      y.Y = static_cast<uint8_t*>(p.Y);
-      y.M = p.M;
-      y.L = L;
       y.d = n;
-      y.r = y.ld = y.rp = rp;  // (the padding is zeros on both sides)
-      y.ranks = r;
-      y.splits = sd.count;
+      y.r = y.ld = rp;  // (the padding is zeros on both sides)
       if ((e = up<TY>(y, st)) != hipSuccess) return e;
     }
   }
@@ -744,26 +882,22 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   q.L = L;
   q.r = r;
   q.rp = rp;
-  q.P = static_cast<const uint8_t*>(p.dY);
-  q.H = h;
-  q.F = d;
-  q.splits = sh.count;
-  if ((e = sums<TY, true>(q, sum_parts(p.M, L, d), p.out_dtype, p.dA, parts, st)) != hipSuccess) return e;
-  q.P = static_cast<const uint8_t*>(p.X);
-  q.H = dh;
-  q.F = n;
-  q.splits = sd.count;
-  return sums<TY, false>(q, sum_parts(p.M, L, n), p.out_dtype, p.dB, parts, st);
+  q.of[0] = Sum{dY, h, p.dA, d, sh};
+  q.of[1] = Sum{X, dh, p.dB, n, sd};
+  return sums<TY>(q, sum_parts(p.M, L, d, n), p.out_dtype, reinterpret_cast<float*>(ws + w.parts), st);
 }
 
 }  // namespace
 
 // Blocks of the largest launch: a grid holds less than 2^32 work-items.
 bool adapters_fit(int64_t M, int64_t d, int64_t n, int64_t r) {
-  const int64_t tiles = M <= kSlotRows ? M + 15 : (M + 31) / 32, widest = d > n ? d : n;
-  const int64_t ups = tiles * ((widest + 63) / 64 < 32 ? (widest + 63) / 64 : (widest + 511) / 512 + 32);
-  const int64_t downs = tiles * ((r + 15) / 16) * 16;
-  return (ups > downs ? ups : downs) / 4 < (int64_t(1) << 24) - 1;
+  const int64_t slots = M < 16 ? (M < 1 ? 1 : M) : 16;
+  const int64_t tiles = M <= kSlotRows ? (M + 15) / 16 * slots : (M + 31) / 32, widest = d > n ? d : n;
+  const int64_t chunk = up_chunk(tiles, widest);
+  const int64_t ups = tiles * ((widest + chunk - 1) / chunk) / 4 + 1, downs = tiles * ((r + 15) / 16) * 8;
+  const int64_t turns = (d + 31) / 32 * ((r + 31) / 32) + (n + 31) / 32 * ((r + 31) / 32);
+  const int64_t most = int64_t(1) << 32;
+  return ups * 256 < most && (M <= kSlotRows ? downs : tiles) * 64 * kDownWaves < most && turns < (int64_t(1) << 31);
 }
 
 size_t adapters_ws_bytes(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
