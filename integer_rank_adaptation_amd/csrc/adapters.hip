@@ -8,31 +8,12 @@
 // factors' gradients.  h stays in binary32; where it meets 16-bit weights on the matrix cores it
 // goes as a sum of two 16-bit numbers (16 or more significant bits, against the outputs' 8 or
 // 11), and in the sums over tokens, whose results may be binary32, as a sum of three (24 bits).
-#include "device_common.h"
-#include "intlora_internal.h"
+#include "gemm_tile.h"
 
 namespace intlora {
 
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef short v4s __attribute__((ext_vector_type(4)));
-typedef uint32_t u4i __attribute__((ext_vector_type(4)));
-typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-typedef float f2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) v4s* lds_v4s_t;
-
-enum { T_BF16 = 0, T_FP16 = 1, T_FP32 = 2 };
-
-constexpr uint32_t kOOB = 0x80000000u;  // a buffer offset past every record: the lane reads zeros
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
-}
 __device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t r, uint32_t offset) {
   return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
 }
@@ -45,12 +26,7 @@ __device__ __forceinline__ v4f mfma(v4i rows, v4i cols, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, rows), __builtin_bit_cast(h8, cols), c, 0, 0, 0);
 }
 
-// Two floats to 16 bits each (round to nearest even), and back.
-template <int TY>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  if (TY == T_FP16) return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){x, y}, h2));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){x, y}, bf2));
-}
+// Two 16-bit numbers of a word.
 template <int TY>
 __device__ __forceinline__ f2 unpack2(uint32_t v) {
   if (TY == T_FP16) return __builtin_convertvector(__builtin_bit_cast(h2, v), f2);
@@ -66,7 +42,7 @@ __device__ __forceinline__ float top_bf16(float v) { return __uint_as_float(__fl
 // ---- the adapters of a tile of 16 TT token rows
 // Lane l holds the adapters of tokens 16 tt + l % 16 (-1: none).
 template <int TT>
-struct Tile {
+struct Ids {
   int id[TT];
   __device__ __forceinline__ void read(const int32_t* __restrict__ index, int64_t t0, int64_t M, int L) {
     const int fr = threadIdx.x & 15;
@@ -85,6 +61,20 @@ struct Tile {
       if (m) return __builtin_amdgcn_readlane(id[i], __builtin_ctzll(m));
     }
     return -1;
+  }
+  // Takes the adapters of the tile in turn: the one `skip` further on, those in front dropped; -1 when
+  // there is none.
+  __device__ __forceinline__ int next(int skip) {
+    for (;;) {
+      const int a = first();
+      if (a < 0 || skip-- == 0) return a;
+      drop(a);
+    }
+  }
+  __device__ __forceinline__ void drop(int a) {
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+      if (id[i] == a) id[i] = -1;
   }
   // The adapter of token `slot` (of the first 16) if no earlier one of these has the same, else -1.
   __device__ __forceinline__ int leader(int slot) const {
@@ -106,105 +96,179 @@ struct DownArgs {
   const int32_t* index;
   int64_t M;
   int L, r, rp;
-  int slots;  // 0: a block takes all adapters of its tile in turn; else one block per token of a tile of 16
+  int slots;  // blocks of a tile
 };
 
-// A block computes 16 TT tokens x 16 RT ranks over one split of the columns: its eight waves take
-// runs of 64 columns in turn, and their sums meet in LDS, where each wave adds the eight parts of
-// a tile in order.  Lane l holds token l % 16 and ranks 4 (l / 16) + 0 .. 3 of a tile.  Rows of
-// other adapters read as zeros and are not written.
+// For few tokens: a block for each token of a tile of 16 and each 16 ranks, where the token is the
+// first of its adapter in the tile: it takes all of that adapter's tokens there.  Its eight waves take runs
+// of 64 columns in turn, and their sums meet in LDS, where they are added in order.  Lane l holds
+// token l % 16 and ranks 4 (l / 16) + 0 .. 3.  Rows of other adapters read as zeros and are not
+// written.
 constexpr int kDownWaves = 8;
 
-template <int TY, int TT, int RT>
-__global__ void __launch_bounds__(64 * kDownWaves) k_down(const DownArgs p) {
-  constexpr int PASS = TT * RT > 8 ? 8 / TT : RT;  // rank tiles whose sums LDS holds at a time
-  __shared__ __attribute__((aligned(16))) float sums[kDownWaves][TT * PASS][256];
+template <int TY>
+__global__ void __launch_bounds__(64 * kDownWaves) k_down_few(const DownArgs p) {
+  __shared__ __attribute__((aligned(16))) float sums[kDownWaves][256];
   const Down& of = p.of[blockIdx.y];
   const int lane = threadIdx.x & 63, fr = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int groups = (p.rp + 16 * RT - 1) / (16 * RT);
-  const uint32_t per_tile = of.splits * groups * (p.slots ? p.slots : 1);
-  const int64_t tile = blockIdx.x / per_tile, t0 = tile * 16 * TT;
-  if (t0 >= p.M) return;
-  int rest = (int)(blockIdx.x - tile * per_tile);
+  const uint32_t groups = p.rp / 16;
+  uint32_t rest = blockIdx.x;
   const int split = rest % of.splits;
   rest /= of.splits;
-  const int g0 = rest % groups * 16 * RT, slot = rest / groups;
-  Tile<TT> tl;
+  const int g0 = rest % groups * 16;
+  rest /= groups;
+  const int64_t t0 = (int64_t)(rest / p.slots) * 16;
+  if (t0 >= p.M) return;
+  Ids<1> tl;
   tl.read(p.index, t0, p.M, p.L);
-  const int rows = p.M - t0 < 16 * TT ? (int)(p.M - t0) : 16 * TT;
+  const int a = __builtin_amdgcn_readfirstlane(tl.leader(rest % p.slots));
+  if (a < 0) return;
+  const int rows = p.M - t0 < 16 ? (int)(p.M - t0) : 16;
   const uint32_t ld = (uint32_t)of.n * 2;
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(of.X + t0 * ld, (int64_t)rows * ld);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(of.W + (int64_t)a * p.r * ld, (int64_t)p.r * ld);
+  const uint32_t ox = tl.id[0] == a ? fr * ld : kOOB, ow = g0 + fr < p.r ? (g0 + fr) * ld : kOOB;
+  // (lane q: 16 bytes each at 8 q and 32 + 8 q of a run; four runs in flight)
+  constexpr int U = 8;
   const int first = 64 * (wave + kDownWaves * split), step = 64 * kDownWaves * of.splits;
-  for (int a = p.slots ? tl.leader(slot) : tl.first(); a >= 0; a = tl.first()) {
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(of.W + (int64_t)a * p.r * ld, (int64_t)p.r * ld);
-    uint32_t ox[TT], ow[RT];
+  v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int k = first; k < of.n; k += U / 2 * step) {
+    v4i x[U], w[U];
 #pragma unroll
-    for (int i = 0; i < TT; ++i) ox[i] = tl.id[i] == a ? (16 * i + fr) * ld : kOOB;
+    for (int u = 0; u < U; ++u) {
+      const int c = k + u / 2 * step + 32 * (u & 1) + 8 * q;
+      const uint32_t o = c < of.n ? 2u * c : kOOB;
+      w[u] = load16(rw, (ow | o) & kOOB ? kOOB : ow + o);
+      x[u] = load16(rx, (ox | o) & kOOB ? kOOB : ox + o);
+    }
 #pragma unroll
-    for (int j = 0; j < RT; ++j) ow[j] = g0 + 16 * j + fr < p.r ? (g0 + 16 * j + fr) * ld : kOOB;
-    v4f acc[TT][RT];
+    for (int u = 0; u < U; ++u) acc = mfma<TY>(w[u], x[u], acc);
+  }
+  *reinterpret_cast<v4f*>(&sums[wave][4 * lane]) = acc;
+  __syncthreads();
+  if (wave != 0 || tl.id[0] != a) return;
 #pragma unroll
-    for (int i = 0; i < TT; ++i)
+  for (int w = 1; w < kDownWaves; ++w) acc += *reinterpret_cast<const v4f*>(&sums[w][4 * lane]);
+  *reinterpret_cast<v4f*>(of.H + (split * p.M + t0 + fr) * p.rp + g0 + 4 * q) = acc;
+}
+
+// For more tokens: a block computes 32 tokens x 16 RT ranks over one split of the columns.  Stages of
+// 256 bytes of the rows go through a ring of three LDS buffers filled by direct loads of 4 rows
+// x 256 bytes (fragments straight from memory, 16 pieces of 64 bytes a load, took twice as long);
+// each of the four waves takes a quarter of a stage, and their sums meet in LDS, where they are
+// added in order.  A place of a tile's adapters each: kSlots blocks take them in turn.
+// MEASURED_DOWN
+template <int RT_>
+struct DownTile {
+  static constexpr int RT = RT_, ROWS = 32 + 16 * RT, RING = 3, STAGE = ROWS * 256;
+  static constexpr int LOADS = 2 + RT;  // direct loads of a wave and stage
+  static constexpr int LDS = RING * STAGE;
+  static_assert(4 * 2 * RT * 1024 <= LDS && LDS <= 160 * 1024, "the sums take the ring's place");
+};
+
+template <int TY, class C>
+__global__ void __launch_bounds__(256) k_down(const DownArgs p) {
+  constexpr int RT = C::RT;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const Down& of = p.of[blockIdx.y];
+  const int lane = threadIdx.x & 63, fr = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tiles = (uint32_t)((p.M + 31) / 32);
+  uint32_t rest = blockIdx.x;  // slots outermost: where tiles have one adapter, only the first slot works
+  const int split = rest % of.splits;
+  rest /= of.splits;
+  const int slot = rest / tiles;
+  if (slot >= p.slots) return;
+  const int64_t t0 = (int64_t)(rest - slot * tiles) * 32;
+  Ids<2> tl;
+  tl.read(p.index, t0, p.M, p.L);
+  const int rows = p.M - t0 < 32 ? (int)(p.M - t0) : 32;
+  const int ld = of.n * 2, stages = (ld + 255) / 256, mine = stages > split ? (stages - split + of.splits - 1) / of.splits : 0;
+  // The blocks of an XCD (each eighth one) start at different stages: rows are a power of two of bytes
+  // apart as a rule, and blocks at the same columns would all be at the same few channels.
+  const int turn = mine > 0 ? (int)((blockIdx.x >> 3) % mine) : 0;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
+  // Lane l of a load: row l / 16 of its four, whose 16-byte chunk c lies at c ^ row % 16.
+  uint32_t ow[RT];
+  int cx[2], cw[RT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j) {
+    const int row = 4 * (wave * RT + j) + q;
+    cw[j] = 16 * (fr ^ (row & 15));
+    ow[j] = row < p.r ? row * ld + cw[j] : kOOB;
+  }
+  int idr[2];
+#pragma unroll
+  for (int l = 0; l < 2; ++l) {
+    const int row = 8 * wave + 4 * l + q;
+    cx[l] = 16 * (fr ^ (row & 15));
+    const int lo = __shfl(tl.id[0], row & 15), hi = __shfl(tl.id[1], row & 15);
+    idr[l] = row < 16 ? lo : hi;
+  }
+  for (int f = tl.next(slot); f >= 0; f = tl.next(p.slots - 1)) {
+    const int a = __builtin_amdgcn_readfirstlane(f);
+    const uint8_t *px = of.X + t0 * ld, *pw = of.W + (int64_t)a * p.r * ld;
+    auto issue = [&](int i, int place) {  // (stages past the last: loads of nothing, so that counts stay)
+      const int at = i < mine ? (i + turn < mine ? i + turn : i + turn - mine) * of.splits + split : stages;
+      const int k0 = at * 256, left = ld - k0;
+      const rsrc_t rx = make_desc(px + k0, rows * ld - k0), rw = make_desc(pw + k0, p.r * ld - k0);
+      const uint32_t S = lds0 + place * C::STAGE;
+#pragma unroll
+      for (int l = 0; l < 2; ++l) {
+        const int row = 8 * wave + 4 * l + q;
+        direct_load16(rx, S + (2 * wave + l) * 1024, idr[l] == a && cx[l] < left ? row * ld + cx[l] : kOOB);
+      }
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+        direct_load16(rw, S + 8192 + (wave * RT + j) * 1024, cw[j] < left ? ow[j] : kOOB);
+    };
+    v4f acc[2][RT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < RT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    // Two runs are in flight at a time (lane q: 16 bytes each at 8 q and 32 + 8 q of a run).  Runs past
-    // the last read zeros.
-    struct Run {
-      v4i x[2][TT], w[2][RT];
-    };
-    auto load = [&](int k, Run& f) {
+    issue(0, 0);
+    issue(1, 1);
+    int place = 0;
+    const uint32_t at = fr * 256 + (((4 * wave + q) ^ fr) << 4);
+    for (int i = 0; i < mine; ++i) {
+      wait_loads<C::LOADS>();  // this stage has landed, and every wave is done with the one before
+      __builtin_amdgcn_s_barrier();
+      __asm__ volatile("" ::: "memory");
+      const uint8_t* S = lds + place * C::STAGE + at;
+      issue(i + 2, place == 0 ? 2 : place - 1);
+      place = place == 2 ? 0 : place + 1;
+      v4i x[2], w[RT];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int c = k + 32 * u + 8 * q;
-        const uint32_t o = c < of.n ? 2u * c : kOOB;
+      for (int t = 0; t < 2; ++t) x[t] = *reinterpret_cast<const v4i*>(S + t * 4096);
 #pragma unroll
-        for (int i = 0; i < TT; ++i) f.x[u][i] = load16(rx, (ox[i] | o) & kOOB ? kOOB : ox[i] + o);
+      for (int j = 0; j < RT; ++j) w[j] = *reinterpret_cast<const v4i*>(S + 8192 + j * 4096);
 #pragma unroll
-        for (int j = 0; j < RT; ++j) f.w[u][j] = load16(rw, (ow[j] | o) & kOOB ? kOOB : ow[j] + o);
-      }
-    };
-    auto add = [&](const Run& f) {
+      for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < TT; ++i)
-#pragma unroll
-          for (int j = 0; j < RT; ++j) acc[i][j] = mfma<TY>(f.w[u][j], f.x[u][i], acc[i][j]);
-    };
-    Run f0, f1;
-    load(first, f0);
-    for (int k = first; k < of.n; k += 2 * step) {
-      load(k + step, f1);
-      add(f0);
-      load(k + 2 * step, f0);
-      add(f1);
+        for (int t = 0; t < 2; ++t) acc[t][j] = mfma<TY>(w[j], x[t], acc[t][j]);
     }
+    wait_loads<0>();
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+    v4f* sums = reinterpret_cast<v4f*>(lds);
 #pragma unroll
-    for (int g = 0; g < RT; g += PASS) {
-      if (g0 + 16 * g >= p.rp) break;
-      __syncthreads();
+    for (int z = 0; z < 2 * RT; ++z) sums[(wave * 2 * RT + z) * 64 + lane] = acc[z & 1][z >> 1];
+    __syncthreads();
 #pragma unroll
-      for (int i = 0; i < TT; ++i)
+    for (int y = 0; y < 2 * RT; y += 4) {
+      const int z = y + wave;  // this wave's tile
+      if (z >= 2 * RT) break;
+      v4f s = sums[z * 64 + lane];
 #pragma unroll
-        for (int j = 0; j < PASS; ++j) *reinterpret_cast<v4f*>(&sums[wave][i * PASS + j][4 * lane]) = acc[i][g + j];
-      __syncthreads();
-#pragma unroll
-      for (int y = 0; y < TT * PASS; y += kDownWaves) {
-        const int z = y + wave, i = z / PASS, j = z % PASS;  // this wave's tile
-        if (z >= TT * PASS) break;
-        v4f s = *reinterpret_cast<const v4f*>(&sums[0][z][4 * lane]);
-#pragma unroll
-        for (int w = 1; w < kDownWaves; ++w) s += *reinterpret_cast<const v4f*>(&sums[w][z][4 * lane]);
-        const int id = TT == 1 || i == 0 ? tl.id[0] : tl.id[TT - 1];
-        if (id == a && g0 + 16 * (g + j) < p.rp)
-          *reinterpret_cast<v4f*>(of.H + (split * p.M + t0 + 16 * i + fr) * p.rp + g0 + 16 * (g + j) + 4 * q) = s;
-      }
+      for (int w = 1; w < 4; ++w) s += sums[(w * 2 * RT + z) * 64 + lane];
+      const int i = z & 1, g = 16 * (z >> 1);
+      if ((i ? tl.id[1] : tl.id[0]) == a && g < p.rp)
+        *reinterpret_cast<v4f*>(of.H + (split * p.M + t0 + 16 * i + fr) * p.rp + g + 4 * q) = s;
     }
-    if (p.slots) return;
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
-      if (tl.id[i] == a) tl.id[i] = -1;
+    __syncthreads();
+    tl.drop(a);
   }
 }
 
@@ -219,7 +283,7 @@ struct UpArgs {
   int L, d, r, ld, rp, splits;
   int ranks;            // numbers of a row of H that count
   int slots;            // as k_down
-  int chunk;            // output columns of a wave (a multiple of 32)
+  int chunk;            // output columns of a block (a multiple of 128)
 };
 
 // Eight numbers of a weight row from number k on; zeros past the row's r.
@@ -235,27 +299,97 @@ __device__ __forceinline__ v4i row8(const uint16_t* __restrict__ row, int k, int
   return v4i{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
 }
 
-// Y = base + s_a W_a h.  A wave takes 16 TT tokens and 32 columns at a time.  Row m of the matrix
-// instruction's tile u is column 8 (m / 4) + 4 u + m % 4, so lane l ends up with columns
-// 8 (l / 16) + 0 .. 7 of token l % 16, and a row is read and written in whole runs of 64 bytes.  The
-// next columns' weights are loaded while these are at work, the first ones before h is there.
+// A token row's h, scaled, as the operand of the matrix cores: the sum of two 16-bit numbers each,
+// and what to multiply the sums with.  Lane l: token l % 16, ranks 32 c + 8 (l / 16) + 0 .. 7.
 // KT: steps of 32 of the rank.
-template <int TY, int TT, int KT, bool WIDE>
-__global__ void __launch_bounds__(256) k_up(const UpArgs p) {
+template <int TY, int KT>
+struct Low {
+  v4i hi[KT], lo[KT];
+  float back;
+
+  __device__ __forceinline__ void read(const UpArgs& p, int64_t t, bool mine, float s) {
+    const int q = (threadIdx.x & 63) >> 4;
+    float v[KT][8];
+#pragma unroll
+    for (int c = 0; c < KT; ++c) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[c][e] = 0.f;
+      const int k = 32 * c + 8 * q;
+      if (!mine || k >= p.rp) continue;
+      const float* h = p.H + t * p.rp + k;
+#pragma unroll 4
+      for (int z = 0; z < p.splits; ++z) {
+        const float4 *o = reinterpret_cast<const float4*>(h + z * p.M * p.rp), x = o[0], y = o[1];
+        v[c][0] += x.x, v[c][1] += x.y, v[c][2] += x.z, v[c][3] += x.w;
+        v[c][4] += y.x, v[c][5] += y.y, v[c][6] += y.z, v[c][7] += y.w;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[c][e] = k + e < p.ranks ? v[c][e] * s : 0.f;  // (an infinite x leaves NaN past them)
+    }
+    // fp16: a power of two per token brings its largest finite |h| into [1/2, 1)
+    back = 1.f;
+    if (TY == T_FP16) {
+      float m = 0.f;
+#pragma unroll
+      for (int c = 0; c < KT; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, finite(v[c][e]) ? fabsf(v[c][e]) : 0.f);
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      if (m > 0.f) {
+        int e = (int)(__float_as_uint(m) >> 23) - 126;  // m < 2^e (subnormals: e = -126)
+        e = e < -100 ? -100 : e > 126 ? 126 : e;
+        back = __uint_as_float((uint32_t)(e + 127) << 23);
+        const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int c = 0; c < KT; ++c)
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[c][x] *= f;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < KT; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = v[c][2 * e], y = v[c][2 * e + 1];
+        uint32_t t2, b;
+        if (TY == T_FP16) {
+          t2 = pack2<T_FP16>(x, y);
+          const f2 w = unpack2<T_FP16>(t2);
+          b = pack2<T_FP16>(finite(w.x) ? x - w.x : 0.f, finite(w.y) ? y - w.y : 0.f);
+        } else {
+          const float tx = top_bf16(x), ty = top_bf16(y);
+          t2 = pack2<T_BF16>(tx, ty);
+          b = pack2<T_BF16>(finite(x) ? x - tx : 0.f, finite(y) ? y - ty : 0.f);
+        }
+        hi[c][e] = (int)t2;
+        lo[c][e] = (int)b;
+      }
+  }
+};
+
+// Y = base + s_a W_a h.  Row m of the matrix instruction's tile u is column 8 (m / 4) + 4 u + m % 4,
+// so lane l ends up with columns 8 (l / 16) + 0 .. 7 of token l % 16.
+//
+// For few tokens: a block for each token of a tile of 16 (as k_down_few), its four waves 32 columns
+// in turn.  Bound by the factors' bytes: the next columns' weights are loaded while these are at
+// work, the first ones before h is there.
+template <int TY, int KT, bool WIDE>
+__global__ void __launch_bounds__(256) k_up_few(const UpArgs p) {
   const int lane = threadIdx.x & 63, fr = lane & 15, q = lane >> 4;
-  const int chunks = (p.d + p.chunk - 1) / p.chunk, slots = p.slots ? p.slots : 1;
-  const int64_t tiles = (p.M + 16 * TT - 1) / (16 * TT);
-  // the four waves of a block: neighbouring tiles (or tokens of a tile), the same columns
-  const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t block = unit / (tiles * slots);
-  if (block >= chunks) return;
-  const int64_t in = unit - block * tiles * slots, tile = in / slots;
-  const int64_t t0 = tile * 16 * TT;
-  Tile<TT> tl, all;
-  tl.read(p.index, t0, p.M, p.L);
-  all = tl;
-  const int c0 = (int)block * p.chunk, c1 = c0 + p.chunk < p.d ? c0 + p.chunk : p.d;
-  for (int a = p.slots ? tl.leader((int)(in - tile * slots)) : tl.first(); a >= 0; a = tl.first()) {
+  const uint32_t tokens = (uint32_t)((p.M + 15) / 16) * p.slots;
+  const uint32_t block = blockIdx.x / tokens, in = blockIdx.x - block * tokens;
+  const int slot = in % p.slots;
+  const int64_t t = (int64_t)(in / p.slots) * 16 + fr;  // this lane's token
+  Ids<1> tl;
+  tl.read(p.index, t - fr, p.M, p.L);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int first = (int)block * p.chunk + 32 * wave, c1 = (int)block * p.chunk + p.chunk;
+  // Steps of 128 columns; the blocks of an XCD start at different ones (as in k_down).
+  const int steps = p.chunk / 128, turn = (int)((blockIdx.x >> 3) % steps);
+  auto column = [&](int step) { return first + 128 * (step + turn < steps ? step + turn : step + turn - steps); };
+  const int a = __builtin_amdgcn_readfirstlane(tl.leader(slot));
+  if (a >= 0) {
     const uint16_t* W = reinterpret_cast<const uint16_t*>(p.W) + (int64_t)a * p.d * p.ld;
     struct Cols {
       v4i w[2][KT];
@@ -270,123 +404,212 @@ __global__ void __launch_bounds__(256) k_up(const UpArgs p) {
       }
     };
     Cols cur;
-    load(c0, cur);
-    const float s = p.scale[a];
-    v4i hi[TT][KT], lo[TT][KT];
-    float back[TT];
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      float v[KT][8];
-      const bool mine = tl.id[i] == a;
-#pragma unroll
-      for (int c = 0; c < KT; ++c) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[c][e] = 0.f;
-        const int k = 32 * c + 8 * q;
-        if (!mine || k >= p.rp) continue;
-        const float* h = p.H + (t0 + 16 * i + fr) * p.rp + k;
-#pragma unroll 4
-        for (int z = 0; z < p.splits; ++z) {
-          const float4 *o = reinterpret_cast<const float4*>(h + z * p.M * p.rp), x = o[0], y = o[1];
-          v[c][0] += x.x, v[c][1] += x.y, v[c][2] += x.z, v[c][3] += x.w;
-          v[c][4] += y.x, v[c][5] += y.y, v[c][6] += y.z, v[c][7] += y.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[c][e] = k + e < p.ranks ? v[c][e] * s : 0.f;  // (an infinite x leaves NaN past them)
-      }
-      // fp16: a power of two per token brings its largest finite |h| into [1/2, 1)
-      back[i] = 1.f;
-      if (TY == T_FP16) {
-        float m = 0.f;
-#pragma unroll
-        for (int c = 0; c < KT; ++c)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, finite(v[c][e]) ? fabsf(v[c][e]) : 0.f);
-        m = fmaxf(m, __shfl_xor(m, 16));
-        m = fmaxf(m, __shfl_xor(m, 32));
-        if (m > 0.f) {
-          int e = (int)(__float_as_uint(m) >> 23) - 126;  // m < 2^e (subnormals: e = -126)
-          e = e < -100 ? -100 : e > 126 ? 126 : e;
-          back[i] = __uint_as_float((uint32_t)(e + 127) << 23);
-          const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-          for (int c = 0; c < KT; ++c)
-#pragma unroll
-            for (int x = 0; x < 8; ++x) v[c][x] *= f;
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < KT; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = v[c][2 * e], y = v[c][2 * e + 1];
-          uint32_t t, b;
-          if (TY == T_FP16) {
-            t = pack2<T_FP16>(x, y);
-            const f2 w = unpack2<T_FP16>(t);
-            b = pack2<T_FP16>(finite(w.x) ? x - w.x : 0.f, finite(w.y) ? y - w.y : 0.f);
-          } else {
-            const float tx = top_bf16(x), ty = top_bf16(y);
-            t = pack2<T_BF16>(tx, ty);
-            b = pack2<T_BF16>(finite(x) ? x - tx : 0.f, finite(y) ? y - ty : 0.f);
-          }
-          hi[i][c][e] = (int)t;
-          lo[i][c][e] = (int)b;
-        }
-    }
-    for (int n0 = c0; n0 < c1; n0 += 32) {
-      const int col = n0 + 8 * q;
-      u4i b[TT];
-#pragma unroll
-      for (int i = 0; i < TT; ++i) {
-        b[i] = u4i{0, 0, 0, 0};
-        if (p.base && tl.id[i] == a && col < p.d)
-          b[i] = *reinterpret_cast<const u4i*>(p.base + 2 * ((t0 + 16 * i + fr) * p.d + col));
-      }
+    load(column(0), cur);
+    const bool mine = tl.id[0] == a;
+    Low<TY, KT> h;
+    h.read(p, t, mine, p.scale[a]);
+    for (int step = 0; step < steps; ++step) {
+      const int col = column(step) + 8 * q;
+      u4i b = u4i{0, 0, 0, 0};
+      if (p.base && mine && col < p.d) b = *reinterpret_cast<const u4i*>(p.base + 2 * (t * p.d + col));
       Cols next;
-      load(n0 + 32 < c1 ? n0 + 32 : p.d, next);
-      v4f acc[TT][2];
+      load(step + 1 < steps ? column(step + 1) : p.d, next);
+      __builtin_amdgcn_sched_barrier(0);
+      v4f acc[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u) {
+        acc[u] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-          acc[i][u] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < KT; ++c) {
-            acc[i][u] = mfma<TY>(cur.w[u][c], lo[i][c], acc[i][u]);
-            acc[i][u] = mfma<TY>(cur.w[u][c], hi[i][c], acc[i][u]);
-          }
+        for (int c = 0; c < KT; ++c) {
+          acc[u] = mfma<TY>(cur.w[u][c], h.lo[c], acc[u]);
+          acc[u] = mfma<TY>(cur.w[u][c], h.hi[c], acc[u]);
         }
-#pragma unroll
-      for (int i = 0; i < TT; ++i) {
-        if (tl.id[i] != a || col >= p.d) continue;
+      }
+      if (mine && col < p.d) {
         u4i y;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const f2 f = unpack2<TY>(b[i][e]);
-          const v4f& t = acc[i][e / 2];
-          y[e] = pack2<TY>(f.x + t[2 * (e & 1)] * back[i], f.y + t[2 * (e & 1) + 1] * back[i]);
+          const f2 f = unpack2<TY>(b[e]);
+          const v4f& v = acc[e / 2];
+          y[e] = pack2<TY>(f.x + v[2 * (e & 1)] * h.back, f.y + v[2 * (e & 1) + 1] * h.back);
         }
-        *reinterpret_cast<u4i*>(p.Y + 2 * ((t0 + 16 * i + fr) * p.d + col)) = y;
+        *reinterpret_cast<u4i*>(p.Y + 2 * (t * p.d + col)) = y;
       }
       cur = next;
     }
-    if (p.slots) break;
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
-      if (tl.id[i] == a) tl.id[i] = -1;
   }
   // Rows without an adapter: the base's (nothing to do in place).
-  if (p.base == p.Y || (p.slots && in - tile * slots != 0)) return;
-  for (int col = c0 + 8 * q; col < c1; col += 32)
+  if (p.base == p.Y || slot != 0 || tl.id[0] >= 0 || t >= p.M) return;
+  for (int col = first + 8 * q; col < c1 && col < p.d; col += 128) {
+    u4i b = u4i{0, 0, 0, 0};
+    if (p.base) b = *reinterpret_cast<const u4i*>(p.base + 2 * (t * p.d + col));
+    *reinterpret_cast<u4i*>(p.Y + 2 * (t * p.d + col)) = b;
+  }
+}
+
+// Rows of `chunks` 16-byte chunks in LDS, chunk c of row m at c ^ turned(m): the 16 lanes that read a
+// chunk of rows 0 .. 15 at a time are on different banks (a power of two of chunks; rows of other
+// lengths spread by themselves).
+__device__ __forceinline__ int turned(int m, int chunks) {
+  return chunks == 16 ? m : chunks == 8 ? m >> 1 : chunks == 4 ? m >> 2 : chunks == 2 ? m >> 3 : 0;
+}
+
+// For more tokens: a block takes 64 tokens (kSlots blocks, as k_down), 16 each wave, and 128 columns at
+// a time.  The columns' weights go through two LDS buffers filled by direct loads, for all four
+// waves.  Here the tokens are the matrix instruction's rows, and row m of the weights' tile u is
+// column 8 m + u: a lane ends up with columns 8 (l % 16) + 0 .. 7 of tokens 4 (l / 16) + 0 .. 3, so
+// that rows are read and written in runs of 256 bytes with no step through LDS.  The next columns'
+// rows of the base are loaded while these are at work.
+// MEASURED_UP
+template <int TY, int KT>
+__global__ void __launch_bounds__(256) k_up(const UpArgs p) {
+  constexpr int NL = 2 * KT, BUF = 4 * NL * 1024;  // direct loads of a wave; bytes of a buffer
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * BUF];
+  const int lane = threadIdx.x & 63, fr = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lots = (uint32_t)((p.M + 63) / 64), chunks = (p.d + p.chunk - 1) / p.chunk;
+  const uint32_t slot = blockIdx.x / (lots * chunks), in = blockIdx.x - slot * (lots * chunks);
+  const uint32_t block = in / lots, lot = in - block * lots;
+  const int64_t t0 = (int64_t)lot * 64 + 16 * wave;  // the wave's first token
+  Ids<4> tl;
+  tl.read(p.index, (int64_t)lot * 64, p.M, p.L);
+  const int id = wave == 0 ? tl.id[0] : wave == 1 ? tl.id[1] : wave == 2 ? tl.id[2] : tl.id[3];
+  const int ldo = 2 * p.d, rows = p.M - t0 >= 16 ? 16 : p.M > t0 ? (int)(p.M - t0) : 0;
+  int idt[4];  // of this lane's tokens of the outputs
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      const int64_t t = t0 + 16 * i + fr;
-      if (all.id[i] >= 0 || t >= p.M) continue;
-      u4i b = u4i{0, 0, 0, 0};
-      if (p.base) b = *reinterpret_cast<const u4i*>(p.base + 2 * (t * p.d + col));
-      *reinterpret_cast<u4i*>(p.Y + 2 * (t * p.d + col)) = b;
+  for (int e = 0; e < 4; ++e) idt[e] = __shfl(id, 4 * q + e);
+  const int64_t at = rows ? t0 * ldo : 0;
+  const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.Y + at, (int64_t)rows * ldo);
+  const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.base ? p.base + at : p.Y, p.base ? (int64_t)rows * ldo : 0);
+  const int c0 = (int)block * p.chunk, steps = p.chunk / 128, turn = (int)((blockIdx.x >> 3) % steps);
+  auto column = [&](int step) { return c0 + 128 * (step + turn < steps ? step + turn : step + turn - steps); };
+  auto place = [&](int a, int e, int col) {  // of eight columns in the rows; kOOB: not this adapter's
+    return idt[e] == a && col < p.d ? (uint32_t)((4 * q + e) * ldo + 2 * col) : kOOB;
+  };
+  // Weights in LDS: rows of `per` chunks of 16 bytes, row 16 u + m holds column 8 m + u, its chunk c at
+  // c ^ turned(m): the 16 rows of a fragment are on different banks.
+  const int per = p.ld / 8;
+  uint32_t wo[NL];
+#pragma unroll
+  for (int j = 0; j < NL; ++j) {
+    const int c = 64 * (wave * NL + j) + lane, R = c / per, m = R & 15;
+    wo[j] = R < 128 ? 16 * ((8 * m + (R >> 4)) * per + ((c - R * per) ^ turned(m, per))) : kOOB;
+  }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds + wave * NL * 1024;
+  struct Rows {
+    v4i v[4];
+  };
+  for (int f = tl.next((int)slot); f >= 0; f = tl.next(p.slots - 1)) {
+    const int a = __builtin_amdgcn_readfirstlane(f);
+    const uint8_t* W = p.W + (int64_t)a * p.d * p.ld * 2;
+    auto issue = [&](int step) {
+      const int col = step < steps ? column(step) : p.d;
+      const int64_t left = (int64_t)(p.d - col) * p.ld * 2;
+      const rsrc_t rw = make_desc(col < p.d ? W + (int64_t)col * p.ld * 2 : W, col < p.d ? (int)(left < 65536 ? left : 65536) : 0);
+#pragma unroll
+      for (int j = 0; j < NL; ++j) direct_load16(rw, lds0 + (step & 1) * BUF + 1024 * j, wo[j]);
+    };
+    auto fetch = [&](int step, Rows& b) {
+      const int col = step < steps ? column(step) + 8 * fr : p.d;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b.v[e] = load16(rb, place(a, e, col));
+    };
+    Rows b0, b1;
+    issue(0);
+    fetch(0, b0);
+    __builtin_amdgcn_sched_barrier(0);
+    Low<TY, KT> h;
+    float back[4];
+    h.read(p, t0 + fr, id == a, p.scale[a]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) back[e] = TY == T_FP16 ? __shfl(h.back, 4 * q + e) : 1.f;
+    auto one = [&](int step, Rows& cur, Rows& next) {
+      // this step's weights have landed (newer: its rows of the base and the last step's stores)
+      if (step == 0)
+        wait_loads<4>();
+      else
+        wait_loads<8>();
+      __builtin_amdgcn_s_barrier();
+      __asm__ volatile("" ::: "memory");
+      issue(step + 1);
+      fetch(step + 1, next);
+      __builtin_amdgcn_sched_barrier(0);
+      const uint8_t* S = lds + (step & 1) * BUF;
+      v4f acc[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        v4f t = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < KT; ++c) {
+          const int k = 4 * c + q;
+          const v4i w = k < per ? *reinterpret_cast<const v4i*>(S + 16 * ((16 * u + fr) * per + (k ^ turned(fr, per))))
+                                : v4i{0, 0, 0, 0};
+          t = mfma<TY>(h.lo[c], w, t);
+          t = mfma<TY>(h.hi[c], w, t);
+        }
+        acc[u] = t;
+      }
+      const int col = column(step) + 8 * fr;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        u4i y;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const f2 g = unpack2<TY>((uint32_t)cur.v[e][z]);
+          y[z] = pack2<TY>(g.x + acc[2 * z][e] * back[e], g.y + acc[2 * z + 1][e] * back[e]);
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(y, ry, place(a, e, col), 0, 0);
+      }
+    };
+    for (int step = 0; step < steps; step += 2) {
+      one(step, b0, b1);
+      if (step + 1 < steps) one(step + 1, b1, b0);
     }
+    wait_loads<0>();
+    __syncthreads();
+    tl.drop(a);
+  }
+  // Rows without an adapter: the base's (nothing to do in place).
+  if (p.base == p.Y || slot != 0) return;
+  for (int step = 0; step < steps; ++step) {
+    const int col = column(step) + 8 * fr;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t o = idt[e] < 0 && 4 * q + e < rows && col < p.d ? (uint32_t)((4 * q + e) * ldo + 2 * col) : kOOB;
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4i, load16(rb, o)), ry, o, 0, 0);
+    }
+  }
+}
+
+// Rows of `ld` numbers of rows of r, zeros behind them.
+__global__ void __launch_bounds__(256) k_pad(const uint16_t* __restrict__ in, uint16_t* __restrict__ out, int64_t units,
+                                             int r, int ld) {
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
+    const int per = ld / 8;
+    const int64_t row = u / per;
+    const v4i v = row8<false>(in + row * r, (int)(u - row * per) * 8, r);
+    *reinterpret_cast<v4i*>(out + u * 8) = v;
+  }
+}
+
+// Launches of kernels with more LDS than the default limit.
+template <class K>
+hipError_t allow_lds(K kernel, int bytes, int& ready_dev) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess || dev == ready_dev) return e;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) ready_dev = dev;
+  return e;
+}
+
+template <int TY, class C>
+hipError_t launch_down(const DownArgs& a, dim3 grid, hipStream_t st) {
+  static thread_local int ready_dev = -1;
+  const hipError_t e = allow_lds(&k_down<TY, C>, C::LDS, ready_dev);
+  if (e != hipSuccess) return e;
+  k_down<TY, C><<<grid, 256, C::LDS, st>>>(a);
+  return hipGetLastError();
 }
 
 // out[a] (cols x ldo) = in[a] (rows x cols) transposed, zeros from column `rows` on, of both factors.
@@ -655,7 +878,22 @@ __global__ void __launch_bounds__(256) k_parts(const PartsArgs p, int parts) {
   }
 }
 
-constexpr int64_t kSlotRows = 1024;  // up to here one block (wave) per token of a tile
+// Up to here a block for each token of a tile of 16 (every request an adapter of its own is the
+// common batch); from there on kSlots blocks for a tile of 32, so that a tile on the border of two
+// requests takes no longer than the others (8192 rows of 12 requests, 4096 x 4096, rank 64: h 48
+// us with one block a tile, SLOT_US with four).
+constexpr int64_t kTokenRows = 1024;
+constexpr int kSlots = 2;
+
+struct Slots {
+  int tt, slots;
+  int64_t tiles;
+  bool token;
+};
+Slots slots_of(int64_t M) {
+  if (M <= kTokenRows) return {1, M < 16 ? (M < 1 ? 1 : (int)M) : 16, (M + 15) / 16, true};
+  return {2, kSlots, (M + 31) / 32, false};
+}
 
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -663,8 +901,8 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 // Splits of k_down over n columns: where its blocks are fewer than the compute units, down to two
 // runs of 64 columns for each wave.
 int down_splits(int64_t M, int64_t n, int64_t r) {
-  const int64_t blocks = M <= kSlotRows ? M * ((r + 15) / 16) : (M + 31) / 32;
-  const int64_t most = n / (2 * 64 * kDownWaves);
+  const int64_t blocks = M <= kTokenRows ? M * ((r + 15) / 16) : (M + 31) / 32;
+  const int64_t most = M <= kTokenRows ? n / (2 * 64 * kDownWaves) : n / 1024;
   int64_t s = blocks > 0 ? 256 / blocks : 1;
   s = s > most ? most : s;
   return (int)(s > 8 ? 8 : s < 1 ? 1 : s);
@@ -690,57 +928,73 @@ Parts sum_parts(int64_t M, int64_t L, int64_t d, int64_t n) {
 template <int TY>
 hipError_t down(DownArgs a, int problems, hipStream_t st) {
   const int rt = a.rp / 16;
-  a.slots = a.M <= kSlotRows ? (a.M < 16 ? (int)a.M : 16) : 0;
-  const int tt = a.slots ? 1 : 2, per = a.slots ? 1 : rt > 4 ? 8 : rt > 2 ? 4 : rt;
+  const Slots sl = slots_of(a.M);
+  a.slots = sl.slots;
   int64_t blocks = 0;
   for (int i = 0; i < problems; ++i) {
-    const int64_t b = (a.M + 16 * tt - 1) / (16 * tt) * a.of[i].splits * ((rt + per - 1) / per) * (a.slots ? a.slots : 1);
+    const int64_t b = sl.tiles * sl.slots * a.of[i].splits * (sl.token ? rt : 1);
     blocks = b > blocks ? b : blocks;
   }
   const dim3 grid((unsigned)blocks, (unsigned)problems);
-  const int threads = 64 * kDownWaves;
-  if (a.slots)
-    k_down<TY, 1, 1><<<grid, threads, 0, st>>>(a);
-  else if (per == 1)
-    k_down<TY, 2, 1><<<grid, threads, 0, st>>>(a);
-  else if (per == 2)
-    k_down<TY, 2, 2><<<grid, threads, 0, st>>>(a);
-  else if (per == 4)
-    k_down<TY, 2, 4><<<grid, threads, 0, st>>>(a);
+  if (sl.token) {
+    k_down_few<TY><<<grid, 64 * kDownWaves, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  return rt == 1   ? launch_down<TY, DownTile<1>>(a, grid, st)
+         : rt == 2 ? launch_down<TY, DownTile<2>>(a, grid, st)
+         : rt <= 4 ? launch_down<TY, DownTile<4>>(a, grid, st)
+                   : launch_down<TY, DownTile<8>>(a, grid, st);
+}
+
+template <int TY, bool WIDE>
+hipError_t up_few(const UpArgs& a, dim3 grid, hipStream_t st) {
+  if (a.r <= 32)
+    k_up_few<TY, 1, WIDE><<<grid, 256, 0, st>>>(a);
+  else if (a.r <= 64)
+    k_up_few<TY, 2, WIDE><<<grid, 256, 0, st>>>(a);
   else
-    k_down<TY, 2, 8><<<grid, threads, 0, st>>>(a);
+    k_up_few<TY, 4, WIDE><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <int TY, int TT, bool WIDE>
-void up_kt(const UpArgs& a, dim3 grid, hipStream_t st) {
-  if (a.r <= 32)
-    k_up<TY, TT, 1, WIDE><<<grid, 256, 0, st>>>(a);
-  else if (a.r <= 64)
-    k_up<TY, TT, 2, WIDE><<<grid, 256, 0, st>>>(a);
-  else
-    k_up<TY, TT, 4, WIDE><<<grid, 256, 0, st>>>(a);
-}
-
-// Columns of a wave: at least 2048 waves where there are columns for them.
-int64_t up_chunk(int64_t tiles, int64_t d) {
-  int64_t chunk = 512;
-  while (chunk > 64 && tiles * ((d + chunk - 1) / chunk) < 2048) chunk /= 2;
+// Columns of a block: at least `want` working blocks where there are columns for them.
+int64_t up_chunk(int64_t tiles, int64_t d, int64_t want) {
+  int64_t chunk = 1024;
+  while (chunk > 128 && tiles * ((d + chunk - 1) / chunk) < want) chunk /= 2;
   return chunk;
 }
 
+// Rows of the factors need to be multiples of 8 for many tokens: others are padded first.
+bool up_pads(int64_t M, int64_t r) { return M > kTokenRows && r % 8 != 0; }
+
 template <int TY>
-hipError_t up(UpArgs a, hipStream_t st) {
-  a.slots = a.M <= kSlotRows ? (a.M < 16 ? (int)a.M : 16) : 0;
-  const int tt = a.slots ? 1 : 2;
-  const int64_t tiles = (a.M + 16 * tt - 1) / (16 * tt) * (a.slots ? a.slots : 1), chunk = up_chunk(tiles, a.d);
+hipError_t up(UpArgs a, uint16_t* pad, hipStream_t st) {
+  const Slots sl = slots_of(a.M);
+  a.slots = sl.slots;
+  if (sl.token) {
+    const int64_t chunk = up_chunk(a.M, a.d, 1024);
+    a.chunk = (int)chunk;
+    const dim3 grid((unsigned)(sl.tiles * sl.slots * ((a.d + chunk - 1) / chunk)));
+    return a.r % 8 == 0 && a.ld % 8 == 0 ? up_few<TY, true>(a, grid, st) : up_few<TY, false>(a, grid, st);
+  }
+  if (up_pads(a.M, a.r)) {
+    const int ld = (a.r + 7) / 8 * 8;
+    const int64_t units = (int64_t)a.L * a.d * (ld / 8), want = (units + 255) / 256;
+    k_pad<<<(unsigned)(want < 8192 ? want : 8192), 256, 0, st>>>(reinterpret_cast<const uint16_t*>(a.W), pad, units, a.r, ld);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.W = reinterpret_cast<const uint8_t*>(pad);
+    a.r = a.ld = ld;
+  }
+  const int64_t lots = (a.M + 63) / 64, chunk = up_chunk(lots, a.d, 512);
   a.chunk = (int)chunk;
-  const dim3 grid((unsigned)((tiles * ((a.d + chunk - 1) / chunk) + 3) / 4));
-  const bool wide = a.r % 8 == 0 && a.ld % 8 == 0;
-  if (a.slots)
-    wide ? up_kt<TY, 1, true>(a, grid, st) : up_kt<TY, 1, false>(a, grid, st);
+  const dim3 grid((unsigned)(lots * sl.slots * ((a.d + chunk - 1) / chunk)));
+  if (a.r <= 32)
+    k_up<TY, 1><<<grid, 256, 0, st>>>(a);
+  else if (a.r <= 64)
+    k_up<TY, 2><<<grid, 256, 0, st>>>(a);
   else
-    wide ? up_kt<TY, 2, true>(a, grid, st) : up_kt<TY, 2, false>(a, grid, st);
+    k_up<TY, 4><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -783,15 +1037,18 @@ hipError_t sums(SumArgs a, const Parts& z, int out_dtype, float* ws, hipStream_t
   return hipGetLastError();
 }
 
-// The workspace: h, and for the gradients dh, A and B transposed, and the parts of the sums.
+// The workspace: h, A padded, and for the gradients dh, A and B transposed, and the parts of the sums.
 struct Ws {
-  int64_t h, dh, at, bt, parts, bytes;
+  int64_t pad, dh, at, bt, parts, bytes;
 };
 Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   Ws w{};
   const int64_t rp = round16(r);
   int64_t at = up256(4 * M * rp * down_splits(M, n, r));
-  if (grads) {
+  if (!grads) {
+    w.pad = at;
+    at += up_pads(M, r) ? up256(2 * L * d * ((r + 7) / 8 * 8)) : 0;
+  } else {
     w.dh = at;
     at += up256(4 * M * rp * down_splits(M, d, r));
     w.at = at;
@@ -843,7 +1100,7 @@ hipError_t fwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   y.W = static_cast<const uint8_t*>(p.A);
   y.d = (int)p.d;
   y.r = y.ld = (int)p.r;
-  return up<TY>(y, st);
+  return up<TY>(y, reinterpret_cast<uint16_t*>(ws + carve(p.M, p.L, p.d, p.n, p.r, false).pad), st);
 }
 
 template <int TY>
@@ -872,7 +1129,7 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
       y.W = reinterpret_cast<const uint8_t*>(bt);
       y.d = n;
       y.r = y.ld = rp;  // (the padding is zeros on both sides)
-      if ((e = up<TY>(y, st)) != hipSuccess) return e;
+      if ((e = up<TY>(y, nullptr, st)) != hipSuccess) return e;
     }
   }
   SumArgs q{};
@@ -891,13 +1148,13 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
 
 // Blocks of the largest launch: a grid holds less than 2^32 work-items.
 bool adapters_fit(int64_t M, int64_t d, int64_t n, int64_t r) {
-  const int64_t slots = M < 16 ? (M < 1 ? 1 : M) : 16;
-  const int64_t tiles = M <= kSlotRows ? (M + 15) / 16 * slots : (M + 31) / 32, widest = d > n ? d : n;
-  const int64_t chunk = up_chunk(tiles, widest);
-  const int64_t ups = tiles * ((widest + chunk - 1) / chunk) / 4 + 1, downs = tiles * ((r + 15) / 16) * 8;
+  const Slots sl = slots_of(M);
+  const int64_t widest = d > n ? d : n, blocks = sl.tiles * sl.slots;
+  const int64_t ups = blocks * ((widest + 127) / 128 < 8 ? (widest + 127) / 128 : (widest + 1023) / 1024 + 8);
+  const int64_t downs = blocks * (sl.token ? 8 : 1) * 8;  // ranks, splits
   const int64_t turns = (d + 31) / 32 * ((r + 31) / 32) + (n + 31) / 32 * ((r + 31) / 32);
   const int64_t most = int64_t(1) << 32;
-  return ups * 256 < most && (M <= kSlotRows ? downs : tiles) * 64 * kDownWaves < most && turns < (int64_t(1) << 31);
+  return ups * 256 < most && downs * 64 * kDownWaves < most && turns < (int64_t(1) << 31);
 }
 
 size_t adapters_ws_bytes(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
