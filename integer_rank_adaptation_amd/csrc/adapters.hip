@@ -643,85 +643,122 @@ __global__ void __launch_bounds__(256) k_turn(const TurnArgs p) {
   }
 }
 
+// h and dh, scaled, as three bf16 numbers each (24 bits) for k_sums: planes x M x rp.  Rows without an
+// adapter are left out.
+struct Split {
+  const float* H;  // splits x M x rp
+  uint16_t* out;
+  int splits;
+};
+struct SplitArgs {
+  Split of[2];
+  const int32_t* index;
+  const float* scale;
+  int64_t M;
+  int L, rp;
+};
+__global__ void __launch_bounds__(256) k_split(const SplitArgs p) {
+  const Split& of = p.of[blockIdx.y];
+  const int per = p.rp / 4;
+  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x, t = u / per;
+  if (t >= p.M) return;
+  const int a = p.index[t];
+  if (a < 0 || a >= p.L) return;
+  const float s = p.scale[a];
+  float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int z = 0; z < of.splits; ++z) {
+    const float4 x = *reinterpret_cast<const float4*>(of.H + z * p.M * p.rp + 4 * u);
+    h.x += x.x, h.y += x.y, h.z += x.z, h.w += x.w;
+  }
+  float v[4] = {h.x * s, h.y * s, h.z * s, h.w * s};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    float t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      t[e] = top_bf16(v[e]);
+      v[e] = finite(v[e]) ? v[e] - t[e] : 0.f;
+    }
+    *reinterpret_cast<uint2*>(of.out + k * p.M * p.rp + 4 * u) = make_uint2(pack2<T_BF16>(t[0], t[1]), pack2<T_BF16>(t[2], t[3]));
+  }
+}
+
 struct Sum {
-  const uint8_t* P;  // M x F token rows (dY or X)
-  const float* H;    // splits x M x rp (h or dh)
-  void* out;         // L x F x r (dA) or L x r x F (dB)
-  int F, splits;
+  const uint8_t* P;   // M x F token rows (dY or X)
+  const uint16_t* H;  // 3 x M x rp (h or dh of k_split)
+  void* out;          // L x F x r (dA) or L x r x F (dB)
+  int F;
 };
 struct SumArgs {
   Sum of[2];             // dA, dB
   const int32_t* index;
-  const float* scale;
   int64_t M;
   int L, r, rp;
-  int blocks0;           // blocks of 64 columns of the first one
+  int blocks0;           // blocks of 128 columns of the first one
   int64_t per;           // tokens of a part
   int64_t numel[2];      // of the outputs: parts lie one after the other
 };
 
-// sum over an adapter's tokens of P_t h_t^T s_a.  A block takes 64 columns of P and all ranks: it
+// sum over an adapter's tokens of P_t h_t^T s_a.  A block takes 128 columns of P and all ranks: it
 // lists its adapter's tokens (of 2048 rows at a time, in order) and adds them T at a time, each
-// wave 16 columns x 16 RT ranks; the next ones are loaded meanwhile.  Both operands have the
-// contraction (tokens) in rows and leave LDS through the transposing reads.  h goes as three bf16
-// numbers; fp16 rows of P as two (exact).
+// wave 32 columns x 16 RT ranks; the next ones are loaded meanwhile.  Both operands have the
+// contraction (tokens) in rows and leave LDS through the transposing reads.  h is three bf16 numbers;
+// fp16 rows of P become two (exact).
+// MEASURED_SUMS
 template <int TY, int RT>
 struct SumLds {
   static constexpr int PP = TY == T_FP16 ? 2 : 1, T = RT == 8 ? 32 : 64;
-  static constexpr int PS = 64 + 8, HS = 16 * RT + 8;  // row strides (16-bit numbers)
+  static constexpr int F = 128, PS = F + 8, HS = 16 * RT + 8;  // row strides (16-bit numbers)
   static constexpr int kScan = 2048;
   uint16_t p[PP][T * PS];
   uint16_t h[3][T * HS];
-  int list[kScan + T];
+  uint16_t list[kScan + T];
   int counts[4];
 };
 
 template <int TY, int TO, int RT, bool RANK_LANES>
 __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64_t numel, int block, SumLds<TY, RT>& L) {
   using S = SumLds<TY, RT>;
-  constexpr int PP = S::PP, T = S::T, PS = S::PS, HS = S::HS;
-  constexpr int NP = T / 32, NH = T * RT / 64;  // 16-byte loads of a thread
+  constexpr int PP = S::PP, T = S::T, PS = S::PS, HS = S::HS, NT = S::F / 64;
+  constexpr int NP = T / 16, NH = (6 * T * RT + 255) / 256;  // 16-byte loads of a thread
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, fr = lane & 15, q = lane >> 4;
-  const int a = blockIdx.y, f0 = block * 64;
-  const float s = p.scale[a];
+  const int a = blockIdx.y, f0 = block * S::F;
   const int64_t tb = blockIdx.z * p.per, te = tb + p.per < p.M ? tb + p.per : p.M;
-  v4f acc[RT];
+  v4f acc[NT][RT];
 #pragma unroll
-  for (int j = 0; j < RT; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
-  u4i pv[NP];
-  float4 hv[NH];
+  for (int j = 0; j < NT * RT; ++j) acc[j / RT][j % RT] = v4f{0.f, 0.f, 0.f, 0.f};
+  struct Lot {
+    u4i p[NP], h[NH];
+  };
+  Lot lot;
+  int64_t t0 = tb;  // the list's rows count from here
 
-  // tokens tb + list[from .. from + n), n <= T: rows past n are zeros
+  // rows list[from .. n), at most T: zeros behind them
   auto fetch = [&](int from, int n) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int row = (tid >> 3) + 32 * i, c = (tid & 7) * 8;
-      pv[i] = u4i{0, 0, 0, 0};
-      if (row < n && f0 + c < of.F)
-        pv[i] = *reinterpret_cast<const u4i*>(of.P + 2 * ((tb + L.list[from + row]) * of.F + f0 + c));
+      const int row = (tid >> 4) + 16 * i, c = (tid & 15) * 8;
+      lot.p[i] = u4i{0, 0, 0, 0};
+      if (from + row < n && f0 + c < of.F)
+        lot.p[i] = *reinterpret_cast<const u4i*>(of.P + 2 * ((t0 + L.list[from + row]) * of.F + f0 + c));
     }
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
-      const int at = tid + 256 * i, row = at / (4 * RT), c = at % (4 * RT) * 4;
-      hv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row < n && c < p.rp) {
-        const float* src = of.H + (tb + L.list[from + row]) * p.rp + c;
-        for (int z = 0; z < of.splits; ++z) {
-          const float4 x = *reinterpret_cast<const float4*>(src + z * p.M * p.rp);
-          hv[i].x += x.x, hv[i].y += x.y, hv[i].z += x.z, hv[i].w += x.w;
-        }
-      }
+      const int at = tid + 256 * i, k = at / (2 * RT * T), in = at % (2 * RT * T), row = in / (2 * RT), c = in % (2 * RT) * 8;
+      lot.h[i] = u4i{0, 0, 0, 0};
+      if (k < 3 && from + row < n && c < p.rp)
+        lot.h[i] = *reinterpret_cast<const u4i*>(of.H + (k * p.M + t0 + L.list[from + row]) * p.rp + c);
     }
   };
   auto store = [&]() {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int at = ((tid >> 3) + 32 * i) * PS + (tid & 7) * 8;
+      const int at = ((tid >> 4) + 16 * i) * PS + (tid & 15) * 8;
       if (TY == T_FP16) {
         u4i t, b;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const f2 x = unpack2<T_FP16>(pv[i][e]);
+          const f2 x = unpack2<T_FP16>(lot.p[i][e]);
           const f2 y = f2{top_bf16(x.x), top_bf16(x.y)};
           t[e] = pack2<T_BF16>(y.x, y.y);
           b[e] = pack2<T_BF16>(finite(x.x) ? x.x - y.x : 0.f, finite(x.y) ? x.y - y.y : 0.f);
@@ -729,23 +766,13 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64
         *reinterpret_cast<u4i*>(&L.p[0][at]) = t;
         *reinterpret_cast<u4i*>(&L.p[PP - 1][at]) = b;
       } else {
-        *reinterpret_cast<u4i*>(&L.p[0][at]) = pv[i];
+        *reinterpret_cast<u4i*>(&L.p[0][at]) = lot.p[i];
       }
     }
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
-      const int at = tid + 256 * i, row = at / (4 * RT), c = at % (4 * RT) * 4;
-      float v[4] = {hv[i].x * s, hv[i].y * s, hv[i].z * s, hv[i].w * s};
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        float t[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          t[e] = top_bf16(v[e]);
-          v[e] = finite(v[e]) ? v[e] - t[e] : 0.f;
-        }
-        *reinterpret_cast<uint2*>(&L.h[k][row * HS + c]) = make_uint2(pack2<T_BF16>(t[0], t[1]), pack2<T_BF16>(t[2], t[3]));
-      }
+      const int at = tid + 256 * i, k = at / (2 * RT * T), in = at % (2 * RT * T), row = in / (2 * RT), c = in % (2 * RT) * 8;
+      if (k < 3) *reinterpret_cast<u4i*>(&L.h[k][row * HS + c]) = lot.h[i];
     }
   };
   auto frag = [&](const uint16_t* m, int stride, int row, int col) {  // rows row + 8 q + 0 .. 7 of column col + fr
@@ -757,9 +784,11 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64
   auto add = [&]() {
 #pragma unroll
     for (int t = 0; t < T; t += 32) {
-      v4i pf[PP];
+      v4i pf[NT][PP];
 #pragma unroll
-      for (int k = 0; k < PP; ++k) pf[k] = frag(L.p[k], PS, t, 16 * wave);
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int k = 0; k < PP; ++k) pf[i][k] = frag(L.p[k], PS, t, 32 * wave + 16 * i);
 #pragma unroll
       for (int j = 0; j < RT; ++j)
 #pragma unroll
@@ -767,25 +796,24 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64
           const v4i h = frag(L.h[k], HS, t, 16 * j);
 #pragma unroll
           for (int z = PP - 1; z >= 0; --z)
-            acc[j] = RANK_LANES ? mfma<T_BF16>(pf[z], h, acc[j]) : mfma<T_BF16>(h, pf[z], acc[j]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+              acc[i][j] = RANK_LANES ? mfma<T_BF16>(pf[i][z], h, acc[i][j]) : mfma<T_BF16>(h, pf[i][z], acc[i][j]);
         }
     }
   };
-  auto run = [&](int n) {  // whole lots of T tokens of the list, or (n < T) its last ones
+  auto run = [&](int n) {  // the first n of the list
     fetch(0, n);
-    for (int from = 0;;) {
+    for (int from = 0; from < n; from += T) {
       __syncthreads();
       store();
       __syncthreads();
-      from += T;
-      const bool more = from + T <= n;
-      if (more) fetch(from, T);
+      fetch(from + T, n);
+      __builtin_amdgcn_sched_barrier(0);
       add();
-      if (!more) break;
     }
   };
 
-  int have = 0;  // listed, not yet added
   for (int64_t t = tb; t < te; t += S::kScan) {
     // eight rows in a row for each thread
     const int64_t mine = t + 8 * tid;
@@ -798,8 +826,8 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64
       for (int e = 0; e < 8; ++e)
         if (mine + e < te && p.index[mine + e] == a) hits |= 1u << e;
     }
-    int at = __builtin_popcount(hits);
-    const int n = at;
+    const int n = __builtin_popcount(hits);
+    int at = n;
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1) {
       const int o = __shfl_up(at, k);
@@ -808,39 +836,34 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64
     __syncthreads();
     if (lane == 63) L.counts[wave] = at;
     __syncthreads();
-    int all = have;
-    at += have - n;
+    int all = 0;
+    at -= n;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       if (w < wave) at += L.counts[w];
       all += L.counts[w];
     }
-    for (uint32_t m = hits; m; m &= m - 1) L.list[at++] = (int)(mine - tb) + __builtin_ctz(m);
+    for (uint32_t m = hits; m; m &= m - 1) L.list[at++] = (uint16_t)(8 * tid + __builtin_ctz(m));
     __syncthreads();
-    const int whole = all / T * T;
-    if (whole) run(whole);
-    have = all - whole;
-    __syncthreads();
-    const int keep = tid < have ? L.list[whole + tid] : 0;
-    __syncthreads();
-    if (tid < have) L.list[tid] = keep;
+    t0 = t;
+    if (all) run(all);
   }
-  __syncthreads();
-  if (have > 0) run(have);
 
   // lane l: column (rank) l % 16 of the tile, rows 4 (l / 16) + 0 .. 3
 #pragma unroll
-  for (int j = 0; j < RT; ++j)
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int f = f0 + 16 * wave + (RANK_LANES ? 4 * q + e : fr), k = 16 * j + (RANK_LANES ? fr : 4 * q + e);
-      if (f >= of.F || k >= p.r) continue;
-      const int64_t at = blockIdx.z * numel + (RANK_LANES ? ((int64_t)a * of.F + f) * p.r + k : ((int64_t)a * p.r + k) * of.F + f);
-      if (TO == T_FP32)
-        static_cast<float*>(of.out)[at] = acc[j][e];
-      else
-        static_cast<uint16_t*>(of.out)[at] = (uint16_t)pack2<TO>(acc[j][e], 0.f);
-    }
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int f = f0 + 32 * wave + 16 * i + (RANK_LANES ? 4 * q + e : fr), k = 16 * j + (RANK_LANES ? fr : 4 * q + e);
+        if (f >= of.F || k >= p.r) continue;
+        const int64_t at = blockIdx.z * numel + (RANK_LANES ? ((int64_t)a * of.F + f) * p.r + k : ((int64_t)a * p.r + k) * of.F + f);
+        if (TO == T_FP32)
+          static_cast<float*>(of.out)[at] = acc[i][j][e];
+        else
+          static_cast<uint16_t*>(of.out)[at] = (uint16_t)pack2<TO>(acc[i][j][e], 0.f);
+      }
 }
 
 template <int TY, int TO, int RT>
@@ -914,8 +937,8 @@ struct Parts {
   int64_t per;
 };
 Parts sum_parts(int64_t M, int64_t L, int64_t d, int64_t n) {
-  const int64_t blocks = L * ((d + 63) / 64 + (n + 63) / 64);
-  int64_t z = (256 + blocks - 1) / blocks;
+  const int64_t blocks = L * ((d + 127) / 128 + (n + 127) / 128);
+  int64_t z = (1024 + blocks - 1) / blocks;
   const int64_t most = (M + 511) / 512;
   z = z > most ? most : z;
   z = z < 1 ? 1 : z;
@@ -1020,8 +1043,8 @@ hipError_t sums(SumArgs a, const Parts& z, int out_dtype, float* ws, hipStream_t
     if (z.count > 1) a.of[i].out = ws + (i ? z.count * a.numel[0] : 0);
     q.in[i] = static_cast<const float*>(a.of[i].out);
   }
-  a.blocks0 = (a.of[0].F + 63) / 64;
-  const dim3 grid((unsigned)(a.blocks0 + (a.of[1].F + 63) / 64), (unsigned)a.L, (unsigned)z.count);
+  a.blocks0 = (a.of[0].F + 127) / 128;
+  const dim3 grid((unsigned)(a.blocks0 + (a.of[1].F + 127) / 128), (unsigned)a.L, (unsigned)z.count);
   if (z.count > 1 || out_dtype == T_FP32)
     sums_rt<TY, T_FP32>(a, grid, st);
   else
@@ -1037,9 +1060,10 @@ hipError_t sums(SumArgs a, const Parts& z, int out_dtype, float* ws, hipStream_t
   return hipGetLastError();
 }
 
-// The workspace: h, A padded, and for the gradients dh, A and B transposed, and the parts of the sums.
+// The workspace: h, A padded, and for the gradients dh, both in pieces, A and B transposed, and the
+// parts of the sums.
 struct Ws {
-  int64_t pad, dh, at, bt, parts, bytes;
+  int64_t pad, dh, ph, pdh, at, bt, parts, bytes;
 };
 Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   Ws w{};
@@ -1051,6 +1075,10 @@ Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   } else {
     w.dh = at;
     at += up256(4 * M * rp * down_splits(M, d, r));
+    w.ph = at;
+    at += up256(6 * M * rp);
+    w.pdh = at;
+    at += up256(6 * M * rp);
     w.at = at;
     at += up256(2 * L * r * d);
     w.bt = at;
@@ -1132,15 +1160,27 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
       if ((e = up<TY>(y, nullptr, st)) != hipSuccess) return e;
     }
   }
+  uint16_t *ph = reinterpret_cast<uint16_t*>(ws + w.ph), *pdh = reinterpret_cast<uint16_t*>(ws + w.pdh);
+  if (p.M > 0) {
+    SplitArgs x{};
+    x.of[0] = Split{h, ph, sh};
+    x.of[1] = Split{dh, pdh, sd};
+    x.index = p.index;
+    x.scale = p.scale;
+    x.M = p.M;
+    x.L = L;
+    x.rp = rp;
+    k_split<<<dim3((unsigned)((p.M * (rp / 4) + 255) / 256), 2), 256, 0, st>>>(x);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   SumArgs q{};
   q.index = p.index;
-  q.scale = p.scale;
   q.M = p.M;
   q.L = L;
   q.r = r;
   q.rp = rp;
-  q.of[0] = Sum{dY, h, p.dA, d, sh};
-  q.of[1] = Sum{X, dh, p.dB, n, sd};
+  q.of[0] = Sum{dY, ph, p.dA, d};
+  q.of[1] = Sum{X, pdh, p.dB, n};
   return sums<TY>(q, sum_parts(p.M, L, d, n), p.out_dtype, reinterpret_cast<float*>(ws + w.parts), st);
 }
 
@@ -1154,7 +1194,7 @@ bool adapters_fit(int64_t M, int64_t d, int64_t n, int64_t r) {
   const int64_t downs = blocks * (sl.token ? 8 : 1) * 8;  // ranks, splits
   const int64_t turns = (d + 31) / 32 * ((r + 31) / 32) + (n + 31) / 32 * ((r + 31) / 32);
   const int64_t most = int64_t(1) << 32;
-  return ups * 256 < most && downs * 64 * kDownWaves < most && turns < (int64_t(1) << 31);
+  return M * (round16(r) / 4) + 256 < most && ups * 256 < most && downs * 64 * kDownWaves < most && turns < (int64_t(1) << 31);
 }
 
 size_t adapters_ws_bytes(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
