@@ -308,6 +308,20 @@ struct Low {
   float back;
 
   __device__ __forceinline__ void read(const UpArgs& p, int64_t t, bool mine, float s) {
+    fill(p, mine, s, [&](int k, float (&v)[8]) {
+      const float* h = p.H + t * p.rp + k;
+#pragma unroll 4
+      for (int z = 0; z < p.splits; ++z) {
+        const float4 *o = reinterpret_cast<const float4*>(h + z * p.M * p.rp), x = o[0], y = o[1];
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+        v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+      }
+    });
+  }
+
+  // add(k, v): adds h of ranks k .. k + 7 to v
+  template <class Add>
+  __device__ __forceinline__ void fill(const UpArgs& p, bool mine, float s, Add add) {
     const int q = (threadIdx.x & 63) >> 4;
     float v[KT][8];
 #pragma unroll
@@ -316,13 +330,7 @@ struct Low {
       for (int e = 0; e < 8; ++e) v[c][e] = 0.f;
       const int k = 32 * c + 8 * q;
       if (!mine || k >= p.rp) continue;
-      const float* h = p.H + t * p.rp + k;
-#pragma unroll 4
-      for (int z = 0; z < p.splits; ++z) {
-        const float4 *o = reinterpret_cast<const float4*>(h + z * p.M * p.rp), x = o[0], y = o[1];
-        v[c][0] += x.x, v[c][1] += x.y, v[c][2] += x.z, v[c][3] += x.w;
-        v[c][4] += y.x, v[c][5] += y.y, v[c][6] += y.z, v[c][7] += y.w;
-      }
+      add(k, v[c]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[c][e] = k + e < p.ranks ? v[c][e] * s : 0.f;  // (an infinite x leaves NaN past them)
     }
@@ -445,6 +453,103 @@ __global__ void __launch_bounds__(256) k_up_few(const UpArgs p) {
     if (p.base) b = *reinterpret_cast<const u4i*>(p.base + 2 * (t * p.d + col));
     *reinterpret_cast<u4i*>(p.Y + 2 * (t * p.d + col)) = b;
   }
+}
+
+// Both steps in one launch, for few tokens and small factors: a block for each token of a tile of 16 (as
+// above) and 256 columns forms h itself, its eight waves as in k_down_few, one rank tile after the
+// other, and then 32 columns each.  Every block of a token reads all of B_a, from L2 but for the
+// first, so this pays as long as that takes less than a launch.
+// MEASURED_TOKEN
+constexpr int kTokenCols = 256;
+
+template <int TY, int KT, bool WIDE>
+__global__ void __launch_bounds__(64 * kDownWaves) k_token(const Down of, const UpArgs p) {
+  __shared__ __attribute__((aligned(16))) float sums[2 * KT][kDownWaves][256];
+  const int lane = threadIdx.x & 63, fr = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tokens = (uint32_t)((p.M + 15) / 16) * p.slots;
+  const uint32_t block = blockIdx.x / tokens, in = blockIdx.x - block * tokens;
+  const int slot = in % p.slots;
+  const int64_t t0 = (int64_t)(in / p.slots) * 16, t = t0 + fr;
+  Ids<1> tl;
+  tl.read(p.index, t0, p.M, p.L);
+  const int a = __builtin_amdgcn_readfirstlane(tl.leader(slot));
+  const int n0 = (int)block * kTokenCols + 32 * wave, col = n0 + 8 * q;
+  const bool mine = tl.id[0] == a;
+  if (a >= 0) {
+    const uint16_t* W = reinterpret_cast<const uint16_t*>(p.W) + (int64_t)a * p.d * p.ld;
+    v4i w[2][KT];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int row = n0 + 8 * (fr >> 2) + 4 * u + (fr & 3);
+#pragma unroll
+      for (int c = 0; c < KT; ++c) w[u][c] = row8<WIDE>(W + (int64_t)row * p.ld, row < p.d ? 32 * c + 8 * q : p.r, p.r);
+    }
+    u4i b = u4i{0, 0, 0, 0};
+    if (p.base && mine && col < p.d) b = *reinterpret_cast<const u4i*>(p.base + 2 * (t * p.d + col));
+    const float s = p.scale[a];
+    const int rows = p.M - t0 < 16 ? (int)(p.M - t0) : 16, tiles = p.rp / 16;
+    const uint32_t ld = (uint32_t)of.n * 2;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(of.X + t0 * ld, (int64_t)rows * ld);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(of.W + (int64_t)a * p.ranks * ld, (int64_t)p.ranks * ld);
+    const uint32_t ox = mine ? fr * ld : kOOB;
+    constexpr int U = 8, step = 64 * kDownWaves;
+    for (int j = 0; j < tiles; ++j) {
+      const uint32_t ow = 16 * j + fr < p.ranks ? (16 * j + fr) * ld : kOOB;
+      v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int k = 64 * wave; k < of.n; k += U / 2 * step) {
+        v4i x[U], v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int c = k + u / 2 * step + 32 * (u & 1) + 8 * q;
+          const uint32_t o = c < of.n ? 2u * c : kOOB;
+          v[u] = load16(rw, (ow | o) & kOOB ? kOOB : ow + o);
+          x[u] = load16(rx, (ox | o) & kOOB ? kOOB : ox + o);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc = mfma<TY>(v[u], x[u], acc);
+      }
+      *reinterpret_cast<v4f*>(&sums[j][wave][4 * lane]) = acc;
+    }
+    __syncthreads();
+    if (wave < tiles) {
+      v4f acc = *reinterpret_cast<const v4f*>(&sums[wave][0][4 * lane]);
+#pragma unroll
+      for (int z = 1; z < kDownWaves; ++z) acc += *reinterpret_cast<const v4f*>(&sums[wave][z][4 * lane]);
+      *reinterpret_cast<v4f*>(&sums[wave][0][4 * lane]) = acc;
+    }
+    __syncthreads();
+    Low<TY, KT> h;
+    h.fill(p, mine, s, [&](int k, float (&v)[8]) {  // lane l of a tile: token l % 16, ranks 4 (l / 16) ..
+      const float* o = &sums[k >> 4][0][4 * (fr + 16 * ((k & 15) >> 2))];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] += o[e];
+        v[4 + e] += o[64 + e];
+      }
+    });
+    u4i y;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < KT; ++c) {
+        acc = mfma<TY>(w[u][c], h.lo[c], acc);
+        acc = mfma<TY>(w[u][c], h.hi[c], acc);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const f2 f = unpack2<TY>(b[2 * u + e]);
+        y[2 * u + e] = pack2<TY>(f.x + acc[2 * e] * h.back, f.y + acc[2 * e + 1] * h.back);
+      }
+    }
+    if (mine && col < p.d) *reinterpret_cast<u4i*>(p.Y + 2 * (t * p.d + col)) = y;
+  }
+  // Rows without an adapter: the base's (nothing to do in place).
+  if (p.base == p.Y || slot != 0 || tl.id[0] >= 0 || t >= p.M || col >= p.d) return;
+  u4i b = u4i{0, 0, 0, 0};
+  if (p.base) b = *reinterpret_cast<const u4i*>(p.base + 2 * (t * p.d + col));
+  *reinterpret_cast<u4i*>(p.Y + 2 * (t * p.d + col)) = b;
 }
 
 // Rows of `chunks` 16-byte chunks in LDS, chunk c of row m at c ^ turned(m): the 16 lanes that read a
@@ -1060,6 +1165,11 @@ hipError_t sums(SumArgs a, const Parts& z, int out_dtype, float* ws, hipStream_t
   return hipGetLastError();
 }
 
+// One launch: B_a small, and no more blocks than compute units.
+bool in_one(int64_t M, int64_t d, int64_t n, int64_t r) {
+  return round16(r) * n <= 65536 && M * ((d + kTokenCols - 1) / kTokenCols) <= 256;
+}
+
 // The workspace: h, A padded, and for the gradients dh, both in pieces, A and B transposed, and the
 // parts of the sums.
 struct Ws {
@@ -1069,6 +1179,7 @@ Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   Ws w{};
   const int64_t rp = round16(r);
   int64_t at = up256(4 * M * rp * down_splits(M, n, r));
+  if (!grads && in_one(M, d, n, r)) return w;
   if (!grads) {
     w.pad = at;
     at += up_pads(M, r) ? up256(2 * L * d * ((r + 7) / 8 * 8)) : 0;
@@ -1089,6 +1200,22 @@ Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   }
   w.bytes = at;
   return w;
+}
+
+template <int TY>
+hipError_t token(const Down& of, UpArgs a, hipStream_t st) {
+  const Slots sl = slots_of(a.M);
+  a.slots = sl.slots;
+  const dim3 grid((unsigned)(sl.tiles * sl.slots * ((a.d + kTokenCols - 1) / kTokenCols)));
+  const int kt = (a.rp + 31) / 32, threads = 64 * kDownWaves;
+  const bool wide = a.r % 8 == 0;
+  if (kt == 1)
+    wide ? k_token<TY, 1, true><<<grid, threads, 0, st>>>(of, a) : k_token<TY, 1, false><<<grid, threads, 0, st>>>(of, a);
+  else if (kt == 2)
+    wide ? k_token<TY, 2, true><<<grid, threads, 0, st>>>(of, a) : k_token<TY, 2, false><<<grid, threads, 0, st>>>(of, a);
+  else
+    wide ? k_token<TY, 4, true><<<grid, threads, 0, st>>>(of, a) : k_token<TY, 4, false><<<grid, threads, 0, st>>>(of, a);
+  return hipGetLastError();
 }
 
 DownArgs down_args(const AdapterArgs& p) {
@@ -1118,16 +1245,18 @@ template <int TY>
 hipError_t fwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   float* h = reinterpret_cast<float*>(ws);
   const int s = down_splits(p.M, p.n, p.r);
-  DownArgs x = down_args(p);
-  x.of[0] = Down{static_cast<const uint8_t*>(p.X), static_cast<const uint8_t*>(p.B), h, (int)p.n, s};
-  const hipError_t e = down<TY>(x, 1, st);
-  if (e != hipSuccess) return e;
+  const Down of{static_cast<const uint8_t*>(p.X), static_cast<const uint8_t*>(p.B), h, (int)p.n, s};
   UpArgs y = up_args(p);
   y.H = h;
   y.splits = s;
   y.W = static_cast<const uint8_t*>(p.A);
   y.d = (int)p.d;
   y.r = y.ld = (int)p.r;
+  if (in_one(p.M, p.d, p.n, p.r)) return token<TY>(of, y, st);
+  DownArgs x = down_args(p);
+  x.of[0] = of;
+  const hipError_t e = down<TY>(x, 1, st);
+  if (e != hipSuccess) return e;
   return up<TY>(y, reinterpret_cast<uint16_t*>(ws + carve(p.M, p.L, p.d, p.n, p.r, false).pad), st);
 }
 

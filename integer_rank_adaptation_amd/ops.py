@@ -487,8 +487,12 @@ def _adapters(tokens, other, index, A, B, scale, dev):
 
 
 def _adapters_ws(M, L, d, n, r, grads, like):
+    """The workspace (None where the call needs none), its address and size."""
     size = B.intlora_adapters_ws_bytes(M, L, d, n, r, grads)
-    return torch.empty(max(size, 16), dtype=torch.uint8, device=like.device), size
+    if size == 0:
+        return None, None, 0
+    ws = torch.empty(size, dtype=torch.uint8, device=like.device)
+    return ws, ws.data_ptr(), size
 
 
 def adapters_linear(base, X, index, A, B_, scale, out=None):
@@ -500,8 +504,8 @@ def adapters_linear(base, X, index, A, B_, scale, out=None):
     M, L, d, n, r, (x, i, a, b, s) = _adapters(X, None, index, A, B_, scale, dev)
     p = None if base is None else _want("base", base, (M, d), (X.dtype,), dev)
     Y, y = _output(out, (M, d), X.dtype, X, dev)
-    ws, size = _adapters_ws(M, L, d, n, r, False, X)
-    B.intlora_adapters_fwd(M, L, d, n, r, _FLOAT[X.dtype], p, x, i, a, b, s, y, ws.data_ptr(), ws_bytes=size)
+    ws, w, size = _adapters_ws(M, L, d, n, r, False, X)
+    B.intlora_adapters_fwd(M, L, d, n, r, _FLOAT[X.dtype], p, x, i, a, b, s, y, w, ws_bytes=size)
     return Y
 
 
@@ -522,9 +526,9 @@ def adapters_linear_grad(dY, X, index, A, B_, scale, base=None, dtype=None, need
     dX, dx = _output(o[0], (M, n), X.dtype, X, dev) if need_dx else (None, None)
     dA, da = _output(o[1], (L, d, r), dtype, X, dev)
     dB, db = _output(o[2], (L, r, n), dtype, X, dev)
-    ws, size = _adapters_ws(M, L, d, n, r, True, X)
-    B.intlora_adapters_grad(M, L, d, n, r, _FLOAT[X.dtype], _FLOAT[dtype], g, x, i, a, b, s, p, dx, da, db,
-                            ws.data_ptr(), ws_bytes=size)
+    ws, w, size = _adapters_ws(M, L, d, n, r, True, X)
+    B.intlora_adapters_grad(M, L, d, n, r, _FLOAT[X.dtype], _FLOAT[dtype], g, x, i, a, b, s, p, dx, da, db, w,
+                            ws_bytes=size)
     return dX, dA, dB
 
 

@@ -20,14 +20,14 @@ def lib():
 
 
 def _fwd(lib, **kw):
-    a = dict(M=8, L=2, d=16, n=16, r=4, dtype=0, base=P[0], X=P[1], index=P[2], A=P[3], B=P[4], scale=P[5], Y=P[6],
+    a = dict(M=8, L=2, d=16, n=1024, r=128, dtype=0, base=P[0], X=P[1], index=P[2], A=P[3], B=P[4], scale=P[5], Y=P[6],
              ws=P[7], size=1 << 20)
     a.update(kw)
     return lib.intlora_adapters_fwd(*a.values(), None)
 
 
 def _grad(lib, **kw):
-    a = dict(M=8, L=2, d=16, n=16, r=4, dtype=0, out=2, dY=P[8], X=P[1], index=P[2], A=P[3], B=P[4], scale=P[5],
+    a = dict(M=8, L=2, d=16, n=1024, r=128, dtype=0, out=2, dY=P[8], X=P[1], index=P[2], A=P[3], B=P[4], scale=P[5],
              base=P[0], dX=P[6], dA=P[9], dB=P[10], ws=P[7], size=1 << 20)
     a.update(kw)
     return lib.intlora_adapters_grad(*a.values(), None)
@@ -75,8 +75,9 @@ def test_workspace(lib):
     assert f(1, 0, 8, 8, 1, 0) == 0 and f(1, 1, 8, 12, 1, 0) == 0  # refused sizes
     for M in (1, 17, 1024, 1025, 5000):
         for r in (1, 16, 17, 128):
-            small, wide = f(M, 3, 64, 512, r, 0), f(M, 3, 64, 512, r, 1)
-            assert wide > small >= 4 * M * ((r + 15) // 16 * 16)
+            small, wide = f(M, 3, 64, 2048, r, 0), f(M, 3, 64, 2048, r, 1)
+            need = 4 * M * ((r + 15) // 16 * 16)
+            assert wide > need and (small >= need or small == 0)  # 0: one launch, without memory in between
 
 
 def test_tensor_checks(monkeypatch):
