@@ -39,50 +39,159 @@ __device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0
 // is exact.
 __device__ __forceinline__ float top_bf16(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
 
-// ---- the adapters of a tile of 16 TT token rows
-// Lane l holds the adapters of tokens 16 tt + l % 16 (-1: none).
-template <int TT>
-struct Ids {
-  int id[TT];
-  __device__ __forceinline__ void read(const int32_t* __restrict__ index, int64_t t0, int64_t M, int L) {
-    const int fr = threadIdx.x & 15;
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      const int64_t t = t0 + 16 * i + fr;
-      const int a = t < M ? index[t] : -1;
-      id[i] = a >= 0 && a < L ? a : -1;
-    }
-  }
-  // The first adapter of the tile that is above -1; -1 when none is left.
-  __device__ __forceinline__ int first() const {
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      const uint64_t m = __builtin_amdgcn_ballot_w64(id[i] >= 0);
-      if (m) return __builtin_amdgcn_readlane(id[i], __builtin_ctzll(m));
-    }
-    return -1;
-  }
-  // Takes the adapters of the tile in turn: the one `skip` further on, those in front dropped; -1 when
-  // there is none.
-  __device__ __forceinline__ int next(int skip) {
-    for (;;) {
-      const int a = first();
-      if (a < 0 || skip-- == 0) return a;
-      drop(a);
-    }
-  }
-  __device__ __forceinline__ void drop(int a) {
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
-      if (id[i] == a) id[i] = -1;
-  }
-  // The adapter of token `slot` (of the first 16) if no earlier one of these has the same, else -1.
-  __device__ __forceinline__ int leader(int slot) const {
-    const int a = __builtin_amdgcn_readlane(id[0], slot);
-    const uint64_t m = __builtin_amdgcn_ballot_w64(id[0] == a);
-    return a >= 0 && (int)__builtin_ctzll(m) == slot ? a : -1;
+// ---- few tokens: the adapters of a tile of 16 token rows, lane l that of token l % 16 (-1: none)
+__device__ __forceinline__ int adapter_of(const int32_t* __restrict__ index, int64_t t, int64_t M, int L) {
+  const int a = t < M ? index[t] : -1;
+  return a >= 0 && a < L ? a : -1;
+}
+// The adapter of token `slot` if no earlier one of the tile has the same, else -1.
+__device__ __forceinline__ int leader(int id, int slot) {
+  const int a = __builtin_amdgcn_readlane(id, slot);
+  const uint64_t m = __builtin_amdgcn_ballot_w64(id == a);
+  // (in a scalar register for the compiler too, which would load lane by lane otherwise)
+  return __builtin_amdgcn_readfirstlane(a >= 0 && (int)__builtin_ctzll(m) == slot ? a : -1);
+}
+
+// ---- more tokens: the rows of each adapter, in order
+// Rows are taken `chunk` at a time (less than 2^31 bytes of any of the tensors, so that offsets
+// inside fit 32 bits; one chunk as a rule).  For each chunk: order[] = its rows sorted by adapter, the ones
+// without an adapter last (group L); group g has the places starts[g] .. starts[g + 1] - 1, and the
+// tiles t32[g] .. of 32 places, t64[g] .. of 64.
+struct Lists {
+  int32_t *order, *starts, *t32, *t64;  // order: M; the others chunks x (L + 2)
+  int64_t M, chunk;
+  int L;
+  __device__ __forceinline__ int rows(int c) const {
+    const int64_t n = M - c * chunk;
+    return (int)(n < chunk ? n : chunk);
   }
 };
+
+// A block for each group: it counts all rows by adapter in LDS, which gives its first place and
+// tiles, and then lists its own.  Bound by latency: 8192 rows LISTS_US.
+constexpr int kMaxGroups = 4096 + 1;
+
+__global__ void __launch_bounds__(1024) k_lists(const int32_t* __restrict__ index, const Lists l) {
+  __shared__ int count[kMaxGroups];
+  __shared__ int sums[16][3];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = blockIdx.x, c = blockIdx.y;
+  const int rows = l.rows(c), groups = l.L + 1;
+  index += c * l.chunk;
+  for (int i = tid; i < groups; i += 1024) count[i] = 0;
+  __syncthreads();
+  // the groups of rows r .. r + 7 (-1 past the end)
+  auto keys = [&](int r, int (&k)[8]) {
+    if (r + 8 <= rows) {
+      const int4 x = *reinterpret_cast<const int4*>(index + r), y = *reinterpret_cast<const int4*>(index + r + 4);
+      k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w, k[4] = y.x, k[5] = y.y, k[6] = y.z, k[7] = y.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) k[e] = r + e < rows ? index[r + e] : 0;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) k[e] = r + e >= rows ? -1 : k[e] >= 0 && k[e] < l.L ? k[e] : l.L;
+  };
+  for (int r = 8 * tid; r < rows; r += 8192) {
+    int k[8];
+    keys(r, k);
+    int at = k[0], n = 1;  // neighbours of one group at once
+#pragma unroll
+    for (int e = 1; e < 8; ++e) {
+      if (k[e] == at) {
+        ++n;
+        continue;
+      }
+      if (at >= 0) atomicAdd(&count[at], n);
+      at = k[e];
+      n = 1;
+    }
+    if (at >= 0) atomicAdd(&count[at], n);
+  }
+  __syncthreads();
+  int s[3] = {0, 0, 0};  // places and tiles in front
+  for (int i = tid; i < g; i += 1024) {
+    const int n = count[i];
+    s[0] += n;
+    s[1] += (n + 31) / 32;
+    s[2] += (n + 63) / 64;
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+#pragma unroll
+    for (int x = 32; x; x >>= 1) s[k] += __shfl_xor(s[k], x);
+    if (lane == 0) sums[wave][k] = s[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    s[k] = 0;
+    for (int w = 0; w < 16; ++w) s[k] += sums[w][k];
+  }
+  const int mine = count[g], at = c * (l.L + 2) + g;
+  if (tid == 0) {
+    l.starts[at] = s[0];
+    l.t32[at] = s[1];
+    l.t64[at] = s[2];
+    if (g == l.L) {
+      l.starts[at + 1] = s[0] + mine;
+      l.t32[at + 1] = s[1] + (mine + 31) / 32;
+      l.t64[at + 1] = s[2] + (mine + 63) / 64;
+    }
+  }
+  if (mine == 0) return;
+  int32_t* out = l.order + c * l.chunk + s[0];
+  for (int r0 = 0; r0 < rows; r0 += 8192) {
+    int k[8];
+    keys(r0 + 8 * tid, k);
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) n += k[e] == g;
+    int before = n;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) {
+      const int o = __shfl_up(before, x);
+      if (lane >= x) before += o;
+    }
+    __syncthreads();
+    if (lane == 63) sums[wave][0] = before;
+    __syncthreads();
+    before -= n;
+    int all = 0;
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) before += sums[w][0];
+      all += sums[w][0];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k[e] == g) out[before++] = r0 + 8 * tid + e;
+    out += all;
+  }
+}
+
+// The group, first place and places of a tile of SIZE places; rows = 0: there is no such tile.
+struct Place {
+  int group, at, rows;
+};
+template <int SIZE>
+__device__ __forceinline__ Place find_tile(const Lists& l, int c, int tile) {
+  const int32_t *t = (SIZE == 32 ? l.t32 : l.t64) + c * (l.L + 2), *starts = l.starts + c * (l.L + 2);
+  const int lane = threadIdx.x & 63, last = l.L + 1;
+  // the last group whose first tile is not behind this one: 64 at a time, before them every 128th
+  int base = 0;
+  if (last >= 64) {
+    const uint64_t m = __builtin_amdgcn_ballot_w64(128 * lane <= last && t[128 * lane <= last ? 128 * lane : last] <= tile);
+    base = 128 * (__builtin_popcountll(m) - 1);
+  }
+  int n = 0;
+  for (int h = 0; h < (last >= 64 ? 2 : 1); ++h) {
+    const int i = base + 64 * h + lane;
+    n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(i <= last && t[i <= last ? i : last] <= tile));
+  }
+  const int g = __builtin_amdgcn_readfirstlane(base + n - 1);
+  if (g >= last) return Place{last, 0, 0};
+  const int at = starts[g] + SIZE * (tile - t[g]), left = starts[g + 1] - at;
+  return Place{g, __builtin_amdgcn_readfirstlane(at), __builtin_amdgcn_readfirstlane(left < SIZE ? left : SIZE)};
+}
 
 // h = W_a x of one or two problems (h and dh: blockIdx.y).
 struct Down {
@@ -94,9 +203,10 @@ struct Down {
 struct DownArgs {
   Down of[2];
   const int32_t* index;
+  Lists lists;
   int64_t M;
   int L, r, rp;
-  int slots;  // blocks of a tile
+  int slots;  // few tokens: tokens of a tile of 16
 };
 
 // For few tokens: a block for each token of a tile of 16 and each 16 ranks, where the token is the
@@ -120,15 +230,13 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_down_few(const DownArgs p) 
   rest /= groups;
   const int64_t t0 = (int64_t)(rest / p.slots) * 16;
   if (t0 >= p.M) return;
-  Ids<1> tl;
-  tl.read(p.index, t0, p.M, p.L);
-  const int a = __builtin_amdgcn_readfirstlane(tl.leader(rest % p.slots));
+  const int id = adapter_of(p.index, t0 + fr, p.M, p.L), a = leader(id, rest % p.slots);
   if (a < 0) return;
   const int rows = p.M - t0 < 16 ? (int)(p.M - t0) : 16;
   const uint32_t ld = (uint32_t)of.n * 2;
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(of.X + t0 * ld, (int64_t)rows * ld);
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(of.W + (int64_t)a * p.r * ld, (int64_t)p.r * ld);
-  const uint32_t ox = tl.id[0] == a ? fr * ld : kOOB, ow = g0 + fr < p.r ? (g0 + fr) * ld : kOOB;
+  const uint32_t ox = id == a ? fr * ld : kOOB, ow = g0 + fr < p.r ? (g0 + fr) * ld : kOOB;
   // (lane q: 16 bytes each at 8 q and 32 + 8 q of a run; four runs in flight)
   constexpr int U = 8;
   const int first = 64 * (wave + kDownWaves * split), step = 64 * kDownWaves * of.splits;
@@ -147,17 +255,17 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_down_few(const DownArgs p) 
   }
   *reinterpret_cast<v4f*>(&sums[wave][4 * lane]) = acc;
   __syncthreads();
-  if (wave != 0 || tl.id[0] != a) return;
+  if (wave != 0 || id != a) return;
 #pragma unroll
   for (int w = 1; w < kDownWaves; ++w) acc += *reinterpret_cast<const v4f*>(&sums[w][4 * lane]);
   *reinterpret_cast<v4f*>(of.H + (split * p.M + t0 + fr) * p.rp + g0 + 4 * q) = acc;
 }
 
-// For more tokens: a block computes 32 tokens x 16 RT ranks over one split of the columns.  Stages of
-// 256 bytes of the rows go through a ring of three LDS buffers filled by direct loads of 4 rows
-// x 256 bytes (fragments straight from memory, 16 pieces of 64 bytes a load, took twice as long);
-// each of the four waves takes a quarter of a stage, and their sums meet in LDS, where they are
-// added in order.  A place of a tile's adapters each: kSlots blocks take them in turn.
+// For more tokens: a block computes 32 rows of one adapter x 16 RT ranks over one split of the columns.
+// Stages of 256 bytes of the rows go through a ring of three LDS buffers filled by direct loads of
+// 4 rows x 256 bytes (fragments straight from memory, 16 pieces of 64 bytes a load, took twice as
+// long); each of the four waves takes a quarter of a stage, and their sums meet in LDS, where they are
+// added in order.
 // MEASURED_DOWN
 template <int RT_>
 struct DownTile {
@@ -174,106 +282,93 @@ __global__ void __launch_bounds__(256) k_down(const DownArgs p) {
   const Down& of = p.of[blockIdx.y];
   const int lane = threadIdx.x & 63, fr = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t tiles = (uint32_t)((p.M + 31) / 32);
-  uint32_t rest = blockIdx.x;  // slots outermost: where tiles have one adapter, only the first slot works
-  const int split = rest % of.splits;
-  rest /= of.splits;
-  const int slot = rest / tiles;
-  if (slot >= p.slots) return;
-  const int64_t t0 = (int64_t)(rest - slot * tiles) * 32;
-  Ids<2> tl;
-  tl.read(p.index, t0, p.M, p.L);
-  const int rows = p.M - t0 < 32 ? (int)(p.M - t0) : 32;
+  const int c = blockIdx.z, tile = blockIdx.x / of.splits, split = blockIdx.x - tile * of.splits;
+  const Place pl = find_tile<32>(p.lists, c, tile);
+  if (pl.rows <= 0 || pl.group >= p.L) return;
+  const int a = pl.group;
+  const int64_t first = c * p.lists.chunk;  // the chunk's first row, and first place
+  const int row = (lane & 31) < pl.rows ? p.lists.order[first + pl.at + (lane & 31)] : -1;
   const int ld = of.n * 2, stages = (ld + 255) / 256, mine = stages > split ? (stages - split + of.splits - 1) / of.splits : 0;
   // The blocks of an XCD (each eighth one) start at different stages: rows are a power of two of bytes
   // apart as a rule, and blocks at the same columns would all be at the same few channels.
   const int turn = mine > 0 ? (int)((blockIdx.x >> 3) % mine) : 0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
-  // Lane l of a load: row l / 16 of its four, whose 16-byte chunk c lies at c ^ row % 16.
-  uint32_t ow[RT];
+  // Lane l of a load: row l / 16 of its four, whose 16-byte chunk k lies at k ^ row % 16.
+  uint32_t ow[RT], ox[2];
   int cx[2], cw[RT];
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
-    const int row = 4 * (wave * RT + j) + q;
-    cw[j] = 16 * (fr ^ (row & 15));
-    ow[j] = row < p.r ? row * ld + cw[j] : kOOB;
+    const int k = 4 * (wave * RT + j) + q;
+    cw[j] = 16 * (fr ^ (k & 15));
+    ow[j] = k < p.r ? k * ld + cw[j] : kOOB;
   }
-  int idr[2];
 #pragma unroll
-  for (int l = 0; l < 2; ++l) {
-    const int row = 8 * wave + 4 * l + q;
-    cx[l] = 16 * (fr ^ (row & 15));
-    const int lo = __shfl(tl.id[0], row & 15), hi = __shfl(tl.id[1], row & 15);
-    idr[l] = row < 16 ? lo : hi;
+  for (int i = 0; i < 2; ++i) {
+    const int k = 8 * wave + 4 * i + q, r = __shfl(row, k);
+    cx[i] = 16 * (fr ^ (k & 15));
+    ox[i] = r >= 0 ? (uint32_t)r * ld + cx[i] : kOOB;
   }
-  for (int f = tl.next(slot); f >= 0; f = tl.next(p.slots - 1)) {
-    const int a = __builtin_amdgcn_readfirstlane(f);
-    const uint8_t *px = of.X + t0 * ld, *pw = of.W + (int64_t)a * p.r * ld;
-    auto issue = [&](int i, int place) {  // (stages past the last: loads of nothing, so that counts stay)
-      const int at = i < mine ? (i + turn < mine ? i + turn : i + turn - mine) * of.splits + split : stages;
-      const int k0 = at * 256, left = ld - k0;
-      const rsrc_t rx = make_desc(px + k0, rows * ld - k0), rw = make_desc(pw + k0, p.r * ld - k0);
-      const uint32_t S = lds0 + place * C::STAGE;
+  const uint8_t *px = of.X + first * ld, *pw = of.W + (int64_t)a * p.r * ld;
+  const int bytes = p.lists.rows(c) * ld;
+  auto issue = [&](int i, int place) {  // (stages past the last: loads of nothing, so that counts stay)
+    const int at = i < mine ? (i + turn < mine ? i + turn : i + turn - mine) * of.splits + split : stages;
+    const int k0 = at * 256, left = ld - k0;
+    const rsrc_t rx = make_desc(px + k0, bytes - k0), rw = make_desc(pw + k0, p.r * ld - k0);
+    const uint32_t S = lds0 + place * C::STAGE;
 #pragma unroll
-      for (int l = 0; l < 2; ++l) {
-        const int row = 8 * wave + 4 * l + q;
-        direct_load16(rx, S + (2 * wave + l) * 1024, idr[l] == a && cx[l] < left ? row * ld + cx[l] : kOOB);
-      }
+    for (int k = 0; k < 2; ++k) direct_load16(rx, S + (2 * wave + k) * 1024, cx[k] < left ? ox[k] : kOOB);
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
-        direct_load16(rw, S + 8192 + (wave * RT + j) * 1024, cw[j] < left ? ow[j] : kOOB);
-    };
-    v4f acc[2][RT];
+    for (int j = 0; j < RT; ++j) direct_load16(rw, S + 8192 + (wave * RT + j) * 1024, cw[j] < left ? ow[j] : kOOB);
+  };
+  v4f acc[2][RT];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    issue(0, 0);
-    issue(1, 1);
-    int place = 0;
-    const uint32_t at = fr * 256 + (((4 * wave + q) ^ fr) << 4);
-    for (int i = 0; i < mine; ++i) {
-      wait_loads<C::LOADS>();  // this stage has landed, and every wave is done with the one before
-      __builtin_amdgcn_s_barrier();
-      __asm__ volatile("" ::: "memory");
-      const uint8_t* S = lds + place * C::STAGE + at;
-      issue(i + 2, place == 0 ? 2 : place - 1);
-      place = place == 2 ? 0 : place + 1;
-      v4i x[2], w[RT];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) x[t] = *reinterpret_cast<const v4i*>(S + t * 4096);
-#pragma unroll
-      for (int j = 0; j < RT; ++j) w[j] = *reinterpret_cast<const v4i*>(S + 8192 + j * 4096);
-#pragma unroll
-      for (int j = 0; j < RT; ++j)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) acc[t][j] = mfma<TY>(w[j], x[t], acc[t][j]);
-    }
-    wait_loads<0>();
+    for (int j = 0; j < RT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  issue(0, 0);
+  issue(1, 1);
+  int place = 0;
+  const uint32_t at = fr * 256 + (((4 * wave + q) ^ fr) << 4);
+  for (int i = 0; i < mine; ++i) {
+    wait_loads<C::LOADS>();  // this stage has landed, and every wave is done with the one before
     __builtin_amdgcn_s_barrier();
     __asm__ volatile("" ::: "memory");
-    v4f* sums = reinterpret_cast<v4f*>(lds);
+    const uint8_t* S = lds + place * C::STAGE + at;
+    issue(i + 2, place == 0 ? 2 : place - 1);
+    place = place == 2 ? 0 : place + 1;
+    v4i x[2], w[RT];
 #pragma unroll
-    for (int z = 0; z < 2 * RT; ++z) sums[(wave * 2 * RT + z) * 64 + lane] = acc[z & 1][z >> 1];
-    __syncthreads();
+    for (int t = 0; t < 2; ++t) x[t] = *reinterpret_cast<const v4i*>(S + t * 4096);
 #pragma unroll
-    for (int y = 0; y < 2 * RT; y += 4) {
-      const int z = y + wave;  // this wave's tile
-      if (z >= 2 * RT) break;
-      v4f s = sums[z * 64 + lane];
+    for (int j = 0; j < RT; ++j) w[j] = *reinterpret_cast<const v4i*>(S + 8192 + j * 4096);
 #pragma unroll
-      for (int w = 1; w < 4; ++w) s += sums[(w * 2 * RT + z) * 64 + lane];
-      const int i = z & 1, g = 16 * (z >> 1);
-      if ((i ? tl.id[1] : tl.id[0]) == a && g < p.rp)
-        *reinterpret_cast<v4f*>(of.H + (split * p.M + t0 + 16 * i + fr) * p.rp + g + 4 * q) = s;
-    }
-    __syncthreads();
-    tl.drop(a);
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) acc[t][j] = mfma<TY>(w[j], x[t], acc[t][j]);
+  }
+  wait_loads<0>();
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
+  v4f* sums = reinterpret_cast<v4f*>(lds);
+#pragma unroll
+  for (int z = 0; z < 2 * RT; ++z) sums[(wave * 2 * RT + z) * 64 + lane] = acc[z & 1][z >> 1];
+  __syncthreads();
+#pragma unroll
+  for (int y = 0; y < 2 * RT; y += 4) {
+    const int z = y + wave;  // this wave's tile
+    if (z >= 2 * RT) break;
+    v4f s = sums[z * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) s += sums[(w * 2 * RT + z) * 64 + lane];
+    const int i = 16 * (z & 1) + fr, g = 16 * (z >> 1);
+    if (i < pl.rows && g < p.rp)
+      *reinterpret_cast<v4f*>(of.H + (split * p.M + first + pl.at + i) * p.rp + g + 4 * q) = s;
   }
 }
 
 struct UpArgs {
-  const float* H;       // splits x M x rp
+  const float* H;       // splits x M x rp, by row (few tokens) or by place in the lists
+  Lists lists;
   const uint8_t* W;     // L x d rows of ld elements, r of them used
   const int32_t* index;
   const float* scale;   // [L]
@@ -389,14 +484,12 @@ __global__ void __launch_bounds__(256) k_up_few(const UpArgs p) {
   const uint32_t block = blockIdx.x / tokens, in = blockIdx.x - block * tokens;
   const int slot = in % p.slots;
   const int64_t t = (int64_t)(in / p.slots) * 16 + fr;  // this lane's token
-  Ids<1> tl;
-  tl.read(p.index, t - fr, p.M, p.L);
+  const int id = adapter_of(p.index, t, p.M, p.L), a = leader(id, slot);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = (int)block * p.chunk + 32 * wave, c1 = (int)block * p.chunk + p.chunk;
   // Steps of 128 columns; the blocks of an XCD start at different ones (as in k_down).
   const int steps = p.chunk / 128, turn = (int)((blockIdx.x >> 3) % steps);
   auto column = [&](int step) { return first + 128 * (step + turn < steps ? step + turn : step + turn - steps); };
-  const int a = __builtin_amdgcn_readfirstlane(tl.leader(slot));
   if (a >= 0) {
     const uint16_t* W = reinterpret_cast<const uint16_t*>(p.W) + (int64_t)a * p.d * p.ld;
     struct Cols {
@@ -413,7 +506,7 @@ __global__ void __launch_bounds__(256) k_up_few(const UpArgs p) {
     };
     Cols cur;
     load(column(0), cur);
-    const bool mine = tl.id[0] == a;
+    const bool mine = id == a;
     Low<TY, KT> h;
     h.read(p, t, mine, p.scale[a]);
     for (int step = 0; step < steps; ++step) {
@@ -447,7 +540,7 @@ __global__ void __launch_bounds__(256) k_up_few(const UpArgs p) {
     }
   }
   // Rows without an adapter: the base's (nothing to do in place).
-  if (p.base == p.Y || slot != 0 || tl.id[0] >= 0 || t >= p.M) return;
+  if (p.base == p.Y || slot != 0 || id >= 0 || t >= p.M) return;
   for (int col = first + 8 * q; col < c1 && col < p.d; col += 128) {
     u4i b = u4i{0, 0, 0, 0};
     if (p.base) b = *reinterpret_cast<const u4i*>(p.base + 2 * (t * p.d + col));
@@ -471,11 +564,9 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_token(const Down of, const 
   const uint32_t block = blockIdx.x / tokens, in = blockIdx.x - block * tokens;
   const int slot = in % p.slots;
   const int64_t t0 = (int64_t)(in / p.slots) * 16, t = t0 + fr;
-  Ids<1> tl;
-  tl.read(p.index, t0, p.M, p.L);
-  const int a = __builtin_amdgcn_readfirstlane(tl.leader(slot));
+  const int id = adapter_of(p.index, t, p.M, p.L), a = leader(id, slot);
   const int n0 = (int)block * kTokenCols + 32 * wave, col = n0 + 8 * q;
-  const bool mine = tl.id[0] == a;
+  const bool mine = id == a;
   if (a >= 0) {
     const uint16_t* W = reinterpret_cast<const uint16_t*>(p.W) + (int64_t)a * p.d * p.ld;
     v4i w[2][KT];
@@ -546,7 +637,7 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_token(const Down of, const 
     if (mine && col < p.d) *reinterpret_cast<u4i*>(p.Y + 2 * (t * p.d + col)) = y;
   }
   // Rows without an adapter: the base's (nothing to do in place).
-  if (p.base == p.Y || slot != 0 || tl.id[0] >= 0 || t >= p.M || col >= p.d) return;
+  if (p.base == p.Y || slot != 0 || id >= 0 || t >= p.M || col >= p.d) return;
   u4i b = u4i{0, 0, 0, 0};
   if (p.base) b = *reinterpret_cast<const u4i*>(p.base + 2 * (t * p.d + col));
   *reinterpret_cast<u4i*>(p.Y + 2 * (t * p.d + col)) = b;
@@ -559,12 +650,12 @@ __device__ __forceinline__ int turned(int m, int chunks) {
   return chunks == 16 ? m : chunks == 8 ? m >> 1 : chunks == 4 ? m >> 2 : chunks == 2 ? m >> 3 : 0;
 }
 
-// For more tokens: a block takes 64 tokens (kSlots blocks, as k_down), 16 each wave, and 128 columns at
-// a time.  The columns' weights go through two LDS buffers filled by direct loads, for all four
-// waves.  Here the tokens are the matrix instruction's rows, and row m of the weights' tile u is
-// column 8 m + u: a lane ends up with columns 8 (l % 16) + 0 .. 7 of tokens 4 (l / 16) + 0 .. 3, so
-// that rows are read and written in runs of 256 bytes with no step through LDS.  The next columns'
-// rows of the base are loaded while these are at work.
+// For more tokens: a block takes 64 rows of one adapter, 16 each wave, and 128 columns at a time.  The
+// columns' weights go through two LDS buffers filled by direct loads, for all four waves.  Here the
+// tokens are the matrix instruction's rows, and row m of the weights' tile u is column 8 m + u: a
+// lane ends up with columns 8 (l % 16) + 0 .. 7 of tokens 4 (l / 16) + 0 .. 3, so that rows are read and
+// written in runs of 256 bytes with no step through LDS.  The next columns' rows of the base are
+// loaded while these are at work.  Rows without an adapter (the last group) take the base's values.
 // MEASURED_UP
 template <int TY, int KT>
 __global__ void __launch_bounds__(256) k_up(const UpArgs p) {
@@ -572,118 +663,115 @@ __global__ void __launch_bounds__(256) k_up(const UpArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * BUF];
   const int lane = threadIdx.x & 63, fr = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t lots = (uint32_t)((p.M + 63) / 64), chunks = (p.d + p.chunk - 1) / p.chunk;
-  const uint32_t slot = blockIdx.x / (lots * chunks), in = blockIdx.x - slot * (lots * chunks);
-  const uint32_t block = in / lots, lot = in - block * lots;
-  const int64_t t0 = (int64_t)lot * 64 + 16 * wave;  // the wave's first token
-  Ids<4> tl;
-  tl.read(p.index, (int64_t)lot * 64, p.M, p.L);
-  const int id = wave == 0 ? tl.id[0] : wave == 1 ? tl.id[1] : wave == 2 ? tl.id[2] : tl.id[3];
-  const int ldo = 2 * p.d, rows = p.M - t0 >= 16 ? 16 : p.M > t0 ? (int)(p.M - t0) : 0;
-  int idt[4];  // of this lane's tokens of the outputs
+  const int chunks = (p.d + p.chunk - 1) / p.chunk, tile = blockIdx.x / chunks, block = blockIdx.x - tile * chunks;
+  const int c = blockIdx.y;
+  const Place pl = find_tile<64>(p.lists, c, tile);
+  if (pl.rows <= 0 || (pl.group >= p.L && p.base == p.Y)) return;
+  const int a = pl.group;
+  const int64_t first = c * p.lists.chunk;  // the chunk's first row, and first place
+  const int at = 16 * wave + fr;            // this lane's place in the tile
+  const int row = at < pl.rows ? p.lists.order[first + pl.at + at] : -1;
+  const int ldo = 2 * p.d;
+  uint32_t ro[4];  // of this lane's tokens of the outputs
 #pragma unroll
-  for (int e = 0; e < 4; ++e) idt[e] = __shfl(id, 4 * q + e);
-  const int64_t at = rows ? t0 * ldo : 0;
-  const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.Y + at, (int64_t)rows * ldo);
-  const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.base ? p.base + at : p.Y, p.base ? (int64_t)rows * ldo : 0);
-  const int c0 = (int)block * p.chunk, steps = p.chunk / 128, turn = (int)((blockIdx.x >> 3) % steps);
+  for (int e = 0; e < 4; ++e) {
+    const int r = __shfl(row, 4 * q + e);
+    ro[e] = r >= 0 ? (uint32_t)r * ldo : kOOB;
+  }
+  const int64_t bytes = (int64_t)p.lists.rows(c) * ldo;
+  const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.Y + first * ldo, bytes);
+  const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.base ? p.base + first * ldo : p.Y, p.base ? bytes : 0);
+  const int c0 = block * p.chunk, steps = p.chunk / 128, turn = (int)((blockIdx.x >> 3) % steps);
   auto column = [&](int step) { return c0 + 128 * (step + turn < steps ? step + turn : step + turn - steps); };
-  auto place = [&](int a, int e, int col) {  // of eight columns in the rows; kOOB: not this adapter's
-    return idt[e] == a && col < p.d ? (uint32_t)((4 * q + e) * ldo + 2 * col) : kOOB;
+  auto place = [&](int e, int col) { return col < p.d && ro[e] != kOOB ? ro[e] + 2 * col : kOOB; };  // of eight columns
+  struct Rows {
+    v4i v[4];
   };
-  // Weights in LDS: rows of `per` chunks of 16 bytes, row 16 u + m holds column 8 m + u, its chunk c at
-  // c ^ turned(m): the 16 rows of a fragment are on different banks.
+  auto fetch = [&](int step, Rows& b) {
+    const int col = step < steps ? column(step) + 8 * fr : p.d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b.v[e] = load16(rb, place(e, col));
+  };
+  if (a >= p.L) {
+    for (int step = 0; step < steps; ++step) {
+      Rows b;
+      fetch(step, b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4i, b.v[e]), ry, place(e, column(step) + 8 * fr), 0, 0);
+    }
+    return;
+  }
+  // Weights in LDS: rows of `per` chunks of 16 bytes, row 16 u + m holds column 8 m + u, its chunk k at
+  // k ^ turned(m): the 16 rows of a fragment are on different banks.
   const int per = p.ld / 8;
   uint32_t wo[NL];
 #pragma unroll
   for (int j = 0; j < NL; ++j) {
-    const int c = 64 * (wave * NL + j) + lane, R = c / per, m = R & 15;
-    wo[j] = R < 128 ? 16 * ((8 * m + (R >> 4)) * per + ((c - R * per) ^ turned(m, per))) : kOOB;
+    const int k = 64 * (wave * NL + j) + lane, R = k / per, m = R & 15;
+    wo[j] = R < 128 ? 16 * ((8 * m + (R >> 4)) * per + ((k - R * per) ^ turned(m, per))) : kOOB;
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds + wave * NL * 1024;
-  struct Rows {
-    v4i v[4];
+  const uint8_t* W = p.W + (int64_t)a * p.d * p.ld * 2;
+  auto issue = [&](int step) {
+    const int col = step < steps ? column(step) : p.d;
+    const int64_t left = (int64_t)(p.d - col) * p.ld * 2;
+    const rsrc_t rw = make_desc(col < p.d ? W + (int64_t)col * p.ld * 2 : W, col < p.d ? (int)(left < 65536 ? left : 65536) : 0);
+#pragma unroll
+    for (int j = 0; j < NL; ++j) direct_load16(rw, lds0 + (step & 1) * BUF + 1024 * j, wo[j]);
   };
-  for (int f = tl.next((int)slot); f >= 0; f = tl.next(p.slots - 1)) {
-    const int a = __builtin_amdgcn_readfirstlane(f);
-    const uint8_t* W = p.W + (int64_t)a * p.d * p.ld * 2;
-    auto issue = [&](int step) {
-      const int col = step < steps ? column(step) : p.d;
-      const int64_t left = (int64_t)(p.d - col) * p.ld * 2;
-      const rsrc_t rw = make_desc(col < p.d ? W + (int64_t)col * p.ld * 2 : W, col < p.d ? (int)(left < 65536 ? left : 65536) : 0);
+  Rows b0, b1;
+  issue(0);
+  fetch(0, b0);
+  __builtin_amdgcn_sched_barrier(0);
+  Low<TY, KT> h;
+  float back[4];
+  h.read(p, first + pl.at + at, row >= 0, p.scale[a]);
 #pragma unroll
-      for (int j = 0; j < NL; ++j) direct_load16(rw, lds0 + (step & 1) * BUF + 1024 * j, wo[j]);
-    };
-    auto fetch = [&](int step, Rows& b) {
-      const int col = step < steps ? column(step) + 8 * fr : p.d;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) b.v[e] = load16(rb, place(a, e, col));
-    };
-    Rows b0, b1;
-    issue(0);
-    fetch(0, b0);
+  for (int e = 0; e < 4; ++e) back[e] = TY == T_FP16 ? __shfl(h.back, 4 * q + e) : 1.f;
+  auto one = [&](int step, Rows& cur, Rows& next) {
+    // this step's weights have landed (newer: its rows of the base and the last step's stores)
+    if (step == 0)
+      wait_loads<4>();
+    else
+      wait_loads<8>();
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+    issue(step + 1);
+    fetch(step + 1, next);
     __builtin_amdgcn_sched_barrier(0);
-    Low<TY, KT> h;
-    float back[4];
-    h.read(p, t0 + fr, id == a, p.scale[a]);
+    const uint8_t* S = lds + (step & 1) * BUF;
+    v4f acc[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) back[e] = TY == T_FP16 ? __shfl(h.back, 4 * q + e) : 1.f;
-    auto one = [&](int step, Rows& cur, Rows& next) {
-      // this step's weights have landed (newer: its rows of the base and the last step's stores)
-      if (step == 0)
-        wait_loads<4>();
-      else
-        wait_loads<8>();
-      __builtin_amdgcn_s_barrier();
-      __asm__ volatile("" ::: "memory");
-      issue(step + 1);
-      fetch(step + 1, next);
-      __builtin_amdgcn_sched_barrier(0);
-      const uint8_t* S = lds + (step & 1) * BUF;
-      v4f acc[8];
+    for (int u = 0; u < 8; ++u) {
+      v4f t = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        v4f t = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < KT; ++c) {
-          const int k = 4 * c + q;
-          const v4i w = k < per ? *reinterpret_cast<const v4i*>(S + 16 * ((16 * u + fr) * per + (k ^ turned(fr, per))))
-                                : v4i{0, 0, 0, 0};
-          t = mfma<TY>(h.lo[c], w, t);
-          t = mfma<TY>(h.hi[c], w, t);
-        }
-        acc[u] = t;
+      for (int x = 0; x < KT; ++x) {
+        const int k = 4 * x + q;
+        const v4i w = k < per ? *reinterpret_cast<const v4i*>(S + 16 * ((16 * u + fr) * per + (k ^ turned(fr, per))))
+                              : v4i{0, 0, 0, 0};
+        t = mfma<TY>(h.lo[x], w, t);
+        t = mfma<TY>(h.hi[x], w, t);
       }
-      const int col = column(step) + 8 * fr;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        u4i y;
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const f2 g = unpack2<TY>((uint32_t)cur.v[e][z]);
-          y[z] = pack2<TY>(g.x + acc[2 * z][e] * back[e], g.y + acc[2 * z + 1][e] * back[e]);
-        }
-        __builtin_amdgcn_raw_buffer_store_b128(y, ry, place(a, e, col), 0, 0);
-      }
-    };
-    for (int step = 0; step < steps; step += 2) {
-      one(step, b0, b1);
-      if (step + 1 < steps) one(step + 1, b1, b0);
+      acc[u] = t;
     }
-    wait_loads<0>();
-    __syncthreads();
-    tl.drop(a);
-  }
-  // Rows without an adapter: the base's (nothing to do in place).
-  if (p.base == p.Y || slot != 0) return;
-  for (int step = 0; step < steps; ++step) {
     const int col = column(step) + 8 * fr;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t o = idt[e] < 0 && 4 * q + e < rows && col < p.d ? (uint32_t)((4 * q + e) * ldo + 2 * col) : kOOB;
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4i, load16(rb, o)), ry, o, 0, 0);
+      u4i y;
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const f2 g = unpack2<TY>((uint32_t)cur.v[e][z]);
+        y[z] = pack2<TY>(g.x + acc[2 * z][e] * back[e], g.y + acc[2 * z + 1][e] * back[e]);
+      }
+      __builtin_amdgcn_raw_buffer_store_b128(y, ry, place(e, col), 0, 0);
     }
+  };
+  for (int step = 0; step < steps; step += 2) {
+    one(step, b0, b1);
+    if (step + 1 < steps) one(step + 1, b1, b0);
   }
+  wait_loads<0>();  // the weights loaded past the last step (zeros)
 }
 
 // Rows of `ld` numbers of rows of r, zeros behind them.
@@ -748,8 +836,8 @@ __global__ void __launch_bounds__(256) k_turn(const TurnArgs p) {
   }
 }
 
-// h and dh, scaled, as three bf16 numbers each (24 bits) for k_sums: planes x M x rp.  Rows without an
-// adapter are left out.
+// h and dh, scaled, as three bf16 numbers each (24 bits) for k_sums: planes x M x rp, by place in the
+// lists.  Rows without an adapter are left out.
 struct Split {
   const float* H;  // splits x M x rp
   uint16_t* out;
@@ -759,20 +847,24 @@ struct SplitArgs {
   Split of[2];
   const int32_t* index;
   const float* scale;
+  Lists lists;
   int64_t M;
   int L, rp;
+  int by_row;  // H's order: rows (few tokens) or places
 };
 __global__ void __launch_bounds__(256) k_split(const SplitArgs p) {
   const Split& of = p.of[blockIdx.y];
   const int per = p.rp / 4;
-  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x, t = u / per;
-  if (t >= p.M) return;
-  const int a = p.index[t];
+  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x, place = u / per;
+  if (place >= p.M) return;
+  const int64_t row = place / p.lists.chunk * p.lists.chunk + p.lists.order[place];
+  const int a = p.index[row];
   if (a < 0 || a >= p.L) return;
   const float s = p.scale[a];
+  const float* H = of.H + (p.by_row ? row : place) * p.rp + 4 * (u - place * per);
   float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int z = 0; z < of.splits; ++z) {
-    const float4 x = *reinterpret_cast<const float4*>(of.H + z * p.M * p.rp + 4 * u);
+    const float4 x = *reinterpret_cast<const float4*>(H + z * p.M * p.rp);
     h.x += x.x, h.y += x.y, h.z += x.z, h.w += x.w;
   }
   float v[4] = {h.x * s, h.y * s, h.z * s, h.w * s};
@@ -795,18 +887,18 @@ struct Sum {
   int F;
 };
 struct SumArgs {
-  Sum of[2];             // dA, dB
-  const int32_t* index;
+  Sum of[2];         // dA, dB
+  Lists lists;
   int64_t M;
   int L, r, rp;
-  int blocks0;           // blocks of 128 columns of the first one
-  int64_t per;           // tokens of a part
-  int64_t numel[2];      // of the outputs: parts lie one after the other
+  int blocks0;       // blocks of 128 columns of the first one
+  int shares;        // blocks that share an adapter's rows of a chunk
+  int64_t numel[2];  // of the outputs: parts lie one after the other
 };
 
-// sum over an adapter's tokens of P_t h_t^T s_a.  A block takes 128 columns of P and all ranks: it
-// lists its adapter's tokens (of 2048 rows at a time, in order) and adds them T at a time, each
-// wave 32 columns x 16 RT ranks; the next ones are loaded meanwhile.  Both operands have the
+// sum over an adapter's tokens of P_t h_t^T s_a.  A block takes 128 columns of P, all ranks and its
+// share of the adapter's rows, T of them at a time, each wave 32 columns x 16 RT ranks; the next
+// ones are loaded meanwhile.  Both operands have the
 // contraction (tokens) in rows and leave LDS through the transposing reads.  h is three bf16 numbers;
 // fp16 rows of P become two (exact).
 // MEASURED_SUMS
@@ -814,11 +906,10 @@ template <int TY, int RT>
 struct SumLds {
   static constexpr int PP = TY == T_FP16 ? 2 : 1, T = RT == 8 ? 32 : 64;
   static constexpr int F = 128, PS = F + 8, HS = 16 * RT + 8;  // row strides (16-bit numbers)
-  static constexpr int kScan = 2048;
+  static constexpr int kList = 1024;  // rows' numbers at a time
   uint16_t p[PP][T * PS];
   uint16_t h[3][T * HS];
-  uint16_t list[kScan + T];
-  int counts[4];
+  int list[kList];
 };
 
 template <int TY, int TO, int RT, bool RANK_LANES>
@@ -828,7 +919,12 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64
   constexpr int NP = T / 16, NH = (6 * T * RT + 255) / 256;  // 16-byte loads of a thread
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, fr = lane & 15, q = lane >> 4;
   const int a = blockIdx.y, f0 = block * S::F;
-  const int64_t tb = blockIdx.z * p.per, te = tb + p.per < p.M ? tb + p.per : p.M;
+  const int c = blockIdx.z / p.shares, share = blockIdx.z - c * p.shares;
+  const int64_t first = c * p.lists.chunk;  // the chunk's first row, and first place
+  const int32_t* starts = p.lists.starts + c * (p.L + 2) + a;
+  const int64_t lots = (starts[1] - starts[0] + T - 1) / T;
+  const int r0 = starts[0] + (int)(lots * share / p.shares) * T;
+  const int r1 = share + 1 == p.shares ? starts[1] : starts[0] + (int)(lots * (share + 1) / p.shares) * T;
   v4f acc[NT][RT];
 #pragma unroll
   for (int j = 0; j < NT * RT; ++j) acc[j / RT][j % RT] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -836,23 +932,22 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64
     u4i p[NP], h[NH];
   };
   Lot lot;
-  int64_t t0 = tb;  // the list's rows count from here
 
-  // rows list[from .. n), at most T: zeros behind them
-  auto fetch = [&](int from, int n) {
+  // places at + from .. at + n - 1, at most T: zeros behind them; list: their rows from `at` on
+  auto fetch = [&](int at0, int from, int n) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int row = (tid >> 4) + 16 * i, c = (tid & 15) * 8;
       lot.p[i] = u4i{0, 0, 0, 0};
       if (from + row < n && f0 + c < of.F)
-        lot.p[i] = *reinterpret_cast<const u4i*>(of.P + 2 * ((t0 + L.list[from + row]) * of.F + f0 + c));
+        lot.p[i] = *reinterpret_cast<const u4i*>(of.P + 2 * ((first + L.list[from + row]) * of.F + f0 + c));
     }
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
       const int at = tid + 256 * i, k = at / (2 * RT * T), in = at % (2 * RT * T), row = in / (2 * RT), c = in % (2 * RT) * 8;
       lot.h[i] = u4i{0, 0, 0, 0};
       if (k < 3 && from + row < n && c < p.rp)
-        lot.h[i] = *reinterpret_cast<const u4i*>(of.H + (k * p.M + t0 + L.list[from + row]) * p.rp + c);
+        lot.h[i] = *reinterpret_cast<const u4i*>(of.H + (k * p.M + first + at0 + from + row) * p.rp + c);
     }
   };
   auto store = [&]() {
@@ -907,51 +1002,20 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64
         }
     }
   };
-  auto run = [&](int n) {  // the first n of the list
-    fetch(0, n);
+  for (int at = r0; at < r1; at += S::kList) {
+    const int n = r1 - at < S::kList ? r1 - at : S::kList;
+    __syncthreads();
+    for (int i = tid; i < n; i += 256) L.list[i] = p.lists.order[first + at + i];
+    __syncthreads();
+    fetch(at, 0, n);
     for (int from = 0; from < n; from += T) {
       __syncthreads();
       store();
       __syncthreads();
-      fetch(from + T, n);
+      fetch(at, from + T, n);
       __builtin_amdgcn_sched_barrier(0);
       add();
     }
-  };
-
-  for (int64_t t = tb; t < te; t += S::kScan) {
-    // eight rows in a row for each thread
-    const int64_t mine = t + 8 * tid;
-    uint32_t hits = 0;
-    if (mine + 8 <= te) {
-      const int4 x = *reinterpret_cast<const int4*>(p.index + mine), y = *reinterpret_cast<const int4*>(p.index + mine + 4);
-      hits = (x.x == a) | (x.y == a) << 1 | (x.z == a) << 2 | (x.w == a) << 3 | (y.x == a) << 4 | (y.y == a) << 5 |
-             (y.z == a) << 6 | (y.w == a) << 7;
-    } else {
-      for (int e = 0; e < 8; ++e)
-        if (mine + e < te && p.index[mine + e] == a) hits |= 1u << e;
-    }
-    const int n = __builtin_popcount(hits);
-    int at = n;
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) {
-      const int o = __shfl_up(at, k);
-      if (lane >= k) at += o;
-    }
-    __syncthreads();
-    if (lane == 63) L.counts[wave] = at;
-    __syncthreads();
-    int all = 0;
-    at -= n;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (w < wave) at += L.counts[w];
-      all += L.counts[w];
-    }
-    for (uint32_t m = hits; m; m &= m - 1) L.list[at++] = (uint16_t)(8 * tid + __builtin_ctz(m));
-    __syncthreads();
-    t0 = t;
-    if (all) run(all);
   }
 
   // lane l: column (rank) l % 16 of the tile, rows 4 (l / 16) + 0 .. 3
@@ -1006,21 +1070,25 @@ __global__ void __launch_bounds__(256) k_parts(const PartsArgs p, int parts) {
   }
 }
 
-// Up to here a block for each token of a tile of 16 (every request an adapter of its own is the
-// common batch); from there on kSlots blocks for a tile of 32, so that a tile on the border of two
-// requests takes no longer than the others (8192 rows of 12 requests, 4096 x 4096, rank 64: h 48
-// us with one block a tile, SLOT_US with four).
+// Up to here a block for each token of a tile of 16, without lists (in decode nearly every request
+// has an adapter of its own); more rows are listed by adapter first.
 constexpr int64_t kTokenRows = 1024;
-constexpr int kSlots = 2;
 
-struct Slots {
-  int tt, slots;
-  int64_t tiles;
-  bool token;
-};
-Slots slots_of(int64_t M) {
-  if (M <= kTokenRows) return {1, M < 16 ? (M < 1 ? 1 : (int)M) : 16, (M + 15) / 16, true};
-  return {2, kSlots, (M + 31) / 32, false};
+int token_slots(int64_t M) { return M < 16 ? (M < 1 ? 1 : (int)M) : 16; }
+
+// Rows at a time: less than 2^31 bytes of the widest tensor.
+int64_t list_chunk(int64_t M, int64_t d, int64_t n) {
+  const int64_t most = ((int64_t(1) << 31) - 65536) / (2 * (d > n ? d : n)) / 64 * 64;
+  return M < most ? (M < 1 ? 1 : M) : most;
+}
+int64_t list_chunks(int64_t M, int64_t d, int64_t n) {
+  const int64_t c = list_chunk(M, d, n);
+  return M < 1 ? 1 : (M + c - 1) / c;
+}
+// Tiles of `size` rows that a chunk can have.
+int64_t most_tiles(int64_t M, int64_t L, int64_t d, int64_t n, int64_t size) {
+  const int64_t c = list_chunk(M, d, n);
+  return c / size + (L + 1 < c ? L + 1 : c);
 }
 
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
@@ -1036,38 +1104,24 @@ int down_splits(int64_t M, int64_t n, int64_t r) {
   return (int)(s > 8 ? 8 : s < 1 ? 1 : s);
 }
 
-// Parts of the tokens of k_sums, each a multiple of 8 rows.
-struct Parts {
-  int count;
-  int64_t per;
-};
-Parts sum_parts(int64_t M, int64_t L, int64_t d, int64_t n) {
-  const int64_t blocks = L * ((d + 127) / 128 + (n + 127) / 128);
-  int64_t z = (1024 + blocks - 1) / blocks;
-  const int64_t most = (M + 511) / 512;
-  z = z > most ? most : z;
-  z = z < 1 ? 1 : z;
-  int64_t per = ((M + z - 1) / z + 7) / 8 * 8;
-  per = per < 8 ? 8 : per;
-  const int64_t c = (M + per - 1) / per;
-  return {(int)(c < 1 ? 1 : c), per};
+// Blocks that share an adapter's rows in k_sums.
+int sum_shares(int64_t M, int64_t L, int64_t d, int64_t n) {
+  const int64_t blocks = L * ((d + 127) / 128 + (n + 127) / 128) * list_chunks(M, d, n);
+  const int64_t z = (512 + blocks - 1) / blocks, most = (M / L + 127) / 128;
+  return (int)(z > most ? (most < 1 ? 1 : most) : z);
 }
 
 template <int TY>
 hipError_t down(DownArgs a, int problems, hipStream_t st) {
-  const int rt = a.rp / 16;
-  const Slots sl = slots_of(a.M);
-  a.slots = sl.slots;
-  int64_t blocks = 0;
-  for (int i = 0; i < problems; ++i) {
-    const int64_t b = sl.tiles * sl.slots * a.of[i].splits * (sl.token ? rt : 1);
-    blocks = b > blocks ? b : blocks;
-  }
-  const dim3 grid((unsigned)blocks, (unsigned)problems);
-  if (sl.token) {
+  const int rt = a.rp / 16, splits = a.of[0].splits > a.of[1].splits ? a.of[0].splits : a.of[1].splits;
+  if (a.M <= kTokenRows) {
+    a.slots = token_slots(a.M);
+    const dim3 grid((unsigned)((a.M + 15) / 16 * a.slots * rt * splits), (unsigned)problems);
     k_down_few<TY><<<grid, 64 * kDownWaves, 0, st>>>(a);
     return hipGetLastError();
   }
+  const int64_t tiles = a.lists.chunk / 32 + (a.L < a.lists.chunk ? a.L : a.lists.chunk);
+  const dim3 grid((unsigned)(tiles * splits), (unsigned)problems, (unsigned)((a.M + a.lists.chunk - 1) / a.lists.chunk));
   return rt == 1   ? launch_down<TY, DownTile<1>>(a, grid, st)
          : rt == 2 ? launch_down<TY, DownTile<2>>(a, grid, st)
          : rt <= 4 ? launch_down<TY, DownTile<4>>(a, grid, st)
@@ -1097,12 +1151,11 @@ bool up_pads(int64_t M, int64_t r) { return M > kTokenRows && r % 8 != 0; }
 
 template <int TY>
 hipError_t up(UpArgs a, uint16_t* pad, hipStream_t st) {
-  const Slots sl = slots_of(a.M);
-  a.slots = sl.slots;
-  if (sl.token) {
+  if (a.M <= kTokenRows) {
+    a.slots = token_slots(a.M);
     const int64_t chunk = up_chunk(a.M, a.d, 1024);
     a.chunk = (int)chunk;
-    const dim3 grid((unsigned)(sl.tiles * sl.slots * ((a.d + chunk - 1) / chunk)));
+    const dim3 grid((unsigned)((a.M + 15) / 16 * a.slots * ((a.d + chunk - 1) / chunk)));
     return a.r % 8 == 0 && a.ld % 8 == 0 ? up_few<TY, true>(a, grid, st) : up_few<TY, false>(a, grid, st);
   }
   if (up_pads(a.M, a.r)) {
@@ -1114,9 +1167,10 @@ hipError_t up(UpArgs a, uint16_t* pad, hipStream_t st) {
     a.W = reinterpret_cast<const uint8_t*>(pad);
     a.r = a.ld = ld;
   }
-  const int64_t lots = (a.M + 63) / 64, chunk = up_chunk(lots, a.d, 512);
+  const int64_t chunk = up_chunk((a.M + 63) / 64, a.d, 512), rows = a.lists.chunk;
   a.chunk = (int)chunk;
-  const dim3 grid((unsigned)(lots * sl.slots * ((a.d + chunk - 1) / chunk)));
+  const int64_t tiles = rows / 64 + (a.L + 1 < rows ? a.L + 1 : rows);
+  const dim3 grid((unsigned)(tiles * ((a.d + chunk - 1) / chunk)), (unsigned)((a.M + rows - 1) / rows));
   if (a.r <= 32)
     k_up<TY, 1><<<grid, 256, 0, st>>>(a);
   else if (a.r <= 64)
@@ -1139,29 +1193,30 @@ void sums_rt(const SumArgs& a, dim3 grid, hipStream_t st) {
 }
 
 template <int TY>
-hipError_t sums(SumArgs a, const Parts& z, int out_dtype, float* ws, hipStream_t st) {
-  a.per = z.per;
+hipError_t sums(SumArgs a, int shares, int out_dtype, float* ws, hipStream_t st) {
+  a.shares = shares;
+  const int parts = shares * (int)((a.M + a.lists.chunk - 1) / a.lists.chunk > 1 ? (a.M + a.lists.chunk - 1) / a.lists.chunk : 1);
   PartsArgs q{};
   for (int i = 0; i < 2; ++i) {
     a.numel[i] = q.numel[i] = (int64_t)a.L * a.of[i].F * a.r;
     q.out[i] = a.of[i].out;
-    if (z.count > 1) a.of[i].out = ws + (i ? z.count * a.numel[0] : 0);
+    if (parts > 1) a.of[i].out = ws + (i ? parts * a.numel[0] : 0);
     q.in[i] = static_cast<const float*>(a.of[i].out);
   }
   a.blocks0 = (a.of[0].F + 127) / 128;
-  const dim3 grid((unsigned)(a.blocks0 + (a.of[1].F + 127) / 128), (unsigned)a.L, (unsigned)z.count);
-  if (z.count > 1 || out_dtype == T_FP32)
+  const dim3 grid((unsigned)(a.blocks0 + (a.of[1].F + 127) / 128), (unsigned)a.L, (unsigned)parts);
+  if (parts > 1 || out_dtype == T_FP32)
     sums_rt<TY, T_FP32>(a, grid, st);
   else
     sums_rt<TY, TY>(a, grid, st);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || z.count == 1) return e;
+  if (e != hipSuccess || parts == 1) return e;
   const int64_t want = ((q.numel[0] + q.numel[1]) / 4 + 255) / 256;
   const unsigned blocks = (unsigned)(want < 2048 ? want : 2048);
   if (out_dtype == T_FP32)
-    k_parts<T_FP32><<<blocks, 256, 0, st>>>(q, z.count);
+    k_parts<T_FP32><<<blocks, 256, 0, st>>>(q, parts);
   else
-    k_parts<TY><<<blocks, 256, 0, st>>>(q, z.count);
+    k_parts<TY><<<blocks, 256, 0, st>>>(q, parts);
   return hipGetLastError();
 }
 
@@ -1170,43 +1225,58 @@ bool in_one(int64_t M, int64_t d, int64_t n, int64_t r) {
   return round16(r) * n <= 65536 && M * ((d + kTokenCols - 1) / kTokenCols) <= 256;
 }
 
-// The workspace: h, A padded, and for the gradients dh, both in pieces, A and B transposed, and the
-// parts of the sums.
+// The workspace: h, the lists, A padded, and for the gradients dh, both in pieces, A and B transposed,
+// and the parts of the sums.
 struct Ws {
-  int64_t pad, dh, ph, pdh, at, bt, parts, bytes;
+  int64_t lists, pad, dh, ph, pdh, at, bt, parts, bytes;
 };
 Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   Ws w{};
   const int64_t rp = round16(r);
-  int64_t at = up256(4 * M * rp * down_splits(M, n, r));
   if (!grads && in_one(M, d, n, r)) return w;
+  int64_t at = up256(4 * M * rp * down_splits(M, n, r));
+  auto take = [&](int64_t& place, int64_t bytes) {
+    place = at;
+    at += up256(bytes);
+  };
+  if (grads || M > kTokenRows) take(w.lists, 4 * M + 12 * list_chunks(M, d, n) * (L + 2));
   if (!grads) {
-    w.pad = at;
-    at += up_pads(M, r) ? up256(2 * L * d * ((r + 7) / 8 * 8)) : 0;
+    take(w.pad, up_pads(M, r) ? 2 * L * d * ((r + 7) / 8 * 8) : 0);
   } else {
-    w.dh = at;
-    at += up256(4 * M * rp * down_splits(M, d, r));
-    w.ph = at;
-    at += up256(6 * M * rp);
-    w.pdh = at;
-    at += up256(6 * M * rp);
-    w.at = at;
-    at += up256(2 * L * r * d);
-    w.bt = at;
-    at += up256(2 * L * n * rp);
-    w.parts = at;
-    const int64_t z = sum_parts(M, L, d, n).count;
-    at += z > 1 ? up256(4 * z * L * r * (d + n)) : 0;
+    take(w.dh, 4 * M * rp * down_splits(M, d, r));
+    take(w.ph, 6 * M * rp);
+    take(w.pdh, 6 * M * rp);
+    take(w.at, 2 * L * r * d);
+    take(w.bt, 2 * L * n * rp);
+    const int64_t parts = sum_shares(M, L, d, n) * list_chunks(M, d, n);
+    take(w.parts, parts > 1 ? 4 * parts * L * r * (d + n) : 0);
   }
   w.bytes = at;
   return w;
 }
 
+Lists lists_of(const AdapterArgs& p, uint8_t* at) {
+  Lists l{};
+  const int64_t tables = list_chunks(p.M, p.d, p.n) * (p.L + 2);
+  l.order = reinterpret_cast<int32_t*>(at);
+  l.starts = l.order + p.M;
+  l.t32 = l.starts + tables;
+  l.t64 = l.t32 + tables;
+  l.M = p.M;
+  l.chunk = list_chunk(p.M, p.d, p.n);
+  l.L = (int)p.L;
+  return l;
+}
+
+hipError_t make_lists(const AdapterArgs& p, const Lists& l, hipStream_t st) {
+  k_lists<<<dim3((unsigned)(p.L + 1), (unsigned)list_chunks(p.M, p.d, p.n)), 1024, 0, st>>>(p.index, l);
+  return hipGetLastError();
+}
+
 template <int TY>
 hipError_t token(const Down& of, UpArgs a, hipStream_t st) {
-  const Slots sl = slots_of(a.M);
-  a.slots = sl.slots;
-  const dim3 grid((unsigned)(sl.tiles * sl.slots * ((a.d + kTokenCols - 1) / kTokenCols)));
+  a.slots = token_slots(a.M);
+  const dim3 grid((unsigned)((a.M + 15) / 16 * a.slots * ((a.d + kTokenCols - 1) / kTokenCols)));
   const int kt = (a.rp + 31) / 32, threads = 64 * kDownWaves;
   const bool wide = a.r % 8 == 0;
   if (kt == 1)
@@ -1253,11 +1323,16 @@ hipError_t fwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   y.d = (int)p.d;
   y.r = y.ld = (int)p.r;
   if (in_one(p.M, p.d, p.n, p.r)) return token<TY>(of, y, st);
+  const Ws w = carve(p.M, p.L, p.d, p.n, p.r, false);
   DownArgs x = down_args(p);
   x.of[0] = of;
-  const hipError_t e = down<TY>(x, 1, st);
-  if (e != hipSuccess) return e;
-  return up<TY>(y, reinterpret_cast<uint16_t*>(ws + carve(p.M, p.L, p.d, p.n, p.r, false).pad), st);
+  hipError_t e;
+  if (p.M > kTokenRows) {
+    x.lists = y.lists = lists_of(p, ws + w.lists);
+    if ((e = make_lists(p, x.lists, st)) != hipSuccess) return e;
+  }
+  if ((e = down<TY>(x, 1, st)) != hipSuccess) return e;
+  return up<TY>(y, reinterpret_cast<uint16_t*>(ws + w.pad), st);
 }
 
 template <int TY>
@@ -1268,7 +1343,10 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   uint16_t *at = reinterpret_cast<uint16_t*>(ws + w.at), *bt = reinterpret_cast<uint16_t*>(ws + w.bt);
   const uint8_t *X = static_cast<const uint8_t*>(p.X), *dY = static_cast<const uint8_t*>(p.dY);
   const int sh = down_splits(p.M, n, r), sd = down_splits(p.M, d, r);
-  hipError_t e;
+  const Lists lists = lists_of(p, ws + w.lists);
+  // (without a row too: the lists are then empty)
+  hipError_t e = make_lists(p, lists, st);
+  if (e != hipSuccess) return e;
   if (p.M > 0) {
     TurnArgs t{};
     t.of[0] = Turn{static_cast<const uint16_t*>(p.A), at, d, r, d, (r + 31) / 32, (r + 31) / 32 * ((d + 31) / 32)};
@@ -1276,11 +1354,13 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
     k_turn<<<dim3(t.of[0].tiles + (p.Y ? t.of[1].tiles : 0), L), 256, 0, st>>>(t);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     DownArgs x = down_args(p);
+    x.lists = lists;
     x.of[0] = Down{X, static_cast<const uint8_t*>(p.B), h, n, sh};
     x.of[1] = Down{dY, reinterpret_cast<const uint8_t*>(at), dh, d, sd};
     if ((e = down<TY>(x, 2, st)) != hipSuccess) return e;
     if (p.Y) {
       UpArgs y = up_args(p);
+      y.lists = lists;
       y.H = dh;
       y.splits = sd;
       y.W = reinterpret_cast<const uint8_t*>(bt);
@@ -1296,34 +1376,39 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
     x.of[1] = Split{dh, pdh, sd};
     x.index = p.index;
     x.scale = p.scale;
+    x.lists = lists;
     x.M = p.M;
     x.L = L;
     x.rp = rp;
+    x.by_row = p.M <= kTokenRows;
     k_split<<<dim3((unsigned)((p.M * (rp / 4) + 255) / 256), 2), 256, 0, st>>>(x);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   SumArgs q{};
-  q.index = p.index;
+  q.lists = lists;
   q.M = p.M;
   q.L = L;
   q.r = r;
   q.rp = rp;
   q.of[0] = Sum{dY, ph, p.dA, d};
   q.of[1] = Sum{X, pdh, p.dB, n};
-  return sums<TY>(q, sum_parts(p.M, L, d, n), p.out_dtype, reinterpret_cast<float*>(ws + w.parts), st);
+  return sums<TY>(q, sum_shares(p.M, L, d, n), p.out_dtype, reinterpret_cast<float*>(ws + w.parts), st);
 }
 
 }  // namespace
 
-// Blocks of the largest launch: a grid holds less than 2^32 work-items.
-bool adapters_fit(int64_t M, int64_t d, int64_t n, int64_t r) {
-  const Slots sl = slots_of(M);
-  const int64_t widest = d > n ? d : n, blocks = sl.tiles * sl.slots;
-  const int64_t ups = blocks * ((widest + 127) / 128 < 8 ? (widest + 127) / 128 : (widest + 1023) / 1024 + 8);
-  const int64_t downs = blocks * (sl.token ? 8 : 1) * 8;  // ranks, splits
-  const int64_t turns = (d + 31) / 32 * ((r + 31) / 32) + (n + 31) / 32 * ((r + 31) / 32);
-  const int64_t most = int64_t(1) << 32;
-  return M * (round16(r) / 4) + 256 < most && ups * 256 < most && downs * 64 * kDownWaves < most && turns < (int64_t(1) << 31);
+// Whether every launch holds: less than 2^32 work-items, at most 65535 blocks along y and z.
+bool adapters_fit(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r) {
+  const int64_t most = int64_t(1) << 32, widest = d > n ? d : n, chunks = list_chunks(M, d, n);
+  const int64_t turns = ((d + 31) / 32 + (n + 31) / 32) * ((round16(r) + 31) / 32);
+  if (chunks * sum_shares(M, L, d, n) > 65535 || turns * L * 256 >= most || M * (round16(r) / 4) + 256 >= most) return false;
+  if (M <= kTokenRows) {
+    const int64_t tokens = (M + 15) / 16 * 16;
+    return tokens * ((widest + 127) / 128) * 256 < most && tokens * 8 * 8 * 64 * kDownWaves < most;
+  }
+  const int64_t downs = most_tiles(M, L, d, n, 32) * 8 * 2 * chunks;
+  const int64_t ups = most_tiles(M, L, d, n, 64) * ((widest + 1023) / 1024 + 4) * chunks;
+  return downs * 256 < most && ups * 256 < most;
 }
 
 size_t adapters_ws_bytes(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {

@@ -379,7 +379,7 @@ int check_adapters(const intlora::AdapterArgs& a, const char* what) {
       a.d % 8 != 0 || a.n % 8 != 0)
     return fail(INTLORA_ESHAPE, "%s: bad shape M=%lld d=%lld n=%lld (d, n multiples of 8, <= 2^20)", what,
                 (long long)a.M, (long long)a.d, (long long)a.n);
-  if (!intlora::adapters_fit(a.M, a.d, a.n, a.r)) return fail(INTLORA_ESHAPE, "%s: too many tiles", what);
+  if (!intlora::adapters_fit(a.M, a.L, a.d, a.n, a.r)) return fail(INTLORA_ESHAPE, "%s: too many tiles", what);
   return INTLORA_OK;
 }
 

@@ -276,3 +276,60 @@ def test_beside_the_integer_layer(ops):
     out = ops.adapters_linear(y, k["x"], k["index"], k["A"], k["B"], k["scale"], out=y)
     want, spread = ref.forward(f64(c["base"]), f64(c["x"]), c["index"].numpy(), f64(c["A"]), f64(c["B"]), f64(c["scale"]))
     check(out, want, spread, "y")
+
+
+@pytest.mark.parametrize("M,L,d,n,r", [(1100, 2, 16, 1 << 20, 3), (2200, 3, 1 << 19, 8, 5)])
+def test_past_31_bits(ops, M, L, d, n, r):
+    """Tensors of more than 2^31 bytes: rows go in several chunks.  Reference in fp64 on the device,
+    a slice of columns at a time."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(torch.bfloat16)
+    x, A, B, base, dy = rand(M, n), rand(L, d, r), rand(L, r, n, std=n ** -0.5), rand(M, d), rand(M, d)
+    ids = torch.randint(-1, L, (M,), generator=g, device="cuda", dtype=torch.int32)
+    s = torch.rand(L, generator=g, device="cuda") + 0.5
+    assert max(M * n, M * d) * 2 > 1 << 31
+    y = ops.adapters_linear(base, x, ids, A, B, s)
+    dx, dA, dB = ops.adapters_linear_grad(dy, x, ids, A, B, s, dtype=torch.float32)
+
+    def cols(width):
+        return [slice(i, i + (1 << 16)) for i in range(0, width, 1 << 16)]
+
+    for a in range(-1, L):
+        rows = torch.nonzero(ids == a).flatten()
+        if a < 0:
+            assert torch.equal(y[rows], base[rows]) and not dx[rows].any()
+            continue
+        h = sum(x[rows][:, c].double() @ B[a][:, c].double().T for c in cols(n)) * s[a].double()
+        dh = sum(dy[rows][:, c].double() @ A[a][c].double() for c in cols(d)) * s[a].double()
+        # binary32 sums over n (d) products of about unit size: 2^-23 of the sum of magnitudes, at most
+        # n 2^-23 times the mean product; two roundings to bf16 outputs
+        for got, want, left in ((y, lambda c: base[rows][:, c].double() + h @ A[a][c].double().T, d),
+                                (dx, lambda c: dh @ B[a][:, c].double(), n)):
+            for c in cols(left):
+                w = want(c)
+                scale = w.abs().amax(1, keepdim=True) + 1.0
+                assert ((got[rows][:, c].double() - w).abs() <= 2.0 ** -8 * (w.abs() + 2.0 ** -3 * scale)).all()
+        for got, want, width in ((dA[a], lambda c: dy[rows][:, c].double().T @ h, d),
+                                 (dB[a].T, lambda c: x[rows][:, c].double().T @ dh, n)):
+            for c in cols(width):
+                w = want(c)
+                assert ((got[c].double() - w).abs() <= 2.0 ** -12 * (w.abs().max() + 1.0)).all()
+
+
+@pytest.mark.parametrize("L", [1, 61, 62, 63, 64, 65, 127, 128, 130, 700, 4096])
+@pytest.mark.parametrize("kind", ["random", "runs"])
+def test_many_adapters(ops, L, kind):
+    """Numbers of adapters around what a wave looks at when it finds its rows."""
+    c = make(2600, L, 32, 40, 3, "bf16", kind)
+    forward(ops, c)
+    if L in (1, 63, 64, 130, 4096):
+        backward(ops, c)
+
+
+def test_long_lists(ops):
+    """More rows than a listing block takes at a time, one adapter with nearly all of them."""
+    c = make(20000, 3, 24, 16, 4, "fp16", "random")
+    c["index"][c["index"] == 1] = 0
+    c["index"][::997] = 1
+    forward(ops, c)
+    backward(ops, c)
