@@ -67,16 +67,60 @@ struct Lists {
   }
 };
 
+// For the gradients, out[a] (cols x ldo) = in[a] (rows x cols) transposed, zeros from column `rows` on, of
+// both factors.
+struct Turn {
+  const uint16_t* in;
+  uint16_t* out;
+  int rows, cols, ldo, tiles_x, tiles;  // tiles of 32 x 32: along the columns, in all
+};
+struct ListArgs {
+  const int32_t* index;
+  Lists lists;
+  int blocks;  // L + 1 for each chunk; the blocks behind them turn four tiles each
+  Turn turn[2];
+};
+
+__device__ __forceinline__ void turn_tile(const ListArgs& p, int unit) {
+  __shared__ uint16_t tiles[4][32][34];
+  auto& t = tiles[threadIdx.x >> 8];
+  const int all = p.turn[0].tiles + p.turn[1].tiles, a = unit / all, in_a = unit - a * all;
+  const bool live = a < p.lists.L, second = in_a >= p.turn[0].tiles;
+  const Turn& w = p.turn[second];
+  const int tile = in_a - (second ? p.turn[0].tiles : 0);
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5 & 7;
+  const int64_t c0 = (int64_t)(tile % w.tiles_x) * 32, r0 = (int64_t)(tile / w.tiles_x) * 32;
+  const uint16_t* in = w.in + (int64_t)a * w.rows * w.cols;
+  uint16_t* out = w.out + (int64_t)a * w.cols * w.ldo;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + y + 8 * i, c = c0 + x;
+    t[y + 8 * i][x] = live && r < w.rows && c < w.cols ? in[r * w.cols + c] : 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = c0 + y + 8 * i, c = r0 + x;
+    if (live && r < w.cols && c < w.ldo) out[r * w.ldo + c] = t[x][y + 8 * i];
+  }
+}
+
 // A block for each group: it counts all rows by adapter in LDS, which gives its first place and
-// tiles, and then lists its own.  Bound by latency: 8192 rows LISTS_US.
+// tiles, and then lists its own.  Bound by latency: 8192 rows of 16 adapters LISTS_US.
 constexpr int kMaxGroups = 4096 + 1;
 
-__global__ void __launch_bounds__(1024) k_lists(const int32_t* __restrict__ index, const Lists l) {
+__global__ void __launch_bounds__(1024) k_lists(const ListArgs p) {
   __shared__ int count[kMaxGroups];
   __shared__ int sums[16][3];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = blockIdx.x, c = blockIdx.y;
-  const int rows = l.rows(c), groups = l.L + 1;
-  index += c * l.chunk;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if ((int)blockIdx.x >= p.blocks) {
+    turn_tile(p, ((int)blockIdx.x - p.blocks) * 4 + (tid >> 8));
+    return;
+  }
+  const Lists& l = p.lists;
+  const int groups = l.L + 1, c = blockIdx.x / groups, g = blockIdx.x - c * groups;
+  const int rows = l.rows(c);
+  const int32_t* index = p.index + c * l.chunk;
   for (int i = tid; i < groups; i += 1024) count[i] = 0;
   __syncthreads();
   // the groups of rows r .. r + 7 (-1 past the end)
@@ -91,9 +135,16 @@ __global__ void __launch_bounds__(1024) k_lists(const int32_t* __restrict__ inde
 #pragma unroll
     for (int e = 0; e < 8; ++e) k[e] = r + e >= rows ? -1 : k[e] >= 0 && k[e] < l.L ? k[e] : l.L;
   };
-  for (int r = 8 * tid; r < rows; r += 8192) {
-    int k[8];
-    keys(r, k);
+  int k[8];
+  for (int r0 = 0; r0 < rows; r0 += 8192) {
+    keys(r0 + 8 * tid, k);
+    bool same = true;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) same = same && k[e] == __builtin_amdgcn_readfirstlane(k[0]);
+    if (__builtin_amdgcn_ballot_w64(!same) == 0) {  // the wave's 512 rows at once
+      if (lane == 0 && k[0] >= 0) atomicAdd(&count[k[0]], 512);
+      continue;
+    }
     int at = k[0], n = 1;  // neighbours of one group at once
 #pragma unroll
     for (int e = 1; e < 8; ++e) {
@@ -116,16 +167,17 @@ __global__ void __launch_bounds__(1024) k_lists(const int32_t* __restrict__ inde
     s[2] += (n + 63) / 64;
   }
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
+  for (int x = 0; x < 3; ++x) {
 #pragma unroll
-    for (int x = 32; x; x >>= 1) s[k] += __shfl_xor(s[k], x);
-    if (lane == 0) sums[wave][k] = s[k];
+    for (int y = 32; y; y >>= 1) s[x] += __shfl_xor(s[x], y);
+    if (lane == 0) sums[wave][x] = s[x];
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    s[k] = 0;
-    for (int w = 0; w < 16; ++w) s[k] += sums[w][k];
+  for (int x = 0; x < 3; ++x) {
+    s[x] = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) s[x] += sums[w][x];
   }
   const int mine = count[g], at = c * (l.L + 2) + g;
   if (tid == 0) {
@@ -141,8 +193,7 @@ __global__ void __launch_bounds__(1024) k_lists(const int32_t* __restrict__ inde
   if (mine == 0) return;
   int32_t* out = l.order + c * l.chunk + s[0];
   for (int r0 = 0; r0 < rows; r0 += 8192) {
-    int k[8];
-    keys(r0 + 8 * tid, k);
+    if (rows > 8192) keys(r0 + 8 * tid, k);  // (else they are still there)
     int n = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) n += k[e] == g;
@@ -157,6 +208,7 @@ __global__ void __launch_bounds__(1024) k_lists(const int32_t* __restrict__ inde
     __syncthreads();
     before -= n;
     int all = 0;
+#pragma unroll
     for (int w = 0; w < 16; ++w) {
       if (w < wave) before += sums[w][0];
       all += sums[w][0];
@@ -195,14 +247,31 @@ __device__ __forceinline__ Place find_tile(const Lists& l, int c, int tile) {
 
 // h = W_a x of one or two problems (h and dh: blockIdx.y).
 struct Down {
-  const uint8_t* X;  // M x n
-  const uint8_t* W;  // L x r x n
-  float* H;          // splits x M x rp
+  const uint8_t* X;   // M x n
+  const uint8_t* W;   // L x r x n
+  float* H;           // splits x M x rp (NULL: not wanted)
   int n, splits;
+  uint16_t* pieces;   // more tokens, one split: h scaled, in pieces, as k_split's (NULL: not wanted)
 };
+
+// The bf16 number at or next to v towards zero three times over, each of what the last one left, of
+// four numbers: 24 bits in three pieces.
+__device__ __forceinline__ void put_pieces(v4f v, uint16_t* out, int64_t stride) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    float t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      t[e] = top_bf16(v[e]);
+      v[e] = finite(v[e]) ? v[e] - t[e] : 0.f;
+    }
+    *reinterpret_cast<uint2*>(out + k * stride) = make_uint2(pack2<T_BF16>(t[0], t[1]), pack2<T_BF16>(t[2], t[3]));
+  }
+}
 struct DownArgs {
   Down of[2];
   const int32_t* index;
+  const float* scale;
   Lists lists;
   int64_t M;
   int L, r, rp;
@@ -361,8 +430,10 @@ __global__ void __launch_bounds__(256) k_down(const DownArgs p) {
 #pragma unroll
     for (int w = 1; w < 4; ++w) s += sums[(w * 2 * RT + z) * 64 + lane];
     const int i = 16 * (z & 1) + fr, g = 16 * (z >> 1);
-    if (i < pl.rows && g < p.rp)
-      *reinterpret_cast<v4f*>(of.H + (split * p.M + first + pl.at + i) * p.rp + g + 4 * q) = s;
+    if (i >= pl.rows || g >= p.rp) continue;
+    const int64_t to = (first + pl.at + i) * p.rp + g + 4 * q;
+    if (of.H) *reinterpret_cast<v4f*>(of.H + split * p.M * p.rp + to) = s;
+    if (of.pieces) put_pieces(s * p.scale[a], of.pieces + to, p.M * p.rp);
   }
 }
 
@@ -805,37 +876,6 @@ hipError_t launch_down(const DownArgs& a, dim3 grid, hipStream_t st) {
   return hipGetLastError();
 }
 
-// out[a] (cols x ldo) = in[a] (rows x cols) transposed, zeros from column `rows` on, of both factors.
-struct Turn {
-  const uint16_t* in;
-  uint16_t* out;
-  int rows, cols, ldo, tiles_x, tiles;  // tiles of 32 x 32: along the columns, in all
-};
-struct TurnArgs {
-  Turn of[2];
-};
-__global__ void __launch_bounds__(256) k_turn(const TurnArgs p) {
-  __shared__ uint16_t t[32][34];
-  const bool second = (int)blockIdx.x >= p.of[0].tiles;
-  const Turn& w = p.of[second];
-  const int tile = blockIdx.x - (second ? p.of[0].tiles : 0);
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int64_t c0 = (int64_t)(tile % w.tiles_x) * 32, r0 = (int64_t)(tile / w.tiles_x) * 32;
-  const uint16_t* in = w.in + (int64_t)blockIdx.y * w.rows * w.cols;
-  uint16_t* out = w.out + (int64_t)blockIdx.y * w.cols * w.ldo;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = r0 + y + 8 * i, c = c0 + x;
-    t[y + 8 * i][x] = r < w.rows && c < w.cols ? in[r * w.cols + c] : 0;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = c0 + y + 8 * i, c = r0 + x;
-    if (r < w.cols && c < w.ldo) out[r * w.ldo + c] = t[x][y + 8 * i];
-  }
-}
-
 // h and dh, scaled, as three bf16 numbers each (24 bits) for k_sums: planes x M x rp, by place in the
 // lists.  Rows without an adapter are left out.
 struct Split {
@@ -867,17 +907,7 @@ __global__ void __launch_bounds__(256) k_split(const SplitArgs p) {
     const float4 x = *reinterpret_cast<const float4*>(H + z * p.M * p.rp);
     h.x += x.x, h.y += x.y, h.z += x.z, h.w += x.w;
   }
-  float v[4] = {h.x * s, h.y * s, h.z * s, h.w * s};
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    float t[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      t[e] = top_bf16(v[e]);
-      v[e] = finite(v[e]) ? v[e] - t[e] : 0.f;
-    }
-    *reinterpret_cast<uint2*>(of.out + k * p.M * p.rp + 4 * u) = make_uint2(pack2<T_BF16>(t[0], t[1]), pack2<T_BF16>(t[2], t[3]));
-  }
+  put_pieces(v4f{h.x * s, h.y * s, h.z * s, h.w * s}, of.out + 4 * u, p.M * p.rp);
 }
 
 struct Sum {
@@ -1107,7 +1137,7 @@ int down_splits(int64_t M, int64_t n, int64_t r) {
 // Blocks that share an adapter's rows in k_sums.
 int sum_shares(int64_t M, int64_t L, int64_t d, int64_t n) {
   const int64_t blocks = L * ((d + 127) / 128 + (n + 127) / 128) * list_chunks(M, d, n);
-  const int64_t z = (512 + blocks - 1) / blocks, most = (M / L + 127) / 128;
+  const int64_t z = blocks > 0 && blocks < 512 ? 512 / blocks : 1, most = (M / L + 127) / 128;  // two to a compute unit
   return (int)(z > most ? (most < 1 ? 1 : most) : z);
 }
 
@@ -1268,8 +1298,11 @@ Lists lists_of(const AdapterArgs& p, uint8_t* at) {
   return l;
 }
 
-hipError_t make_lists(const AdapterArgs& p, const Lists& l, hipStream_t st) {
-  k_lists<<<dim3((unsigned)(p.L + 1), (unsigned)list_chunks(p.M, p.d, p.n)), 1024, 0, st>>>(p.index, l);
+hipError_t make_lists(const AdapterArgs& p, ListArgs a, hipStream_t st) {
+  a.index = p.index;
+  a.blocks = (int)((p.L + 1) * list_chunks(p.M, p.d, p.n));
+  const int64_t turns = p.L * (a.turn[0].tiles + a.turn[1].tiles);
+  k_lists<<<(unsigned)(a.blocks + (turns + 3) / 4), 1024, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -1315,7 +1348,7 @@ template <int TY>
 hipError_t fwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   float* h = reinterpret_cast<float*>(ws);
   const int s = down_splits(p.M, p.n, p.r);
-  const Down of{static_cast<const uint8_t*>(p.X), static_cast<const uint8_t*>(p.B), h, (int)p.n, s};
+  const Down of{static_cast<const uint8_t*>(p.X), static_cast<const uint8_t*>(p.B), h, (int)p.n, s, nullptr};
   UpArgs y = up_args(p);
   y.H = h;
   y.splits = s;
@@ -1328,8 +1361,9 @@ hipError_t fwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   x.of[0] = of;
   hipError_t e;
   if (p.M > kTokenRows) {
-    x.lists = y.lists = lists_of(p, ws + w.lists);
-    if ((e = make_lists(p, x.lists, st)) != hipSuccess) return e;
+    ListArgs l{};
+    l.lists = x.lists = y.lists = lists_of(p, ws + w.lists);
+    if ((e = make_lists(p, l, st)) != hipSuccess) return e;
   }
   if ((e = down<TY>(x, 1, st)) != hipSuccess) return e;
   return up<TY>(y, reinterpret_cast<uint16_t*>(ws + w.pad), st);
@@ -1343,20 +1377,24 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   uint16_t *at = reinterpret_cast<uint16_t*>(ws + w.at), *bt = reinterpret_cast<uint16_t*>(ws + w.bt);
   const uint8_t *X = static_cast<const uint8_t*>(p.X), *dY = static_cast<const uint8_t*>(p.dY);
   const int sh = down_splits(p.M, n, r), sd = down_splits(p.M, d, r);
+  uint16_t *ph = reinterpret_cast<uint16_t*>(ws + w.ph), *pdh = reinterpret_cast<uint16_t*>(ws + w.pdh);
   const Lists lists = lists_of(p, ws + w.lists);
-  // (without a row too: the lists are then empty)
-  hipError_t e = make_lists(p, lists, st);
+  ListArgs l{};
+  l.lists = lists;
+  if (p.M > 0) {
+    l.turn[0] = Turn{static_cast<const uint16_t*>(p.A), at, d, r, d, (r + 31) / 32, (r + 31) / 32 * ((d + 31) / 32)};
+    if (p.Y)
+      l.turn[1] = Turn{static_cast<const uint16_t*>(p.B), bt, r, n, rp, (n + 31) / 32, (n + 31) / 32 * ((rp + 31) / 32)};
+  }
+  hipError_t e = make_lists(p, l, st);  // (without a row too: the lists are then empty)
   if (e != hipSuccess) return e;
   if (p.M > 0) {
-    TurnArgs t{};
-    t.of[0] = Turn{static_cast<const uint16_t*>(p.A), at, d, r, d, (r + 31) / 32, (r + 31) / 32 * ((d + 31) / 32)};
-    t.of[1] = Turn{static_cast<const uint16_t*>(p.B), bt, r, n, rp, (n + 31) / 32, (n + 31) / 32 * ((rp + 31) / 32)};
-    k_turn<<<dim3(t.of[0].tiles + (p.Y ? t.of[1].tiles : 0), L), 256, 0, st>>>(t);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const bool few = p.M <= kTokenRows, split = few || sh > 1 || sd > 1;
     DownArgs x = down_args(p);
     x.lists = lists;
-    x.of[0] = Down{X, static_cast<const uint8_t*>(p.B), h, n, sh};
-    x.of[1] = Down{dY, reinterpret_cast<const uint8_t*>(at), dh, d, sd};
+    x.scale = p.scale;
+    x.of[0] = Down{X, static_cast<const uint8_t*>(p.B), split ? h : nullptr, n, sh, split ? nullptr : ph};
+    x.of[1] = Down{dY, reinterpret_cast<const uint8_t*>(at), split || p.Y ? dh : nullptr, d, sd, split ? nullptr : pdh};
     if ((e = down<TY>(x, 2, st)) != hipSuccess) return e;
     if (p.Y) {
       UpArgs y = up_args(p);
@@ -1368,21 +1406,20 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
       y.r = y.ld = rp;  // (the padding is zeros on both sides)
       if ((e = up<TY>(y, nullptr, st)) != hipSuccess) return e;
     }
-  }
-  uint16_t *ph = reinterpret_cast<uint16_t*>(ws + w.ph), *pdh = reinterpret_cast<uint16_t*>(ws + w.pdh);
-  if (p.M > 0) {
-    SplitArgs x{};
-    x.of[0] = Split{h, ph, sh};
-    x.of[1] = Split{dh, pdh, sd};
-    x.index = p.index;
-    x.scale = p.scale;
-    x.lists = lists;
-    x.M = p.M;
-    x.L = L;
-    x.rp = rp;
-    x.by_row = p.M <= kTokenRows;
-    k_split<<<dim3((unsigned)((p.M * (rp / 4) + 255) / 256), 2), 256, 0, st>>>(x);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (split) {
+      SplitArgs v{};
+      v.of[0] = Split{h, ph, sh};
+      v.of[1] = Split{dh, pdh, sd};
+      v.index = p.index;
+      v.scale = p.scale;
+      v.lists = lists;
+      v.M = p.M;
+      v.L = L;
+      v.rp = rp;
+      v.by_row = few;
+      k_split<<<dim3((unsigned)((p.M * (rp / 4) + 255) / 256), 2), 256, 0, st>>>(v);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
   }
   SumArgs q{};
   q.lists = lists;
@@ -1401,7 +1438,7 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
 bool adapters_fit(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r) {
   const int64_t most = int64_t(1) << 32, widest = d > n ? d : n, chunks = list_chunks(M, d, n);
   const int64_t turns = ((d + 31) / 32 + (n + 31) / 32) * ((round16(r) + 31) / 32);
-  if (chunks * sum_shares(M, L, d, n) > 65535 || turns * L * 256 >= most || M * (round16(r) / 4) + 256 >= most) return false;
+  if (chunks * sum_shares(M, L, d, n) > 65535 || (turns * L + 4) * 256 + (L + 1) * chunks * 1024 >= most || M * (round16(r) / 4) + 256 >= most) return false;
   if (M <= kTokenRows) {
     const int64_t tokens = (M + 15) / 16 * 16;
     return tokens * ((widest + 127) / 128) * 256 < most && tokens * 8 * 8 * 64 * kDownWaves < most;
