@@ -56,11 +56,11 @@ __device__ __forceinline__ int leader(int id, int slot) {
 // Rows are taken `chunk` at a time (less than 2^31 bytes of any of the tensors, so that offsets
 // inside fit 32 bits; one chunk as a rule).  For each chunk: order[] = its rows sorted by adapter, the ones
 // without an adapter last (group L); group g has the places starts[g] .. starts[g + 1] - 1, and the
-// tiles t32[g] .. of 32 places, t64[g] .. of 64.
+// tiles t32[g] .. of 32 places, t64[g] .. of 64, tp[g] .. of `part`.
 struct Lists {
-  int32_t *order, *starts, *t32, *t64;  // order: M; the others chunks x (L + 2)
+  int32_t *order, *starts, *t32, *t64, *tp;  // order: M; the others chunks x (L + 2)
   int64_t M, chunk;
-  int L;
+  int L, part;
   __device__ __forceinline__ int rows(int c) const {
     const int64_t n = M - c * chunk;
     return (int)(n < chunk ? n : chunk);
@@ -111,7 +111,7 @@ constexpr int kMaxGroups = 4096 + 1;
 
 __global__ void __launch_bounds__(1024) k_lists(const ListArgs p) {
   __shared__ int count[kMaxGroups];
-  __shared__ int sums[16][3];
+  __shared__ int sums[16][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if ((int)blockIdx.x >= p.blocks) {
     turn_tile(p, ((int)blockIdx.x - p.blocks) * 4 + (tid >> 8));
@@ -159,22 +159,23 @@ __global__ void __launch_bounds__(1024) k_lists(const ListArgs p) {
     if (at >= 0) atomicAdd(&count[at], n);
   }
   __syncthreads();
-  int s[3] = {0, 0, 0};  // places and tiles in front
+  int s[4] = {0, 0, 0, 0};  // places and tiles in front
   for (int i = tid; i < g; i += 1024) {
     const int n = count[i];
     s[0] += n;
     s[1] += (n + 31) / 32;
     s[2] += (n + 63) / 64;
+    s[3] += (n + l.part - 1) / l.part;
   }
 #pragma unroll
-  for (int x = 0; x < 3; ++x) {
+  for (int x = 0; x < 4; ++x) {
 #pragma unroll
     for (int y = 32; y; y >>= 1) s[x] += __shfl_xor(s[x], y);
     if (lane == 0) sums[wave][x] = s[x];
   }
   __syncthreads();
 #pragma unroll
-  for (int x = 0; x < 3; ++x) {
+  for (int x = 0; x < 4; ++x) {
     s[x] = 0;
 #pragma unroll
     for (int w = 0; w < 16; ++w) s[x] += sums[w][x];
@@ -184,10 +185,12 @@ __global__ void __launch_bounds__(1024) k_lists(const ListArgs p) {
     l.starts[at] = s[0];
     l.t32[at] = s[1];
     l.t64[at] = s[2];
+    l.tp[at] = s[3];
     if (g == l.L) {
       l.starts[at + 1] = s[0] + mine;
       l.t32[at + 1] = s[1] + (mine + 31) / 32;
       l.t64[at + 1] = s[2] + (mine + 63) / 64;
+      l.tp[at + 1] = s[3] + (mine + l.part - 1) / l.part;
     }
   }
   if (mine == 0) return;
@@ -220,13 +223,14 @@ __global__ void __launch_bounds__(1024) k_lists(const ListArgs p) {
   }
 }
 
-// The group, first place and places of a tile of SIZE places; rows = 0: there is no such tile.
+// The group, first place and places of a tile of SIZE places (0: `part`); rows = 0: there is no such
+// tile.
 struct Place {
   int group, at, rows;
 };
 template <int SIZE>
 __device__ __forceinline__ Place find_tile(const Lists& l, int c, int tile) {
-  const int32_t *t = (SIZE == 32 ? l.t32 : l.t64) + c * (l.L + 2), *starts = l.starts + c * (l.L + 2);
+  const int32_t *t = (SIZE == 32 ? l.t32 : SIZE == 64 ? l.t64 : l.tp) + c * (l.L + 2), *starts = l.starts + c * (l.L + 2);
   const int lane = threadIdx.x & 63, last = l.L + 1;
   // the last group whose first tile is not behind this one: 64 at a time, before them every 128th
   int base = 0;
@@ -241,8 +245,8 @@ __device__ __forceinline__ Place find_tile(const Lists& l, int c, int tile) {
   }
   const int g = __builtin_amdgcn_readfirstlane(base + n - 1);
   if (g >= last) return Place{last, 0, 0};
-  const int at = starts[g] + SIZE * (tile - t[g]), left = starts[g + 1] - at;
-  return Place{g, __builtin_amdgcn_readfirstlane(at), __builtin_amdgcn_readfirstlane(left < SIZE ? left : SIZE)};
+  const int size = SIZE ? SIZE : l.part, at = starts[g] + size * (tile - t[g]), left = starts[g + 1] - at;
+  return Place{g, __builtin_amdgcn_readfirstlane(at), __builtin_amdgcn_readfirstlane(left < size ? left : size)};
 }
 
 // h = W_a x of one or two problems (h and dh: blockIdx.y).
@@ -921,13 +925,13 @@ struct SumArgs {
   Lists lists;
   int64_t M;
   int L, r, rp;
-  int blocks0;       // blocks of 128 columns of the first one
-  int shares;        // blocks that share an adapter's rows of a chunk
-  int64_t numel[2];  // of the outputs: parts lie one after the other
+  int blocks0;   // blocks of 128 columns of the first one
+  int parts;     // of a chunk at most, each with sums of its own (float); 0: a block takes all of an adapter
+  int64_t each;  // numbers of a part: d r of dA's, then r n of dB's
 };
 
-// sum over an adapter's tokens of P_t h_t^T s_a.  A block takes 128 columns of P, all ranks and its
-// share of the adapter's rows, T of them at a time, each wave 32 columns x 16 RT ranks; the next
+// sum over an adapter's tokens of P_t h_t^T s_a.  A block takes 128 columns of P, all ranks and all of
+// the adapter's rows, or one of the parts that they are cut into, T of them at a time, each wave 32 columns x 16 RT ranks; the next
 // ones are loaded meanwhile.  Both operands have the
 // contraction (tokens) in rows and leave LDS through the transposing reads.  h is three bf16 numbers;
 // fp16 rows of P become two (exact).
@@ -943,18 +947,20 @@ struct SumLds {
 };
 
 template <int TY, int TO, int RT, bool RANK_LANES>
-__device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64_t numel, int block, SumLds<TY, RT>& L) {
+__device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int block, SumLds<TY, RT>& L) {
   using S = SumLds<TY, RT>;
   constexpr int PP = S::PP, T = S::T, PS = S::PS, HS = S::HS, NT = S::F / 64;
   constexpr int NP = T / 16, NH = (6 * T * RT + 255) / 256;  // 16-byte loads of a thread
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, fr = lane & 15, q = lane >> 4;
-  const int a = blockIdx.y, f0 = block * S::F;
-  const int c = blockIdx.z / p.shares, share = blockIdx.z - c * p.shares;
-  const int64_t first = c * p.lists.chunk;  // the chunk's first row, and first place
-  const int32_t* starts = p.lists.starts + c * (p.L + 2) + a;
-  const int64_t lots = (starts[1] - starts[0] + T - 1) / T;
-  const int r0 = starts[0] + (int)(lots * share / p.shares) * T;
-  const int r1 = share + 1 == p.shares ? starts[1] : starts[0] + (int)(lots * (share + 1) / p.shares) * T;
+  const int f0 = block * S::F, c0 = p.parts ? blockIdx.z : 0;
+  const int chunks = p.parts ? c0 + 1 : (int)((p.M + p.lists.chunk - 1) / p.lists.chunk);
+  int a = blockIdx.y;
+  Place pl{};
+  if (p.parts) {
+    pl = find_tile<0>(p.lists, c0, blockIdx.y);
+    a = pl.group;
+    if (pl.rows <= 0 || a >= p.L) return;
+  }
   v4f acc[NT][RT];
 #pragma unroll
   for (int j = 0; j < NT * RT; ++j) acc[j / RT][j % RT] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -964,7 +970,7 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64
   Lot lot;
 
   // places at + from .. at + n - 1, at most T: zeros behind them; list: their rows from `at` on
-  auto fetch = [&](int at0, int from, int n) {
+  auto fetch = [&](int64_t first, int at0, int from, int n) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int row = (tid >> 4) + 16 * i, c = (tid & 15) * 8;
@@ -1032,22 +1038,29 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64
         }
     }
   };
-  for (int at = r0; at < r1; at += S::kList) {
-    const int n = r1 - at < S::kList ? r1 - at : S::kList;
-    __syncthreads();
-    for (int i = tid; i < n; i += 256) L.list[i] = p.lists.order[first + at + i];
-    __syncthreads();
-    fetch(at, 0, n);
-    for (int from = 0; from < n; from += T) {
+  for (int c = c0; c < chunks; ++c) {
+    const int64_t first = c * p.lists.chunk;  // the chunk's first row, and first place
+    const int32_t* starts = p.lists.starts + c * (p.L + 2) + a;
+    const int r0 = p.parts ? pl.at : starts[0], r1 = p.parts ? pl.at + pl.rows : starts[1];
+    for (int at = r0; at < r1; at += S::kList) {
+      const int n = r1 - at < S::kList ? r1 - at : S::kList;
       __syncthreads();
-      store();
+      for (int i = tid; i < n; i += 256) L.list[i] = p.lists.order[first + at + i];
       __syncthreads();
-      fetch(at, from + T, n);
-      __builtin_amdgcn_sched_barrier(0);
-      add();
+      fetch(first, at, 0, n);
+      for (int from = 0; from < n; from += T) {
+        __syncthreads();
+        store();
+        __syncthreads();
+        fetch(first, at, from + T, n);
+        __builtin_amdgcn_sched_barrier(0);
+        add();
+      }
     }
   }
 
+  const int64_t to = p.parts ? ((int64_t)c0 * p.parts + blockIdx.y) * p.each + (RANK_LANES ? 0 : (int64_t)p.of[0].F * p.r)
+                             : (int64_t)a * of.F * p.r;
   // lane l: column (rank) l % 16 of the tile, rows 4 (l / 16) + 0 .. 3
 #pragma unroll
   for (int i = 0; i < NT; ++i)
@@ -1057,7 +1070,7 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int64
       for (int e = 0; e < 4; ++e) {
         const int f = f0 + 32 * wave + 16 * i + (RANK_LANES ? 4 * q + e : fr), k = 16 * j + (RANK_LANES ? fr : 4 * q + e);
         if (f >= of.F || k >= p.r) continue;
-        const int64_t at = blockIdx.z * numel + (RANK_LANES ? ((int64_t)a * of.F + f) * p.r + k : ((int64_t)a * p.r + k) * of.F + f);
+        const int64_t at = to + (RANK_LANES ? (int64_t)f * p.r + k : (int64_t)k * of.F + f);
         if (TO == T_FP32)
           static_cast<float*>(of.out)[at] = acc[i][j][e];
         else
@@ -1070,34 +1083,40 @@ __global__ void __launch_bounds__(256) k_sums(const SumArgs p) {
   __shared__ __attribute__((aligned(16))) SumLds<TY, RT> lds;
   const int b = blockIdx.x;
   if (b < p.blocks0)
-    sum_block<TY, TO, RT, true>(p, p.of[0], p.numel[0], b, lds);
+    sum_block<TY, TO, RT, true>(p, p.of[0], b, lds);
   else
-    sum_block<TY, TO, RT, false>(p, p.of[1], p.numel[1], b - p.blocks0, lds);
+    sum_block<TY, TO, RT, false>(p, p.of[1], b - p.blocks0, lds);
 }
 
-// out = the parts added in order, of both gradients; numbers of elements multiples of 4.
+// An adapter's gradients: its parts added in order.  d and n are multiples of 8.
 struct PartsArgs {
-  const float* in[2];
-  void* out[2];
-  int64_t numel[2];
+  const float* in;
+  void *dA, *dB;
+  Lists lists;
+  int chunks, parts, na;  // na = d r
+  int64_t each;
 };
 template <int TO>
-__global__ void __launch_bounds__(256) k_parts(const PartsArgs p, int parts) {
-  const int64_t all = p.numel[0] + p.numel[1];
-  for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; at < all; at += (int64_t)gridDim.x * 1024) {
-    const int b = at >= p.numel[0];
-    const int64_t i = at - (b ? p.numel[0] : 0);
-    const float* in = p.in[b] + i;
-    float4 s = *reinterpret_cast<const float4*>(in);
-    for (int z = 1; z < parts; ++z) {
-      const float4 x = *reinterpret_cast<const float4*>(in + z * p.numel[b]);
+__global__ void __launch_bounds__(256) k_parts(const PartsArgs p) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int a = blockIdx.y;
+  if (i >= p.each) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < p.chunks; ++c) {
+    const int32_t* t = p.lists.tp + c * (p.lists.L + 2) + a;
+    const int z1 = t[1];
+#pragma unroll 4
+    for (int z = t[0]; z < z1; ++z) {
+      const float4 x = *reinterpret_cast<const float4*>(p.in + ((int64_t)c * p.parts + z) * p.each + i);
       s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
     }
-    if (TO == T_FP32)
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out[b]) + i) = s;
-    else
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out[b]) + i) = make_uint2(pack2<TO>(s.x, s.y), pack2<TO>(s.z, s.w));
   }
+  const int64_t at = i < p.na ? (int64_t)a * p.na + i : a * (p.each - p.na) + i - p.na;
+  void* out = i < p.na ? p.dA : p.dB;
+  if (TO == T_FP32)
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = s;
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack2<TO>(s.x, s.y), pack2<TO>(s.z, s.w));
 }
 
 // Up to here a block for each token of a tile of 16, without lists (in decode nearly every request
@@ -1134,11 +1153,19 @@ int down_splits(int64_t M, int64_t n, int64_t r) {
   return (int)(s > 8 ? 8 : s < 1 ? 1 : s);
 }
 
-// Blocks that share an adapter's rows in k_sums.
-int sum_shares(int64_t M, int64_t L, int64_t d, int64_t n) {
-  const int64_t blocks = L * ((d + 127) / 128 + (n + 127) / 128) * list_chunks(M, d, n);
-  const int64_t z = blocks > 0 && blocks < 512 ? 512 / blocks : 1, most = (M / L + 127) / 128;  // two to a compute unit
-  return (int)(z > most ? (most < 1 ? 1 : most) : z);
+// Rows of a part in k_sums (a multiple of 64), 0: an adapter's rows in one go.  Where there are fewer
+// blocks than two to a compute unit, the rows are cut so that about three to a unit have work.
+int64_t part_rows(int64_t M, int64_t L, int64_t d, int64_t n) {
+  const int64_t blocks = (d + 127) / 128 + (n + 127) / 128;
+  if (L * blocks >= 512 || M < 1) return 0;
+  const int64_t parts = (768 + blocks - 1) / blocks;
+  const int64_t rows = ((M + parts - 1) / parts + 63) / 64 * 64;
+  return rows < 128 ? 128 : rows;
+}
+// Parts of a chunk at most.
+int64_t most_parts(int64_t M, int64_t L, int64_t d, int64_t n) {
+  const int64_t rows = part_rows(M, L, d, n), c = list_chunk(M, d, n);
+  return rows ? c / rows + (L < c ? L : c) : 0;
 }
 
 template <int TY>
@@ -1223,30 +1250,26 @@ void sums_rt(const SumArgs& a, dim3 grid, hipStream_t st) {
 }
 
 template <int TY>
-hipError_t sums(SumArgs a, int shares, int out_dtype, float* ws, hipStream_t st) {
-  a.shares = shares;
-  const int parts = shares * (int)((a.M + a.lists.chunk - 1) / a.lists.chunk > 1 ? (a.M + a.lists.chunk - 1) / a.lists.chunk : 1);
-  PartsArgs q{};
-  for (int i = 0; i < 2; ++i) {
-    a.numel[i] = q.numel[i] = (int64_t)a.L * a.of[i].F * a.r;
-    q.out[i] = a.of[i].out;
-    if (parts > 1) a.of[i].out = ws + (i ? parts * a.numel[0] : 0);
-    q.in[i] = static_cast<const float*>(a.of[i].out);
-  }
+hipError_t sums(SumArgs a, const AdapterArgs& p, float* ws, hipStream_t st) {
+  const int chunks = (int)list_chunks(p.M, p.d, p.n);
+  a.parts = (int)most_parts(p.M, p.L, p.d, p.n);
+  a.each = p.r * (p.d + p.n);
   a.blocks0 = (a.of[0].F + 127) / 128;
-  const dim3 grid((unsigned)(a.blocks0 + (a.of[1].F + 127) / 128), (unsigned)a.L, (unsigned)parts);
-  if (parts > 1 || out_dtype == T_FP32)
+  const unsigned blocks = (unsigned)(a.blocks0 + (a.of[1].F + 127) / 128);
+  if (a.parts) a.of[0].out = a.of[1].out = ws;
+  const dim3 grid(blocks, (unsigned)(a.parts ? a.parts : p.L), (unsigned)(a.parts ? chunks : 1));
+  if (a.parts || p.out_dtype == T_FP32)
     sums_rt<TY, T_FP32>(a, grid, st);
   else
     sums_rt<TY, TY>(a, grid, st);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || parts == 1) return e;
-  const int64_t want = ((q.numel[0] + q.numel[1]) / 4 + 255) / 256;
-  const unsigned blocks = (unsigned)(want < 2048 ? want : 2048);
-  if (out_dtype == T_FP32)
-    k_parts<T_FP32><<<blocks, 256, 0, st>>>(q, parts);
+  if (e != hipSuccess || !a.parts) return e;
+  const PartsArgs q{ws, p.dA, p.dB, a.lists, chunks, a.parts, (int)(p.d * p.r), a.each};
+  const dim3 each((unsigned)((a.each / 4 + 255) / 256), (unsigned)p.L);
+  if (p.out_dtype == T_FP32)
+    k_parts<T_FP32><<<each, 256, 0, st>>>(q);
   else
-    k_parts<TY><<<blocks, 256, 0, st>>>(q, parts);
+    k_parts<TY><<<each, 256, 0, st>>>(q);
   return hipGetLastError();
 }
 
@@ -1269,7 +1292,7 @@ Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
     place = at;
     at += up256(bytes);
   };
-  if (grads || M > kTokenRows) take(w.lists, 4 * M + 12 * list_chunks(M, d, n) * (L + 2));
+  if (grads || M > kTokenRows) take(w.lists, 4 * M + 16 * list_chunks(M, d, n) * (L + 2));
   if (!grads) {
     take(w.pad, up_pads(M, r) ? 2 * L * d * ((r + 7) / 8 * 8) : 0);
   } else {
@@ -1278,8 +1301,7 @@ Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
     take(w.pdh, 6 * M * rp);
     take(w.at, 2 * L * r * d);
     take(w.bt, 2 * L * n * rp);
-    const int64_t parts = sum_shares(M, L, d, n) * list_chunks(M, d, n);
-    take(w.parts, parts > 1 ? 4 * parts * L * r * (d + n) : 0);
+    take(w.parts, 4 * most_parts(M, L, d, n) * list_chunks(M, d, n) * r * (d + n));
   }
   w.bytes = at;
   return w;
@@ -1292,6 +1314,9 @@ Lists lists_of(const AdapterArgs& p, uint8_t* at) {
   l.starts = l.order + p.M;
   l.t32 = l.starts + tables;
   l.t64 = l.t32 + tables;
+  l.tp = l.t64 + tables;
+  const int64_t part = part_rows(p.M, p.L, p.d, p.n);
+  l.part = part ? (int)part : 64;
   l.M = p.M;
   l.chunk = list_chunk(p.M, p.d, p.n);
   l.L = (int)p.L;
@@ -1429,7 +1454,7 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   q.rp = rp;
   q.of[0] = Sum{dY, ph, p.dA, d};
   q.of[1] = Sum{X, pdh, p.dB, n};
-  return sums<TY>(q, sum_shares(p.M, L, d, n), p.out_dtype, reinterpret_cast<float*>(ws + w.parts), st);
+  return sums<TY>(q, p, reinterpret_cast<float*>(ws + w.parts), st);
 }
 
 }  // namespace
@@ -1438,7 +1463,7 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
 bool adapters_fit(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r) {
   const int64_t most = int64_t(1) << 32, widest = d > n ? d : n, chunks = list_chunks(M, d, n);
   const int64_t turns = ((d + 31) / 32 + (n + 31) / 32) * ((round16(r) + 31) / 32);
-  if (chunks * sum_shares(M, L, d, n) > 65535 || (turns * L + 4) * 256 + (L + 1) * chunks * 1024 >= most || M * (round16(r) / 4) + 256 >= most) return false;
+  if (chunks > 65535 || most_parts(M, L, d, n) > 65535 || (turns * L + 4) * 256 + (L + 1) * chunks * 1024 >= most || M * (round16(r) / 4) + 256 >= most) return false;
   if (M <= kTokenRows) {
     const int64_t tokens = (M + 15) / 16 * 16;
     return tokens * ((widest + 127) / 128) * 256 < most && tokens * 8 * 8 * 64 * kDownWaves < most;

@@ -9,7 +9,7 @@ from integer_rank_adaptation_amd import binding as B
 from integer_rank_adaptation_amd import ops
 from oracle import adapters as ref
 
-P = [0x100000 * (i + 1) for i in range(16)]  # 16-byte aligned, apart, never dereferenced
+P = [0x1000000 * (i + 1) for i in range(16)]  # 16-byte aligned, apart, never dereferenced
 OK, EINVAL, ESHAPE, EALIGN, EWS = (B.INTLORA_OK, B.INTLORA_EINVAL, B.INTLORA_ESHAPE, B.INTLORA_EALIGN,
                                    B.INTLORA_EWORKSPACE)
 
@@ -21,14 +21,14 @@ def lib():
 
 def _fwd(lib, **kw):
     a = dict(M=8, L=2, d=16, n=1024, r=128, dtype=0, base=P[0], X=P[1], index=P[2], A=P[3], B=P[4], scale=P[5], Y=P[6],
-             ws=P[7], size=1 << 20)
+             ws=P[7], size=1 << 22)
     a.update(kw)
     return lib.intlora_adapters_fwd(*a.values(), None)
 
 
 def _grad(lib, **kw):
     a = dict(M=8, L=2, d=16, n=1024, r=128, dtype=0, out=2, dY=P[8], X=P[1], index=P[2], A=P[3], B=P[4], scale=P[5],
-             base=P[0], dX=P[6], dA=P[9], dB=P[10], ws=P[7], size=1 << 20)
+             base=P[0], dX=P[6], dA=P[9], dB=P[10], ws=P[7], size=1 << 22)
     a.update(kw)
     return lib.intlora_adapters_grad(*a.values(), None)
 
