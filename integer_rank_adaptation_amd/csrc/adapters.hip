@@ -313,13 +313,17 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_down_few(const DownArgs p) 
   // (lane q: 16 bytes each at 8 q and 32 + 8 q of a run; four runs in flight)
   constexpr int U = 8;
   const int first = 64 * (wave + kDownWaves * split), step = 64 * kDownWaves * of.splits;
+  // The blocks of an XCD (each eighth one) start at different runs: rows are a power of two of bytes
+  // apart as a rule, and blocks at the same columns would all be at the same few channels.
+  const int runs = (of.n + step - 1) / step, turn = (int)((blockIdx.x >> 3) % runs);
   v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int k = first; k < of.n; k += U / 2 * step) {
+  for (int run = 0; run < runs; run += U / 2) {
     v4i x[U], w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = k + u / 2 * step + 32 * (u & 1) + 8 * q;
-      const uint32_t o = c < of.n ? 2u * c : kOOB;
+      const int i = run + u / 2, k = first + (i + turn < runs ? i + turn : i + turn - runs) * step;
+      const int c = k + 32 * (u & 1) + 8 * q;
+      const uint32_t o = i < runs && c < of.n ? 2u * c : kOOB;
       w[u] = load16(rw, (ow | o) & kOOB ? kOOB : ow + o);
       x[u] = load16(rx, (ox | o) & kOOB ? kOOB : ox + o);
     }
@@ -362,8 +366,7 @@ __global__ void __launch_bounds__(256) k_down(const DownArgs p) {
   const int64_t first = c * p.lists.chunk;  // the chunk's first row, and first place
   const int row = (lane & 31) < pl.rows ? p.lists.order[first + pl.at + (lane & 31)] : -1;
   const int ld = of.n * 2, stages = (ld + 255) / 256, mine = stages > split ? (stages - split + of.splits - 1) / of.splits : 0;
-  // The blocks of an XCD (each eighth one) start at different stages: rows are a power of two of bytes
-  // apart as a rule, and blocks at the same columns would all be at the same few channels.
+  // (blocks of an XCD start at different stages, as in k_down_few)
   const int turn = mine > 0 ? (int)((blockIdx.x >> 3) % mine) : 0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
   // Lane l of a load: row l / 16 of its four, whose 16-byte chunk k lies at k ^ row % 16.
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(256) k_up_few(const UpArgs p) {
   const int id = adapter_of(p.index, t, p.M, p.L), a = leader(id, slot);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = (int)block * p.chunk + 32 * wave, c1 = (int)block * p.chunk + p.chunk;
-  // Steps of 128 columns; the blocks of an XCD start at different ones (as in k_down).
+  // Steps of 128 columns; the blocks of an XCD start at different ones (as in k_down_few).
   const int steps = p.chunk / 128, turn = (int)((blockIdx.x >> 3) % steps);
   auto column = [&](int step) { return first + 128 * (step + turn < steps ? step + turn : step + turn - steps); };
   if (a >= 0) {
@@ -1143,12 +1146,15 @@ int64_t most_tiles(int64_t M, int64_t L, int64_t d, int64_t n, int64_t size) {
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// Splits of k_down over n columns: where its blocks are fewer than the compute units, down to two
-// runs of 64 columns for each wave.
-int down_splits(int64_t M, int64_t n, int64_t r) {
-  const int64_t blocks = M <= kTokenRows ? M * ((r + 15) / 16) : (M + 31) / 32;
-  const int64_t most = M <= kTokenRows ? n / (2 * 64 * kDownWaves) : n / 1024;
-  int64_t s = blocks > 0 ? 256 / blocks : 1;
+// Splits of the columns in k_down (and k_down_few): where its blocks are fewer than the compute units,
+// with at least two runs of 64 columns for each wave, or 1024 columns for a block.  The forward's tiles
+// go for two blocks to a unit, which evens out a last tile more than units (8192 x 4096, rank
+// 64, 262 tiles: 31.7 us, in two splits 27.7); in the gradients one split saves k_split's launch.
+int down_splits(int64_t M, int64_t n, int64_t r, bool grads) {
+  const bool few = M <= kTokenRows;
+  const int64_t blocks = few ? M * ((r + 15) / 16) : (M + 31) / 32;
+  const int64_t most = few ? n / (2 * 64 * kDownWaves) : n / 1024;
+  int64_t s = blocks > 0 ? (few || grads ? 256 : 512) / blocks : 1;
   s = s > most ? most : s;
   return (int)(s > 8 ? 8 : s < 1 ? 1 : s);
 }
@@ -1287,7 +1293,7 @@ Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   Ws w{};
   const int64_t rp = round16(r);
   if (!grads && in_one(M, d, n, r)) return w;
-  int64_t at = up256(4 * M * rp * down_splits(M, n, r));
+  int64_t at = up256(4 * M * rp * down_splits(M, n, r, grads));
   auto take = [&](int64_t& place, int64_t bytes) {
     place = at;
     at += up256(bytes);
@@ -1296,7 +1302,7 @@ Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   if (!grads) {
     take(w.pad, up_pads(M, r) ? 2 * L * d * ((r + 7) / 8 * 8) : 0);
   } else {
-    take(w.dh, 4 * M * rp * down_splits(M, d, r));
+    take(w.dh, 4 * M * rp * down_splits(M, d, r, grads));
     take(w.ph, 6 * M * rp);
     take(w.pdh, 6 * M * rp);
     take(w.at, 2 * L * r * d);
@@ -1372,7 +1378,7 @@ UpArgs up_args(const AdapterArgs& p) {
 template <int TY>
 hipError_t fwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   float* h = reinterpret_cast<float*>(ws);
-  const int s = down_splits(p.M, p.n, p.r);
+  const int s = down_splits(p.M, p.n, p.r, false);
   const Down of{static_cast<const uint8_t*>(p.X), static_cast<const uint8_t*>(p.B), h, (int)p.n, s, nullptr};
   UpArgs y = up_args(p);
   y.H = h;
@@ -1401,7 +1407,7 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   float *h = reinterpret_cast<float*>(ws), *dh = reinterpret_cast<float*>(ws + w.dh);
   uint16_t *at = reinterpret_cast<uint16_t*>(ws + w.at), *bt = reinterpret_cast<uint16_t*>(ws + w.bt);
   const uint8_t *X = static_cast<const uint8_t*>(p.X), *dY = static_cast<const uint8_t*>(p.dY);
-  const int sh = down_splits(p.M, n, r), sd = down_splits(p.M, d, r);
+  const int sh = down_splits(p.M, n, r, true), sd = down_splits(p.M, d, r, true);
   uint16_t *ph = reinterpret_cast<uint16_t*>(ws + w.ph), *pdh = reinterpret_cast<uint16_t*>(ws + w.pdh);
   const Lists lists = lists_of(p, ws + w.lists);
   ListArgs l{};
