@@ -106,7 +106,7 @@ __device__ __forceinline__ void turn_tile(const ListArgs& p, int unit) {
 }
 
 // A block for each group: it counts all rows by adapter in LDS, which gives its first place and
-// tiles, and then lists its own.  Bound by latency: 8192 rows of 16 adapters LISTS_US.
+// tiles, and then lists its own.  Bound by latency: 8192 rows of 16 adapters 7.2 us.
 constexpr int kMaxGroups = 4096 + 1;
 
 __global__ void __launch_bounds__(1024) k_lists(const ListArgs p) {
@@ -283,10 +283,10 @@ struct DownArgs {
 };
 
 // For few tokens: a block for each token of a tile of 16 and each 16 ranks, where the token is the
-// first of its adapter in the tile: it takes all of that adapter's tokens there.  Its eight waves take runs
-// of 64 columns in turn, and their sums meet in LDS, where they are added in order.  Lane l holds
+// first of its adapter in the tile: it takes all of that adapter's tokens there.  Its eight waves take
+// runs of 64 columns in turn, and their sums meet in LDS, where they are added in order.  Lane l holds
 // token l % 16 and ranks 4 (l / 16) + 0 .. 3.  Rows of other adapters read as zeros and are not
-// written.
+// written.  64 adapters of rank 64, n = 4096, a token each 9.3 us (3.6 TB/s; four waves a block 11.5).
 constexpr int kDownWaves = 8;
 
 template <int TY>
@@ -342,8 +342,8 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_down_few(const DownArgs p) 
 // Stages of 256 bytes of the rows go through a ring of three LDS buffers filled by direct loads of
 // 4 rows x 256 bytes (fragments straight from memory, 16 pieces of 64 bytes a load, took twice as
 // long); each of the four waves takes a quarter of a stage, and their sums meet in LDS, where they are
-// added in order.
-// MEASURED_DOWN
+// added in order.  Bound by what a compute unit takes from L2, the rows and, twice as much, the factor:
+// 8192 x 4096, rank 64 27.8 us (67 MB of rows, 2.4 TB/s).
 template <int RT_>
 struct DownTile {
   static constexpr int RT = RT_, ROWS = 32 + 16 * RT, RING = 3, STAGE = ROWS * 256;
@@ -554,7 +554,7 @@ struct Low {
 //
 // For few tokens: a block for each token of a tile of 16 (as k_down_few), its four waves 32 columns
 // in turn.  Bound by the factors' bytes: the next columns' weights are loaded while these are at
-// work, the first ones before h is there.
+// work, the first ones before h is there (64 adapters of 14336 x 64, a token each 23.4 us, 5.0 TB/s).
 template <int TY, int KT, bool WIDE>
 __global__ void __launch_bounds__(256) k_up_few(const UpArgs p) {
   const int lane = threadIdx.x & 63, fr = lane & 15, q = lane >> 4;
@@ -626,16 +626,15 @@ __global__ void __launch_bounds__(256) k_up_few(const UpArgs p) {
   }
 }
 
-// Both steps in one launch, for few tokens and small factors: a block for each token of a tile of 16 (as
-// above) and 256 columns forms h itself, its eight waves as in k_down_few, one rank tile after the
-// other, and then 32 columns each.  Every block of a token reads all of B_a, from L2 but for the
-// first, so this pays as long as that takes less than a launch.
-// MEASURED_TOKEN
+// Both steps in one launch, for few tokens and up to 16 ranks: a block for each token of a tile of 16 (as
+// above) and 256 columns forms h itself, as k_down_few does, and then 32 columns each wave.  Every
+// block of a token reads all of B_a, from L2 but for the first: 35 GB/s of a compute unit, so this
+// pays as long as that takes less than a launch.
 constexpr int kTokenCols = 256;
 
-template <int TY, int KT, bool WIDE>
+template <int TY, bool WIDE>
 __global__ void __launch_bounds__(64 * kDownWaves) k_token(const Down of, const UpArgs p) {
-  __shared__ __attribute__((aligned(16))) float sums[2 * KT][kDownWaves][256];
+  __shared__ __attribute__((aligned(16))) float sums[kDownWaves][256];
   const int lane = threadIdx.x & 63, fr = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t tokens = (uint32_t)((p.M + 15) / 16) * p.slots;
@@ -647,65 +646,53 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_token(const Down of, const 
   const bool mine = id == a;
   if (a >= 0) {
     const uint16_t* W = reinterpret_cast<const uint16_t*>(p.W) + (int64_t)a * p.d * p.ld;
-    v4i w[2][KT];
+    v4i w[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int row = n0 + 8 * (fr >> 2) + 4 * u + (fr & 3);
-#pragma unroll
-      for (int c = 0; c < KT; ++c) w[u][c] = row8<WIDE>(W + (int64_t)row * p.ld, row < p.d ? 32 * c + 8 * q : p.r, p.r);
+      w[u] = row8<WIDE>(W + (int64_t)row * p.ld, row < p.d ? 8 * q : p.r, p.r);
     }
     u4i b = u4i{0, 0, 0, 0};
     if (p.base && mine && col < p.d) b = *reinterpret_cast<const u4i*>(p.base + 2 * (t * p.d + col));
     const float s = p.scale[a];
-    const int rows = p.M - t0 < 16 ? (int)(p.M - t0) : 16, tiles = p.rp / 16;
+    const int rows = p.M - t0 < 16 ? (int)(p.M - t0) : 16;
     const uint32_t ld = (uint32_t)of.n * 2;
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(of.X + t0 * ld, (int64_t)rows * ld);
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(of.W + (int64_t)a * p.ranks * ld, (int64_t)p.ranks * ld);
-    const uint32_t ox = mine ? fr * ld : kOOB;
+    const uint32_t ox = mine ? fr * ld : kOOB, ow = fr < p.ranks ? fr * ld : kOOB;
     constexpr int U = 8, step = 64 * kDownWaves;
-    for (int j = 0; j < tiles; ++j) {
-      const uint32_t ow = 16 * j + fr < p.ranks ? (16 * j + fr) * ld : kOOB;
-      v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
-      for (int k = 64 * wave; k < of.n; k += U / 2 * step) {
-        v4i x[U], v[U];
+    v4f part = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int k = 64 * wave; k < of.n; k += U / 2 * step) {
+      v4i x[U], v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int c = k + u / 2 * step + 32 * (u & 1) + 8 * q;
-          const uint32_t o = c < of.n ? 2u * c : kOOB;
-          v[u] = load16(rw, (ow | o) & kOOB ? kOOB : ow + o);
-          x[u] = load16(rx, (ox | o) & kOOB ? kOOB : ox + o);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) acc = mfma<TY>(v[u], x[u], acc);
+      for (int u = 0; u < U; ++u) {
+        const int c = k + u / 2 * step + 32 * (u & 1) + 8 * q;
+        const uint32_t o = c < of.n ? 2u * c : kOOB;
+        v[u] = load16(rw, (ow | o) & kOOB ? kOOB : ow + o);
+        x[u] = load16(rx, (ox | o) & kOOB ? kOOB : ox + o);
       }
-      *reinterpret_cast<v4f*>(&sums[j][wave][4 * lane]) = acc;
-    }
-    __syncthreads();
-    if (wave < tiles) {
-      v4f acc = *reinterpret_cast<const v4f*>(&sums[wave][0][4 * lane]);
 #pragma unroll
-      for (int z = 1; z < kDownWaves; ++z) acc += *reinterpret_cast<const v4f*>(&sums[wave][z][4 * lane]);
-      *reinterpret_cast<v4f*>(&sums[wave][0][4 * lane]) = acc;
+      for (int u = 0; u < U; ++u) part = mfma<TY>(v[u], x[u], part);
     }
+    *reinterpret_cast<v4f*>(&sums[wave][4 * lane]) = part;
     __syncthreads();
-    Low<TY, KT> h;
-    h.fill(p, mine, s, [&](int k, float (&v)[8]) {  // lane l of a tile: token l % 16, ranks 4 (l / 16) ..
-      const float* o = &sums[k >> 4][0][4 * (fr + 16 * ((k & 15) >> 2))];
+    Low<TY, 1> h;
+    h.fill(p, mine, s, [&](int k, float (&v)[8]) {  // lane l of a wave's part: token l % 16, ranks 4 (l / 16) ..
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] += o[e];
-        v[4 + e] += o[64 + e];
+      for (int z = 0; z < kDownWaves; ++z) {
+        const float* o = &sums[z][4 * (fr + 4 * k)];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] += o[e];
+          v[4 + e] += o[64 + e];
+        }
       }
     });
     u4i y;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < KT; ++c) {
-        acc = mfma<TY>(w[u][c], h.lo[c], acc);
-        acc = mfma<TY>(w[u][c], h.hi[c], acc);
-      }
+      v4f acc = mfma<TY>(w[u], h.lo[0], v4f{0.f, 0.f, 0.f, 0.f});
+      acc = mfma<TY>(w[u], h.hi[0], acc);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const f2 f = unpack2<TY>(b[2 * u + e]);
@@ -734,7 +721,9 @@ __device__ __forceinline__ int turned(int m, int chunks) {
 // lane ends up with columns 8 (l % 16) + 0 .. 7 of tokens 4 (l / 16) + 0 .. 3, so that rows are read and
 // written in runs of 256 bytes with no step through LDS.  The next columns' rows of the base are
 // loaded while these are at work.  Rows without an adapter (the last group) take the base's values.
-// MEASURED_UP
+// Bound by memory and by the last tiles: 8192 x 4096, rank 64 39 us (134 MB read and written, 3.4 TB/s;
+// one adapter, without partly filled tiles, 32).  Weights straight from memory to registers took 51,
+// sums turned to rows in LDS with one block to a unit 80.
 template <int TY, int KT>
 __global__ void __launch_bounds__(256) k_up(const UpArgs p) {
   constexpr int NL = 2 * KT, BUF = 4 * NL * 1024;  // direct loads of a wave; bytes of a buffer
@@ -934,11 +923,12 @@ struct SumArgs {
 };
 
 // sum over an adapter's tokens of P_t h_t^T s_a.  A block takes 128 columns of P, all ranks and all of
-// the adapter's rows, or one of the parts that they are cut into, T of them at a time, each wave 32 columns x 16 RT ranks; the next
-// ones are loaded meanwhile.  Both operands have the
-// contraction (tokens) in rows and leave LDS through the transposing reads.  h is three bf16 numbers;
-// fp16 rows of P become two (exact).
-// MEASURED_SUMS
+// the adapter's rows, or one of the parts that they are cut into, T of them at a time, each wave 32
+// columns x 16 RT ranks; the next ones are loaded meanwhile.  Both operands have the contraction
+// (tokens) in rows and leave LDS through the transposing reads.  h is three bf16 numbers; fp16 rows of P
+// become two (exact).  4099 rows of 5 adapters, 2560 and 640 columns in fp16, rank 20: 18.7 us, a chain of
+// LDS writes, barriers and products per 64 rows (h split here, 64 columns a block and rows cut by
+// range instead of by adapter: 43).
 template <int TY, int RT>
 struct SumLds {
   static constexpr int PP = TY == T_FP16 ? 2 : 1, T = RT == 8 ? 32 : 64;
@@ -1122,9 +1112,12 @@ __global__ void __launch_bounds__(256) k_parts(const PartsArgs p) {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack2<TO>(s.x, s.y), pack2<TO>(s.z, s.w));
 }
 
-// Up to here a block for each token of a tile of 16, without lists (in decode nearly every request
-// has an adapter of its own); more rows are listed by adapter first.
-constexpr int64_t kTokenRows = 1024;
+// Few tokens take a block for each token of a tile of 16, without lists; more are listed by adapter
+// first.  The host knows how many adapters there are, not how many the rows use (4096 x 4096, rank 16,
+// us with and without lists; 8 adapters in runs: 200 rows 16 and 20, 400 rows 16 and 34, 800 rows 17
+// and 59; 64 at random: 25 and 17, 25 and 27, 27 and 43; 512 at random: 51 and 18, 75 and 28, 100 and
+// 44, 2000 rows 93 and 90).
+bool few_rows(int64_t M, int64_t L) { return M <= 256 || (M <= 640 && M < 4 * L); }
 
 int token_slots(int64_t M) { return M < 16 ? (M < 1 ? 1 : (int)M) : 16; }
 
@@ -1150,8 +1143,8 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 // with at least two runs of 64 columns for each wave, or 1024 columns for a block.  The forward's tiles
 // go for two blocks to a unit, which evens out a last tile more than units (8192 x 4096, rank
 // 64, 262 tiles: 31.7 us, in two splits 27.7); in the gradients one split saves k_split's launch.
-int down_splits(int64_t M, int64_t n, int64_t r, bool grads) {
-  const bool few = M <= kTokenRows;
+int down_splits(int64_t M, int64_t L, int64_t n, int64_t r, bool grads) {
+  const bool few = few_rows(M, L);
   const int64_t blocks = few ? M * ((r + 15) / 16) : (M + 31) / 32;
   const int64_t most = few ? n / (2 * 64 * kDownWaves) : n / 1024;
   int64_t s = blocks > 0 ? (few || grads ? 256 : 512) / blocks : 1;
@@ -1177,7 +1170,7 @@ int64_t most_parts(int64_t M, int64_t L, int64_t d, int64_t n) {
 template <int TY>
 hipError_t down(DownArgs a, int problems, hipStream_t st) {
   const int rt = a.rp / 16, splits = a.of[0].splits > a.of[1].splits ? a.of[0].splits : a.of[1].splits;
-  if (a.M <= kTokenRows) {
+  if (few_rows(a.M, a.L)) {
     a.slots = token_slots(a.M);
     const dim3 grid((unsigned)((a.M + 15) / 16 * a.slots * rt * splits), (unsigned)problems);
     k_down_few<TY><<<grid, 64 * kDownWaves, 0, st>>>(a);
@@ -1210,18 +1203,18 @@ int64_t up_chunk(int64_t tiles, int64_t d, int64_t want) {
 }
 
 // Rows of the factors need to be multiples of 8 for many tokens: others are padded first.
-bool up_pads(int64_t M, int64_t r) { return M > kTokenRows && r % 8 != 0; }
+bool up_pads(int64_t M, int64_t L, int64_t r) { return !few_rows(M, L) && r % 8 != 0; }
 
 template <int TY>
 hipError_t up(UpArgs a, uint16_t* pad, hipStream_t st) {
-  if (a.M <= kTokenRows) {
+  if (few_rows(a.M, a.L)) {
     a.slots = token_slots(a.M);
     const int64_t chunk = up_chunk(a.M, a.d, 1024);
     a.chunk = (int)chunk;
     const dim3 grid((unsigned)((a.M + 15) / 16 * a.slots * ((a.d + chunk - 1) / chunk)));
     return a.r % 8 == 0 && a.ld % 8 == 0 ? up_few<TY, true>(a, grid, st) : up_few<TY, false>(a, grid, st);
   }
-  if (up_pads(a.M, a.r)) {
+  if (up_pads(a.M, a.L, a.r)) {
     const int ld = (a.r + 7) / 8 * 8;
     const int64_t units = (int64_t)a.L * a.d * (ld / 8), want = (units + 255) / 256;
     k_pad<<<(unsigned)(want < 8192 ? want : 8192), 256, 0, st>>>(reinterpret_cast<const uint16_t*>(a.W), pad, units, a.r, ld);
@@ -1279,9 +1272,11 @@ hipError_t sums(SumArgs a, const AdapterArgs& p, float* ws, hipStream_t st) {
   return hipGetLastError();
 }
 
-// One launch: B_a small, and no more blocks than compute units.
+// One launch: one rank tile, B_a small, and no more blocks than compute units (one token, 4096 columns,
+// rank 16, us of the kernels alone: n = 640 4.7, in two launches 6.6; 2560 6.7 and 7.1; 4096 7.7 and
+// 7.1, but a call 9.8 and 13.9 with its host side; rank 64 with n = 640 would be 9.1 and 7.5).
 bool in_one(int64_t M, int64_t d, int64_t n, int64_t r) {
-  return round16(r) * n <= 65536 && M * ((d + kTokenCols - 1) / kTokenCols) <= 256;
+  return r <= 16 && n <= 4096 && M * ((d + kTokenCols - 1) / kTokenCols) <= 256;
 }
 
 // The workspace: h, the lists, A padded, and for the gradients dh, both in pieces, A and B transposed,
@@ -1293,16 +1288,16 @@ Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   Ws w{};
   const int64_t rp = round16(r);
   if (!grads && in_one(M, d, n, r)) return w;
-  int64_t at = up256(4 * M * rp * down_splits(M, n, r, grads));
+  int64_t at = up256(4 * M * rp * down_splits(M, L, n, r, grads));
   auto take = [&](int64_t& place, int64_t bytes) {
     place = at;
     at += up256(bytes);
   };
-  if (grads || M > kTokenRows) take(w.lists, 4 * M + 16 * list_chunks(M, d, n) * (L + 2));
+  if (grads || !few_rows(M, L)) take(w.lists, 4 * M + 16 * list_chunks(M, d, n) * (L + 2));
   if (!grads) {
-    take(w.pad, up_pads(M, r) ? 2 * L * d * ((r + 7) / 8 * 8) : 0);
+    take(w.pad, up_pads(M, L, r) ? 2 * L * d * ((r + 7) / 8 * 8) : 0);
   } else {
-    take(w.dh, 4 * M * rp * down_splits(M, d, r, grads));
+    take(w.dh, 4 * M * rp * down_splits(M, L, d, r, grads));
     take(w.ph, 6 * M * rp);
     take(w.pdh, 6 * M * rp);
     take(w.at, 2 * L * r * d);
@@ -1341,14 +1336,10 @@ template <int TY>
 hipError_t token(const Down& of, UpArgs a, hipStream_t st) {
   a.slots = token_slots(a.M);
   const dim3 grid((unsigned)((a.M + 15) / 16 * a.slots * ((a.d + kTokenCols - 1) / kTokenCols)));
-  const int kt = (a.rp + 31) / 32, threads = 64 * kDownWaves;
-  const bool wide = a.r % 8 == 0;
-  if (kt == 1)
-    wide ? k_token<TY, 1, true><<<grid, threads, 0, st>>>(of, a) : k_token<TY, 1, false><<<grid, threads, 0, st>>>(of, a);
-  else if (kt == 2)
-    wide ? k_token<TY, 2, true><<<grid, threads, 0, st>>>(of, a) : k_token<TY, 2, false><<<grid, threads, 0, st>>>(of, a);
+  if (a.r % 8 == 0)
+    k_token<TY, true><<<grid, 64 * kDownWaves, 0, st>>>(of, a);
   else
-    wide ? k_token<TY, 4, true><<<grid, threads, 0, st>>>(of, a) : k_token<TY, 4, false><<<grid, threads, 0, st>>>(of, a);
+    k_token<TY, false><<<grid, 64 * kDownWaves, 0, st>>>(of, a);
   return hipGetLastError();
 }
 
@@ -1378,7 +1369,7 @@ UpArgs up_args(const AdapterArgs& p) {
 template <int TY>
 hipError_t fwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   float* h = reinterpret_cast<float*>(ws);
-  const int s = down_splits(p.M, p.n, p.r, false);
+  const int s = down_splits(p.M, p.L, p.n, p.r, false);
   const Down of{static_cast<const uint8_t*>(p.X), static_cast<const uint8_t*>(p.B), h, (int)p.n, s, nullptr};
   UpArgs y = up_args(p);
   y.H = h;
@@ -1391,7 +1382,7 @@ hipError_t fwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   DownArgs x = down_args(p);
   x.of[0] = of;
   hipError_t e;
-  if (p.M > kTokenRows) {
+  if (!few_rows(p.M, p.L)) {
     ListArgs l{};
     l.lists = x.lists = y.lists = lists_of(p, ws + w.lists);
     if ((e = make_lists(p, l, st)) != hipSuccess) return e;
@@ -1407,7 +1398,7 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   float *h = reinterpret_cast<float*>(ws), *dh = reinterpret_cast<float*>(ws + w.dh);
   uint16_t *at = reinterpret_cast<uint16_t*>(ws + w.at), *bt = reinterpret_cast<uint16_t*>(ws + w.bt);
   const uint8_t *X = static_cast<const uint8_t*>(p.X), *dY = static_cast<const uint8_t*>(p.dY);
-  const int sh = down_splits(p.M, n, r, true), sd = down_splits(p.M, d, r, true);
+  const int sh = down_splits(p.M, L, n, r, true), sd = down_splits(p.M, L, d, r, true);
   uint16_t *ph = reinterpret_cast<uint16_t*>(ws + w.ph), *pdh = reinterpret_cast<uint16_t*>(ws + w.pdh);
   const Lists lists = lists_of(p, ws + w.lists);
   ListArgs l{};
@@ -1420,7 +1411,7 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   hipError_t e = make_lists(p, l, st);  // (without a row too: the lists are then empty)
   if (e != hipSuccess) return e;
   if (p.M > 0) {
-    const bool few = p.M <= kTokenRows, split = few || sh > 1 || sd > 1;
+    const bool few = few_rows(p.M, p.L), split = few || sh > 1 || sd > 1;
     DownArgs x = down_args(p);
     x.lists = lists;
     x.scale = p.scale;
@@ -1470,7 +1461,7 @@ bool adapters_fit(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r) {
   const int64_t most = int64_t(1) << 32, widest = d > n ? d : n, chunks = list_chunks(M, d, n);
   const int64_t turns = ((d + 31) / 32 + (n + 31) / 32) * ((round16(r) + 31) / 32);
   if (chunks > 65535 || most_parts(M, L, d, n) > 65535 || (turns * L + 4) * 256 + (L + 1) * chunks * 1024 >= most || M * (round16(r) / 4) + 256 >= most) return false;
-  if (M <= kTokenRows) {
+  if (few_rows(M, L)) {
     const int64_t tokens = (M + 15) / 16 * 16;
     return tokens * ((widest + 127) / 128) * 256 < most && tokens * 8 * 8 * 64 * kDownWaves < most;
   }

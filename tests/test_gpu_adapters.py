@@ -76,14 +76,16 @@ def backward(ops, c, dtype=torch.float32, base=True):
     return g, (dx, dA, dB)
 
 
-@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 100, 1024, 1025, 1500])
-@pytest.mark.parametrize("x,r,d,n", [("bf16", 16, 72, 136), ("fp16", 20, 136, 72), ("bf16", 3, 64, 1096)])
-def test_rows(ops, M, x, r, d, n):
-    forward(ops, make(M, 5, d, n, r, x))
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 100, 256, 257, 640, 641, 1025, 1500])
+@pytest.mark.parametrize("x,r,d,n", [("bf16", 16, 72, 136), ("fp16", 20, 136, 72), ("bf16", 3, 64, 1096),
+                                     ("fp16", 16, 264, 4096), ("bf16", 13, 520, 4104), ("fp16", 128, 1000, 2048)])
+@pytest.mark.parametrize("L", [5, 200])
+def test_rows(ops, M, x, r, d, n, L):
+    forward(ops, make(M, L, d, n, r, x))
 
 
 @pytest.mark.parametrize("r", [1, 2, 7, 8, 15, 17, 24, 32, 33, 48, 63, 64, 65, 100, 127, 128])
-@pytest.mark.parametrize("x,M", [("bf16", 37), ("fp16", 37), ("bf16", 1100)])
+@pytest.mark.parametrize("x,M", [("bf16", 37), ("fp16", 37), ("bf16", 1100), ("fp16", 300)])
 def test_ranks(ops, r, x, M):
     forward(ops, make(M, 3, 104, 200, r, x, "runs"))
 
@@ -160,7 +162,8 @@ def test_wide_range(ops, x, big):
     (33, 2, 136, 72, 17, "bf16", "one"), (300, 7, 72, 200, 20, "fp16", "random"), (700, 2, 264, 64, 64, "bf16", "runs"),
     (700, 2, 64, 264, 33, "fp16", "runs"), (1500, 3, 136, 72, 128, "bf16", "random"),
     (1500, 40, 72, 136, 100, "fp16", "random"), (2100, 5, 640, 72, 20, "fp16", "runs"),
-    (1100, 3, 72, 1096, 7, "bf16", "none"),
+    (1100, 3, 72, 1096, 7, "bf16", "none"), (256, 2, 64, 2056, 16, "bf16", "runs"), (257, 2, 2056, 64, 16, "bf16", "runs"),
+    (600, 200, 64, 72, 8, "fp16", "random"), (2000, 300, 264, 136, 9, "bf16", "runs"),
 ])
 def test_gradients(ops, M, L, d, n, r, x, kind):
     c = make(M, L, d, n, r, x, kind)
