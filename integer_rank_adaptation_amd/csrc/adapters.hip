@@ -286,7 +286,7 @@ struct DownArgs {
 // first of its adapter in the tile: it takes all of that adapter's tokens there.  Its eight waves take
 // runs of 64 columns in turn, and their sums meet in LDS, where they are added in order.  Lane l holds
 // token l % 16 and ranks 4 (l / 16) + 0 .. 3.  Rows of other adapters read as zeros and are not
-// written.  64 adapters of rank 64, n = 4096, a token each 9.3 us (3.6 TB/s; four waves a block 11.5).
+// written.  64 adapters of rank 64, n = 4096, a token each 9.0 us (3.7 TB/s; four waves a block 11.5).
 constexpr int kDownWaves = 8;
 
 template <int TY>
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_down_few(const DownArgs p) 
 // 4 rows x 256 bytes (fragments straight from memory, 16 pieces of 64 bytes a load, took twice as
 // long); each of the four waves takes a quarter of a stage, and their sums meet in LDS, where they are
 // added in order.  Bound by what a compute unit takes from L2, the rows and, twice as much, the factor:
-// 8192 x 4096, rank 64 27.8 us (67 MB of rows, 2.4 TB/s).
+// 8192 x 4096, rank 64 26.9 us (67 MB of rows, 2.5 TB/s).
 template <int RT_>
 struct DownTile {
   static constexpr int RT = RT_, ROWS = 32 + 16 * RT, RING = 3, STAGE = ROWS * 256;
@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(256) k_down(const DownArgs p) {
   const int a = pl.group;
   const int64_t first = c * p.lists.chunk;  // the chunk's first row, and first place
   const int row = (lane & 31) < pl.rows ? p.lists.order[first + pl.at + (lane & 31)] : -1;
-  const int ld = of.n * 2, stages = (ld + 255) / 256, mine = stages > split ? (stages - split + of.splits - 1) / of.splits : 0;
+  const int ld = of.n * 2, stages = (ld + 255) / 256;
+  const int mine = stages > split ? (stages - split + of.splits - 1) / of.splits : 0;
   // (blocks of an XCD start at different stages, as in k_down_few)
   const int turn = mine > 0 ? (int)((blockIdx.x >> 3) % mine) : 0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
@@ -629,7 +630,8 @@ __global__ void __launch_bounds__(256) k_up_few(const UpArgs p) {
 // Both steps in one launch, for few tokens and up to 16 ranks: a block for each token of a tile of 16 (as
 // above) and 256 columns forms h itself, as k_down_few does, and then 32 columns each wave.  Every
 // block of a token reads all of B_a, from L2 but for the first: 35 GB/s of a compute unit, so this
-// pays as long as that takes less than a launch.
+// pays as long as that takes less than a launch.  Bound by latency, the launch and two chains of loads:
+// 4096 x 4096, rank 16, 1 token 8 us.
 constexpr int kTokenCols = 256;
 
 template <int TY, bool WIDE>
@@ -721,7 +723,7 @@ __device__ __forceinline__ int turned(int m, int chunks) {
 // lane ends up with columns 8 (l % 16) + 0 .. 7 of tokens 4 (l / 16) + 0 .. 3, so that rows are read and
 // written in runs of 256 bytes with no step through LDS.  The next columns' rows of the base are
 // loaded while these are at work.  Rows without an adapter (the last group) take the base's values.
-// Bound by memory and by the last tiles: 8192 x 4096, rank 64 39 us (134 MB read and written, 3.4 TB/s;
+// Bound by memory and by the last tiles: 8192 x 4096, rank 64 38 us (134 MB read and written, 3.5 TB/s;
 // one adapter, without partly filled tiles, 32).  Weights straight from memory to registers took 51,
 // sums turned to rows in LDS with one block to a unit 80.
 template <int TY, int KT>
@@ -783,7 +785,8 @@ __global__ void __launch_bounds__(256) k_up(const UpArgs p) {
   auto issue = [&](int step) {
     const int col = step < steps ? column(step) : p.d;
     const int64_t left = (int64_t)(p.d - col) * p.ld * 2;
-    const rsrc_t rw = make_desc(col < p.d ? W + (int64_t)col * p.ld * 2 : W, col < p.d ? (int)(left < 65536 ? left : 65536) : 0);
+    const int bytes = col < p.d ? (int)(left < 65536 ? left : 65536) : 0;
+    const rsrc_t rw = make_desc(col < p.d ? W + (int64_t)col * p.ld * 2 : W, bytes);
 #pragma unroll
     for (int j = 0; j < NL; ++j) direct_load16(rw, lds0 + (step & 1) * BUF + 1024 * j, wo[j]);
   };
@@ -841,7 +844,8 @@ __global__ void __launch_bounds__(256) k_up(const UpArgs p) {
   wait_loads<0>();  // the weights loaded past the last step (zeros)
 }
 
-// Rows of `ld` numbers of rows of r, zeros behind them.
+// Rows of `ld` numbers of rows of r, zeros behind them, so that direct loads bring whole 16 bytes of
+// ranks that are no multiple of 8.  Bound by the launch for all but the largest sets of adapters.
 __global__ void __launch_bounds__(256) k_pad(const uint16_t* __restrict__ in, uint16_t* __restrict__ out, int64_t units,
                                              int r, int ld) {
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
@@ -926,7 +930,7 @@ struct SumArgs {
 // the adapter's rows, or one of the parts that they are cut into, T of them at a time, each wave 32
 // columns x 16 RT ranks; the next ones are loaded meanwhile.  Both operands have the contraction
 // (tokens) in rows and leave LDS through the transposing reads.  h is three bf16 numbers; fp16 rows of P
-// become two (exact).  4099 rows of 5 adapters, 2560 and 640 columns in fp16, rank 20: 18.7 us, a chain of
+// become two (exact).  4099 rows of 5 adapters, 2560 and 640 columns in fp16, rank 20: 18.0 us, a chain of
 // LDS writes, barriers and products per 64 rows (h split here, 64 columns a block and rows cut by
 // range instead of by adapter: 43).
 template <int TY, int RT>
@@ -1460,7 +1464,8 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
 bool adapters_fit(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r) {
   const int64_t most = int64_t(1) << 32, widest = d > n ? d : n, chunks = list_chunks(M, d, n);
   const int64_t turns = ((d + 31) / 32 + (n + 31) / 32) * ((round16(r) + 31) / 32);
-  if (chunks > 65535 || most_parts(M, L, d, n) > 65535 || (turns * L + 4) * 256 + (L + 1) * chunks * 1024 >= most || M * (round16(r) / 4) + 256 >= most) return false;
+  if (chunks > 65535 || most_parts(M, L, d, n) > 65535) return false;
+  if ((turns * L + 4) * 256 + (L + 1) * chunks * 1024 >= most || M * (round16(r) / 4) + 256 >= most) return false;
   if (few_rows(M, L)) {
     const int64_t tokens = (M + 15) / 16 * 16;
     return tokens * ((widest + 127) / 128) * 256 < most && tokens * 8 * 8 * 64 * kDownWaves < most;
