@@ -930,18 +930,25 @@ struct SumArgs {
 // the adapter's rows, or one of the parts that they are cut into, T of them at a time, each wave 32
 // columns x 16 RT ranks; the next ones are loaded meanwhile.  Both operands have the contraction
 // (tokens) in rows and leave LDS through the transposing reads.  h is three bf16 numbers; fp16 rows of P
-// become two (exact).  4099 rows of 5 adapters, 2560 and 640 columns in fp16, rank 20: 18.0 us, a chain of
-// LDS writes, barriers and products per 64 rows (h split here, 64 columns a block and rows cut by
-// range instead of by adapter: 43).
+// become two (exact).  4099 rows of 5 adapters, 2560 and 640 columns in fp16, rank 20: 14.8 us, a chain of
+// LDS writes, barriers and products per 64 rows, with three blocks to a unit (rows padded to other
+// banks instead of turned, and two blocks: 18; h split here, 64 columns a block and rows cut by range
+// instead of by adapter: 43).
 template <int TY, int RT>
 struct SumLds {
   static constexpr int PP = TY == T_FP16 ? 2 : 1, T = RT == 8 ? 32 : 64;
-  static constexpr int F = 128, PS = F + 8, HS = 16 * RT + 8;  // row strides (16-bit numbers)
-  static constexpr int kList = 1024;  // rows' numbers at a time
+  static constexpr int F = 128, PS = F, HS = 16 * RT;  // row strides (16-bit numbers)
+  static constexpr int kList = 512;                    // rows' numbers at a time
   uint16_t p[PP][T * PS];
   uint16_t h[3][T * HS];
   int list[kList];
 };
+
+// Where column c of a row is: the 32 bytes that half a wave reads of each of 8 rows are on different
+// banks, and so are 16 lanes' writes of 16 bytes.
+__device__ __forceinline__ int spread(int row, int c, int stride) {
+  return c ^ 16 * (row / (128 / stride) % (stride / 16));
+}
 
 template <int TY, int TO, int RT, bool RANK_LANES>
 __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int block, SumLds<TY, RT>& L) {
@@ -986,7 +993,7 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int b
   auto store = [&]() {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int at = ((tid >> 4) + 16 * i) * PS + (tid & 15) * 8;
+      const int row = (tid >> 4) + 16 * i, at = row * PS + spread(row, (tid & 15) * 8, PS);
       if (TY == T_FP16) {
         u4i t, b;
 #pragma unroll
@@ -1005,13 +1012,15 @@ __device__ __forceinline__ void sum_block(const SumArgs& p, const Sum& of, int b
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
       const int at = tid + 256 * i, k = at / (2 * RT * T), in = at % (2 * RT * T), row = in / (2 * RT), c = in % (2 * RT) * 8;
-      if (k < 3) *reinterpret_cast<u4i*>(&L.h[k][row * HS + c]) = lot.h[i];
+      if (k < 3) *reinterpret_cast<u4i*>(&L.h[k][row * HS + spread(row, c, HS)]) = lot.h[i];
     }
   };
-  auto frag = [&](const uint16_t* m, int stride, int row, int col) {  // rows row + 8 q + 0 .. 7 of column col + fr
-    const uint16_t* at = m + (row + 8 * q + (fr >> 2)) * stride + col + 4 * (fr & 3);
+  // Rows row + 4 q + 0 .. 3 and 16 further of column col + fr: in both operands the same ones.
+  auto frag = [&](const uint16_t* m, int stride, int row, int col) {
+    const int R = row + 4 * q + (fr >> 2);
+    const uint16_t* at = m + R * stride + spread(R, col + 4 * (fr & 3), stride);
     const int2 x = __builtin_bit_cast(int2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t)at));
-    const int2 y = __builtin_bit_cast(int2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t)(at + 4 * stride)));
+    const int2 y = __builtin_bit_cast(int2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t)(at + 16 * stride)));
     return v4i{x.x, x.y, y.x, y.y};
   };
   auto add = [&]() {
