@@ -930,7 +930,7 @@ struct SumArgs {
 // the adapter's rows, or one of the parts that they are cut into, T of them at a time, each wave 32
 // columns x 16 RT ranks; the next ones are loaded meanwhile.  Both operands have the contraction
 // (tokens) in rows and leave LDS through the transposing reads.  h is three bf16 numbers; fp16 rows of P
-// become two (exact).  4099 rows of 5 adapters, 2560 and 640 columns in fp16, rank 20: 14.8 us, a chain of
+// become two (exact).  4099 rows of 5 adapters, 2560 and 640 columns in fp16, rank 20: 14.1 us, a chain of
 // LDS writes, barriers and products per 64 rows, with three blocks to a unit (rows padded to other
 // banks instead of turned, and two blocks: 18; h split here, 64 columns a block and rows cut by range
 // instead of by adapter: 43).
