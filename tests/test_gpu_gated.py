@@ -330,3 +330,83 @@ def test_training_step(ops, T, E):
                            f64(cpu["s"]))
     for k, t in (("dx", "dh2"), ("dA", "dA"), ("dB", "dB")):
         check(out[t], w[k], tol[k], t)
+
+
+def test_outputs_past_31_bits(ops):
+    """Projections, gradients and restored codes of more than 2^31 bytes: the first, some middle and the
+    last rows, at the first and last columns."""
+    T, f, n = 41003, 13120, 32
+    assert 2 * T * 2 * f > 1 << 31
+    X, W = rand((T, n), DT["bf16"], 1).cuda(), rand((1, 2 * f, n), DT["bf16"], 2, 2 * n ** -0.5).cuda()
+    h, gu = ops.gated_linear(X, None, W, save=True)
+    dh = torch.randn(T, f, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").to(torch.bfloat16)
+    dgu, h2 = ops.gated_linear_dgu(dh, gu)
+    pair = ops.fp8_quant_act(gu)
+    dguq, _ = ops.gated_linear_dgu(dh, pair)
+    back = ops.fp8_dequant_act(*pair, torch.bfloat16)
+    rows = torch.tensor([0, 1, 127, 128, 20000, 20479, 20480, T - 4, T - 3, T - 2, T - 1], device="cuda")
+    for a in (0, f // 2 - 80, f - 128):
+        c = torch.cat((torch.arange(a, a + 128), torch.arange(f + a, f + a + 128))).cuda()
+        at = lambda t, k=c: t[rows][:, k]
+        want, wgu, eh, eg = ref.forward(f64(X[rows]), f64(W[:, c]), None, "silu")
+        check(at(h, c[:128]), want, eh, "h")
+        check(at(gu), wgu, eg, "gu")
+        w, wh, tol, th = ref.backward(f64(at(dh, c[:128])), f64(at(gu)), "silu")
+        check(at(dgu), w, tol, "dgu")
+        check(at(h2, c[:128]), wh, th, "h again")
+        assert (at(back).double() - at(gu).double()).abs().max() <= 2.0 ** -4 * at(gu).double().abs().max()
+        w, _, tol, _ = ref.backward(f64(at(dh, c[:128])), f64(at(back)), "silu")
+        check(at(dguq), w, tol, "dgu of codes")
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_weights_past_31_bits(ops, T):
+    f, n = (1 << 19) - 8, 1032
+    X = rand((T, n), DT["bf16"], 1).cuda()
+    W = torch.randn(1, 2 * f, n, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda",
+                    dtype=torch.bfloat16) * n ** -0.5
+    assert 2 * W.numel() > 1 << 31
+    h, gu = ops.gated_linear(X, None, W, act="gelu", save=True)
+    for a in (0, f // 2, f - 136):
+        c = torch.cat((torch.arange(a, a + 136), torch.arange(f + a, f + a + 136))).cuda()
+        want, wgu, eh, eg = ref.forward(f64(X), f64(W[:, c]), None, "gelu")
+        check(h[:, c[:136]], want, eh, "h")
+        check(gu[:, c], wgu, eg, "gu")
+
+
+def test_two_threads(ops):
+    """Calls of two threads at once, each on a stream of its own."""
+    import threading
+
+    X, W = rand((200, 264), DT["fp16"], 1).cuda(), rand((1, 272, 264), DT["fp16"], 2, 264 ** -0.5).cuda()
+    A, B = rand((3, 264, 20), DT["fp16"], 3, 0.1).cuda(), rand((3, 20, 136), DT["fp16"], 4, 0.1).cuda()
+    ids, s = torch.arange(200, dtype=torch.int32).cuda() % 4 - 1, torch.ones(3).cuda()
+
+    def work():
+        h, gu = ops.gated_linear(X, None, W, save=True)
+        y = ops.adapters_linear(X, h, ids, A, B, s)
+        return [y, ops.gated_linear_dgu(h, ops.fp8_quant_act(gu))[0],
+                *ops.adapters_linear_grad(y, h, ids, A, B, s, dtype=torch.float32)]
+
+    want = work()
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def run(k):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(20):
+                    got[k] = work()
+            st.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(want, g))
