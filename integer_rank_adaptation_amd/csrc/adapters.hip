@@ -342,8 +342,10 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_down_few(const DownArgs p) 
 // Stages of 256 bytes of the rows go through a ring of three LDS buffers filled by direct loads of
 // 4 rows x 256 bytes (fragments straight from memory, 16 pieces of 64 bytes a load, took twice as
 // long); each of the four waves takes a quarter of a stage, and their sums meet in LDS, where they are
-// added in order.  Bound by what a compute unit takes from L2, the rows and, twice as much, the factor:
-// 8192 x 4096, rank 64 26.9 us (67 MB of rows, 2.5 TB/s).
+// added in order.  Bound by the rows' way from memory (16384 x 4096, rank 16: 39 us, 3.5 TB/s) and, with
+// more ranks, the factor's from L2 (rank 64 47 us, 128 69); 8192 x 4096, rank 64 26.9 us.  Tiles of 64
+// rows read the factor half as often: 47 and 59 us for the same ranks at 16384 rows, 23.5 at 8192 in
+// three splits, of which k_up's joining takes two back; deeper rings 33.
 template <int RT_>
 struct DownTile {
   static constexpr int RT = RT_, ROWS = 32 + 16 * RT, RING = 3, STAGE = ROWS * 256;
