@@ -1128,11 +1128,19 @@ __global__ void __launch_bounds__(256) k_parts(const PartsArgs p) {
 }
 
 // Few tokens take a block for each token of a tile of 16, without lists; more are listed by adapter
-// first.  The host knows how many adapters there are, not how many the rows use (4096 x 4096, rank 16,
-// us with and without lists; 8 adapters in runs: 200 rows 16 and 20, 400 rows 16 and 34, 800 rows 17
-// and 59; 64 at random: 25 and 17, 25 and 27, 27 and 43; 512 at random: 51 and 18, 75 and 28, 100 and
-// 44, 2000 rows 93 and 90).
-bool few_rows(int64_t M, int64_t L) { return M <= 256 || (M <= 640 && M < 4 * L); }
+// first.  Without lists a row costs its adapter's bytes again, with them each adapter (of how many the
+// host knows only that they are at most L and M) a tile that is filled in part, and the lists 7 us.
+// us of the kernels without and with lists, 4096 x 4096: rank 16, one adapter, 128 rows 15.0 and 17.3;
+// 8 adapters, 200 rows 20 and 18; 64, 256 rows 21 and 27; 512, 256 rows 22 and 58.  Rank 64: one, 64
+// rows 19 and 22, 128 rows 32 and 22; 8, 64 rows 17 and 21, 128 rows 26 and 21; 64, 128 rows 28 and 33,
+// 256 rows 45 and 36; 512, 256 rows 54 and 92.  14336 x 4096, rank 64: one, 48 rows 29 and 21; 64, 96
+// rows 47 and 58, 256 rows 97 and 78.  640 x 640, 256 rows, one: rank 16 8.8 and 15.7, rank 64 19 and
+// 19.  The gradients need lists in any case (2560 x 640, rank 20, us of all kernels: 33 rows 29 and 31,
+// 100 rows 32.5 and 31, 200 rows 42 and 33; 4096 x 4096, rank 64, 200 rows 83 and 47).
+bool few_rows(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
+  if (grads) return M <= 64;
+  return M <= 640 && (d + n) * (M * r - (L < M ? L : M) * (2 * r + 48)) < 3 << 23;
+}
 
 int token_slots(int64_t M) { return M < 16 ? (M < 1 ? 1 : (int)M) : 16; }
 
@@ -1158,8 +1166,7 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 // with at least two runs of 64 columns for each wave, or 1024 columns for a block.  The forward's tiles
 // go for two blocks to a unit, which evens out a last tile more than units (8192 x 4096, rank
 // 64, 262 tiles: 31.7 us, in two splits 27.7); in the gradients one split saves k_split's launch.
-int down_splits(int64_t M, int64_t L, int64_t n, int64_t r, bool grads) {
-  const bool few = few_rows(M, L);
+int down_splits(int64_t M, int64_t n, int64_t r, bool few, bool grads) {
   const int64_t blocks = few ? M * ((r + 15) / 16) : (M + 31) / 32;
   const int64_t most = few ? n / (2 * 64 * kDownWaves) : n / 1024;
   int64_t s = blocks > 0 ? (few || grads ? 256 : 512) / blocks : 1;
@@ -1183,9 +1190,9 @@ int64_t most_parts(int64_t M, int64_t L, int64_t d, int64_t n) {
 }
 
 template <int TY>
-hipError_t down(DownArgs a, int problems, hipStream_t st) {
+hipError_t down(DownArgs a, int problems, bool few, hipStream_t st) {
   const int rt = a.rp / 16, splits = a.of[0].splits > a.of[1].splits ? a.of[0].splits : a.of[1].splits;
-  if (few_rows(a.M, a.L)) {
+  if (few) {
     a.slots = token_slots(a.M);
     const dim3 grid((unsigned)((a.M + 15) / 16 * a.slots * rt * splits), (unsigned)problems);
     k_down_few<TY><<<grid, 64 * kDownWaves, 0, st>>>(a);
@@ -1218,18 +1225,16 @@ int64_t up_chunk(int64_t tiles, int64_t d, int64_t want) {
 }
 
 // Rows of the factors need to be multiples of 8 for many tokens: others are padded first.
-bool up_pads(int64_t M, int64_t L, int64_t r) { return !few_rows(M, L) && r % 8 != 0; }
-
 template <int TY>
-hipError_t up(UpArgs a, uint16_t* pad, hipStream_t st) {
-  if (few_rows(a.M, a.L)) {
+hipError_t up(UpArgs a, uint16_t* pad, bool few, hipStream_t st) {
+  if (few) {
     a.slots = token_slots(a.M);
     const int64_t chunk = up_chunk(a.M, a.d, 1024);
     a.chunk = (int)chunk;
     const dim3 grid((unsigned)((a.M + 15) / 16 * a.slots * ((a.d + chunk - 1) / chunk)));
     return a.r % 8 == 0 && a.ld % 8 == 0 ? up_few<TY, true>(a, grid, st) : up_few<TY, false>(a, grid, st);
   }
-  if (up_pads(a.M, a.L, a.r)) {
+  if (a.ld % 8 != 0) {
     const int ld = (a.r + 7) / 8 * 8;
     const int64_t units = (int64_t)a.L * a.d * (ld / 8), want = (units + 255) / 256;
     k_pad<<<(unsigned)(want < 8192 ? want : 8192), 256, 0, st>>>(reinterpret_cast<const uint16_t*>(a.W), pad, units, a.r, ld);
@@ -1303,16 +1308,17 @@ Ws carve(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   Ws w{};
   const int64_t rp = round16(r);
   if (!grads && in_one(M, d, n, r)) return w;
-  int64_t at = up256(4 * M * rp * down_splits(M, L, n, r, grads));
+  const bool few = few_rows(M, L, d, n, r, grads);
+  int64_t at = up256(4 * M * rp * down_splits(M, n, r, few, grads));
   auto take = [&](int64_t& place, int64_t bytes) {
     place = at;
     at += up256(bytes);
   };
-  if (grads || !few_rows(M, L)) take(w.lists, 4 * M + 16 * list_chunks(M, d, n) * (L + 2));
+  if (grads || !few) take(w.lists, 4 * M + 16 * list_chunks(M, d, n) * (L + 2));
   if (!grads) {
-    take(w.pad, up_pads(M, L, r) ? 2 * L * d * ((r + 7) / 8 * 8) : 0);
+    take(w.pad, !few && r % 8 != 0 ? 2 * L * d * ((r + 7) / 8 * 8) : 0);
   } else {
-    take(w.dh, 4 * M * rp * down_splits(M, L, d, r, grads));
+    take(w.dh, 4 * M * rp * down_splits(M, d, r, few, grads));
     take(w.ph, 6 * M * rp);
     take(w.pdh, 6 * M * rp);
     take(w.at, 2 * L * r * d);
@@ -1384,7 +1390,8 @@ UpArgs up_args(const AdapterArgs& p) {
 template <int TY>
 hipError_t fwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   float* h = reinterpret_cast<float*>(ws);
-  const int s = down_splits(p.M, p.L, p.n, p.r, false);
+  const bool few = few_rows(p.M, p.L, p.d, p.n, p.r, false);
+  const int s = down_splits(p.M, p.n, p.r, few, false);
   const Down of{static_cast<const uint8_t*>(p.X), static_cast<const uint8_t*>(p.B), h, (int)p.n, s, nullptr};
   UpArgs y = up_args(p);
   y.H = h;
@@ -1397,13 +1404,13 @@ hipError_t fwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   DownArgs x = down_args(p);
   x.of[0] = of;
   hipError_t e;
-  if (!few_rows(p.M, p.L)) {
+  if (!few) {
     ListArgs l{};
     l.lists = x.lists = y.lists = lists_of(p, ws + w.lists);
     if ((e = make_lists(p, l, st)) != hipSuccess) return e;
   }
-  if ((e = down<TY>(x, 1, st)) != hipSuccess) return e;
-  return up<TY>(y, reinterpret_cast<uint16_t*>(ws + w.pad), st);
+  if ((e = down<TY>(x, 1, few, st)) != hipSuccess) return e;
+  return up<TY>(y, reinterpret_cast<uint16_t*>(ws + w.pad), few, st);
 }
 
 template <int TY>
@@ -1413,7 +1420,8 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   float *h = reinterpret_cast<float*>(ws), *dh = reinterpret_cast<float*>(ws + w.dh);
   uint16_t *at = reinterpret_cast<uint16_t*>(ws + w.at), *bt = reinterpret_cast<uint16_t*>(ws + w.bt);
   const uint8_t *X = static_cast<const uint8_t*>(p.X), *dY = static_cast<const uint8_t*>(p.dY);
-  const int sh = down_splits(p.M, L, n, r, true), sd = down_splits(p.M, L, d, r, true);
+  const bool few = few_rows(p.M, L, d, n, r, true);
+  const int sh = down_splits(p.M, n, r, few, true), sd = down_splits(p.M, d, r, few, true);
   uint16_t *ph = reinterpret_cast<uint16_t*>(ws + w.ph), *pdh = reinterpret_cast<uint16_t*>(ws + w.pdh);
   const Lists lists = lists_of(p, ws + w.lists);
   ListArgs l{};
@@ -1426,13 +1434,13 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   hipError_t e = make_lists(p, l, st);  // (without a row too: the lists are then empty)
   if (e != hipSuccess) return e;
   if (p.M > 0) {
-    const bool few = few_rows(p.M, p.L), split = few || sh > 1 || sd > 1;
+    const bool split = few || sh > 1 || sd > 1;
     DownArgs x = down_args(p);
     x.lists = lists;
     x.scale = p.scale;
     x.of[0] = Down{X, static_cast<const uint8_t*>(p.B), split ? h : nullptr, n, sh, split ? nullptr : ph};
     x.of[1] = Down{dY, reinterpret_cast<const uint8_t*>(at), split || p.Y ? dh : nullptr, d, sd, split ? nullptr : pdh};
-    if ((e = down<TY>(x, 2, st)) != hipSuccess) return e;
+    if ((e = down<TY>(x, 2, few, st)) != hipSuccess) return e;
     if (p.Y) {
       UpArgs y = up_args(p);
       y.lists = lists;
@@ -1441,7 +1449,7 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
       y.W = reinterpret_cast<const uint8_t*>(bt);
       y.d = n;
       y.r = y.ld = rp;  // (the padding is zeros on both sides)
-      if ((e = up<TY>(y, nullptr, st)) != hipSuccess) return e;
+      if ((e = up<TY>(y, nullptr, few, st)) != hipSuccess) return e;
     }
     if (split) {
       SplitArgs v{};
@@ -1471,16 +1479,13 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
 
 }  // namespace
 
-// Whether every launch holds: less than 2^32 work-items, at most 65535 blocks along y and z.
+// Whether every launch holds: less than 2^32 work-items, at most 65535 blocks along y and z.  (Few tokens
+// are at most 640: their blocks always do.)
 bool adapters_fit(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r) {
   const int64_t most = int64_t(1) << 32, widest = d > n ? d : n, chunks = list_chunks(M, d, n);
   const int64_t turns = ((d + 31) / 32 + (n + 31) / 32) * ((round16(r) + 31) / 32);
   if (chunks > 65535 || most_parts(M, L, d, n) > 65535) return false;
   if ((turns * L + 4) * 256 + (L + 1) * chunks * 1024 >= most || M * (round16(r) / 4) + 256 >= most) return false;
-  if (few_rows(M, L)) {
-    const int64_t tokens = (M + 15) / 16 * 16;
-    return tokens * ((widest + 127) / 128) * 256 < most && tokens * 8 * 8 * 64 * kDownWaves < most;
-  }
   const int64_t downs = most_tiles(M, L, d, n, 32) * 8 * 2 * chunks;
   const int64_t ups = most_tiles(M, L, d, n, 64) * ((widest + 1023) / 1024 + 4) * chunks;
   return downs * 256 < most && ups * 256 < most;

@@ -84,6 +84,18 @@ def test_rows(ops, M, x, r, d, n, L):
     forward(ops, make(M, L, d, n, r, x))
 
 
+@pytest.mark.parametrize("M,L,d,n,r,x,kind", [
+    (33, 1, 8192, 4096, 64, "bf16", "one"), (40, 1, 8192, 4096, 64, "bf16", "one"),
+    (25, 2, 14336, 4104, 100, "fp16", "random"), (31, 2, 14344, 4104, 101, "fp16", "random"),
+    (200, 8, 4096, 4096, 16, "bf16", "runs"), (230, 8, 4096, 4096, 16, "bf16", "runs"),
+    (150, 40, 4104, 2056, 64, "fp16", "random"), (260, 40, 4104, 2056, 64, "fp16", "random"),
+    (640, 2, 1032, 776, 20, "bf16", "random"), (640, 2, 2056, 1032, 20, "bf16", "random"),
+])
+def test_around_the_lists(ops, M, L, d, n, r, x, kind):
+    """Either side of where rows are listed first, which depends on rows, adapters, sizes and rank."""
+    forward(ops, make(M, L, d, n, r, x, kind))
+
+
 @pytest.mark.parametrize("r", [1, 2, 7, 8, 15, 17, 24, 32, 33, 48, 63, 64, 65, 100, 127, 128])
 @pytest.mark.parametrize("x,M", [("bf16", 37), ("fp16", 37), ("bf16", 1100), ("fp16", 300)])
 def test_ranks(ops, r, x, M):
@@ -164,6 +176,8 @@ def test_wide_range(ops, x, big):
     (1500, 40, 72, 136, 100, "fp16", "random"), (2100, 5, 640, 72, 20, "fp16", "runs"),
     (1100, 3, 72, 1096, 7, "bf16", "none"), (256, 2, 64, 2056, 16, "bf16", "runs"), (257, 2, 2056, 64, 16, "bf16", "runs"),
     (600, 200, 64, 72, 8, "fp16", "random"), (2000, 300, 264, 136, 9, "bf16", "runs"),
+    (64, 3, 1096, 264, 20, "fp16", "random"), (65, 3, 1096, 264, 20, "fp16", "random"), (70, 2, 2056, 1032, 64, "bf16", "runs"),
+    (100, 80, 72, 136, 17, "bf16", "random"), (250, 5, 136, 72, 128, "fp16", "one"),
 ])
 def test_gradients(ops, M, L, d, n, r, x, kind):
     c = make(M, L, d, n, r, x, kind)
