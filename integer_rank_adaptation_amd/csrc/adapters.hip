@@ -72,7 +72,7 @@ struct Lists {
 struct Turn {
   const uint16_t* in;
   uint16_t* out;
-  int rows, cols, ldo, tiles_x, tiles;  // tiles of 32 x 32: along the columns, in all
+  int rows, cols, ldo, tiles_x, tiles;  // tiles of 64 x 64: along the columns, in all
 };
 struct ListArgs {
   const int32_t* index;
@@ -81,27 +81,52 @@ struct ListArgs {
   Turn turn[2];
 };
 
+// A tile by 256 threads, 16 bytes at a time (rows of A that are no multiple of 8 long two numbers
+// at a time, odd ones one by one): 16 adapters of 4096 x 64 and 64 x 4096 11.5 us with the lists (33 MB
+// read and written; tiles of 32 x 32, a number a lane 25.5).
 __device__ __forceinline__ void turn_tile(const ListArgs& p, int unit) {
-  __shared__ uint16_t tiles[4][32][34];
+  __shared__ __attribute__((aligned(16))) uint16_t tiles[4][64][66];
   auto& t = tiles[threadIdx.x >> 8];
   const int all = p.turn[0].tiles + p.turn[1].tiles, a = unit / all, in_a = unit - a * all;
   const bool live = a < p.lists.L, second = in_a >= p.turn[0].tiles;
   const Turn& w = p.turn[second];
   const int tile = in_a - (second ? p.turn[0].tiles : 0);
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5 & 7;
-  const int64_t c0 = (int64_t)(tile % w.tiles_x) * 32, r0 = (int64_t)(tile / w.tiles_x) * 32;
+  const int y = threadIdx.x >> 3 & 31, x = (threadIdx.x & 7) * 8;
+  const int64_t c0 = (int64_t)(tile % w.tiles_x) * 64, r0 = (int64_t)(tile / w.tiles_x) * 64;
   const uint16_t* in = w.in + (int64_t)a * w.rows * w.cols;
   uint16_t* out = w.out + (int64_t)a * w.cols * w.ldo;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = r0 + y + 8 * i, c = c0 + x;
-    t[y + 8 * i][x] = live && r < w.rows && c < w.cols ? in[r * w.cols + c] : 0;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t r = r0 + y + 32 * i, c = c0 + x;
+    u4i v = u4i{0, 0, 0, 0};
+    if (live && r < w.rows && c < w.cols) {
+      const uint16_t* at = in + r * w.cols + c;
+      if (w.cols % 8 == 0) {
+        v = *reinterpret_cast<const u4i*>(at);
+      } else if (w.cols % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + 2 * e < w.cols) v[e] = *reinterpret_cast<const uint32_t*>(at + 2 * e);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < w.cols) v[e / 2] |= (uint32_t)at[e] << 16 * (e & 1);
+      }
+    }
+    uint32_t* to = reinterpret_cast<uint32_t*>(&t[y + 32 * i][x]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) to[e] = v[e];
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = c0 + y + 8 * i, c = r0 + x;
-    if (live && r < w.cols && c < w.ldo) out[r * w.ldo + c] = t[x][y + 8 * i];
+  for (int i = 0; i < 2; ++i) {
+    const int64_t r = c0 + y + 32 * i, c = r0 + x;
+    if (!live || r >= w.cols || c >= w.ldo) continue;
+    u4i v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = t[x + 2 * e][y + 32 * i] | (uint32_t)t[x + 2 * e + 1][y + 32 * i] << 16;
+    *reinterpret_cast<u4i*>(out + r * w.ldo + c) = v;  // (ldo is a multiple of 8)
   }
 }
 
@@ -1135,8 +1160,9 @@ __global__ void __launch_bounds__(256) k_parts(const PartsArgs p) {
 // rows 19 and 22, 128 rows 32 and 22; 8, 64 rows 17 and 21, 128 rows 26 and 21; 64, 128 rows 28 and 33,
 // 256 rows 45 and 36; 512, 256 rows 54 and 92.  14336 x 4096, rank 64: one, 48 rows 29 and 21; 64, 96
 // rows 47 and 58, 256 rows 97 and 78.  640 x 640, 256 rows, one: rank 16 8.8 and 15.7, rank 64 19 and
-// 19.  The gradients need lists in any case (2560 x 640, rank 20, us of all kernels: 33 rows 29 and 31,
-// 100 rows 32.5 and 31, 200 rows 42 and 33; 4096 x 4096, rank 64, 200 rows 83 and 47).
+// 19.  The gradients need lists in any case (2560 x 640, rank 20, us without the launches that both have:
+// 33 rows 13.0 and 14.5, 100 rows 16.8 and 15.4, 200 rows 24 and 15; 4096 x 4096, rank 64, 200 rows 57
+// and 21).
 bool few_rows(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   if (grads) return M <= 64;
   return M <= 640 && (d + n) * (M * r - (L < M ? L : M) * (2 * r + 48)) < 3 << 23;
@@ -1427,9 +1453,9 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
   ListArgs l{};
   l.lists = lists;
   if (p.M > 0) {
-    l.turn[0] = Turn{static_cast<const uint16_t*>(p.A), at, d, r, d, (r + 31) / 32, (r + 31) / 32 * ((d + 31) / 32)};
+    l.turn[0] = Turn{static_cast<const uint16_t*>(p.A), at, d, r, d, (r + 63) / 64, (r + 63) / 64 * ((d + 63) / 64)};
     if (p.Y)
-      l.turn[1] = Turn{static_cast<const uint16_t*>(p.B), bt, r, n, rp, (n + 31) / 32, (n + 31) / 32 * ((rp + 31) / 32)};
+      l.turn[1] = Turn{static_cast<const uint16_t*>(p.B), bt, r, n, rp, (n + 63) / 64, (n + 63) / 64 * ((rp + 63) / 64)};
   }
   hipError_t e = make_lists(p, l, st);  // (without a row too: the lists are then empty)
   if (e != hipSuccess) return e;
@@ -1483,7 +1509,7 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
 // are at most 640: their blocks always do.)
 bool adapters_fit(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r) {
   const int64_t most = int64_t(1) << 32, widest = d > n ? d : n, chunks = list_chunks(M, d, n);
-  const int64_t turns = ((d + 31) / 32 + (n + 31) / 32) * ((round16(r) + 31) / 32);
+  const int64_t turns = ((d + 63) / 64 + (n + 63) / 64) * ((round16(r) + 63) / 64);
   if (chunks > 65535 || most_parts(M, L, d, n) > 65535) return false;
   if ((turns * L + 4) * 256 + (L + 1) * chunks * 1024 >= most || M * (round16(r) / 4) + 256 >= most) return false;
   const int64_t downs = most_tiles(M, L, d, n, 32) * 8 * 2 * chunks;
