@@ -427,13 +427,14 @@ int intlora_grouped_linear_dw(int64_t M, int64_t E, int64_t d, int64_t n, int dt
 
 /* The weight gradient from X as intlora_fp8_quant_act saved it (xq, sx): dW as above of dY and of
  * the numbers the codes stand for, in dY's type (exact where X had that type; a code past fp16's
- * largest number counts as that).  n a multiple of 16.  Workspace: 2 M n bytes. */
+ * largest number counts as that).  n a multiple of 16, M n < 2^36 - 2^12 (INTLORA_ESHAPE past that:
+ * more rows go in several calls whose fp32 dW are added).  Workspace: 2 M n bytes. */
 int intlora_grouped_linear_dw_fp8(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype, const void* dY,
                                   const uint8_t* xq, const uint8_t* sx, const int64_t* offsets, void* dW, void* ws,
                                   size_t ws_bytes, void* stream);
 
 /* The numbers of intlora_fp8_quant_act's codes (M x n, dtype): code x 2^(byte - 127), rounded to
- * the type; a code past fp16's largest number gives that number, the byte 255 NaN. */
+ * the type; a code past fp16's largest number gives that number, the byte 255 NaN.  The same limits. */
 int intlora_fp8_dequant_act(int64_t M, int64_t n, int dtype, const uint8_t* xq, const uint8_t* sx, void* X,
                             void* stream);
 

@@ -360,6 +360,14 @@ int fp8_linear(const char* what, int64_t M, int64_t E, int64_t d, int64_t n, con
                        what);
 }
 
+// Codes are restored in units of 16, counted in 32 bits, a work-item each.
+int check_restore(int64_t M, int64_t n, const char* what) {
+  if (M < 0 || M >= kMaxDim || n < 1 || n > kMaxFeatures || n % 16 != 0 || M * (n / 16) >= (int64_t(1) << 32) - 256)
+    return fail(INTLORA_ESHAPE, "%s needs n a multiple of 16 and <= 2^20, M n < 2^36 - 2^12 (got M=%lld n=%lld)", what,
+                (long long)M, (long long)n);
+  return INTLORA_OK;
+}
+
 int check_act(int act, const char* what) {
   if (act == INTLORA_SILU || act == INTLORA_GELU) return INTLORA_OK;
   return fail(INTLORA_EINVAL, "%s: act must be INTLORA_SILU or INTLORA_GELU (got %d)", what, act);
@@ -938,7 +946,7 @@ int intlora_grouped_linear_dw_fp8(int64_t M, int64_t E, int64_t d, int64_t n, in
   const char* what = "grouped_linear_dw_fp8";
   int s = check_grouped(M, E, d, n, dtype, out_dtype, offsets, what);
   if (s) return s;
-  if (n % 16 != 0) return fail(INTLORA_ESHAPE, "%s needs n a multiple of 16 (got %lld)", what, (long long)n);
+  if ((s = check_restore(M, n, what))) return s;
   if (d == 0) return ok();
   if (M > 0 && (s = check_ptrs({dY, xq, sx}, what))) return s;
   if ((s = check_ptrs({dW}, what))) return s;
@@ -959,9 +967,7 @@ int intlora_fp8_dequant_act(int64_t M, int64_t n, int dtype, const uint8_t* xq, 
                             void* stream) {
   int s = check_dtype(dtype, true, "fp8_dequant_act");
   if (s) return s;
-  if (M < 0 || M >= kMaxDim || n < 1 || n > kMaxFeatures || n % 16 != 0 || M * (n / 16) >= (int64_t(1) << 32) - 256)
-    return fail(INTLORA_ESHAPE, "fp8_dequant_act needs n a multiple of 16 and <= 2^20, M n < 2^36 (got M=%lld n=%lld)",
-                (long long)M, (long long)n);
+  if ((s = check_restore(M, n, "fp8_dequant_act"))) return s;
   if (M == 0) return ok();
   if ((s = check_ptrs({xq, sx, X}, "fp8_dequant_act"))) return s;
   if ((s = check_apart({{X, M * n * (dtype == INTLORA_FP32 ? 4 : 2)}},

@@ -387,7 +387,8 @@ def grouped_linear_dx(dY, offsets, W, out=None):
 def grouped_linear_dw(dY, X, offsets, dtype=None, out=None):
     """The gradient of grouped_linear's W: dW [E, d, n] of dY [M, d] and X [M, n], in their type
     or in fp32 (dtype).  With offsets = None one group of all rows: dW [1, d, n], whose fp32
-    form is the G of ste_backward.  X may be the pair (xq, sx) that fp8_quant_act saved of it."""
+    form is the G of ste_backward.  X may be the pair (xq, sx) that fp8_quant_act saved of it, of
+    less than 2^36 - 2^12 codes."""
     M, d = _dims("dY", dY, 2)
     saved = not isinstance(X, torch.Tensor)
     if saved:
@@ -411,7 +412,8 @@ def grouped_linear_dw(dY, X, offsets, dtype=None, out=None):
 
 
 def fp8_dequant_act(xq, sx, dtype, out=None):
-    """The numbers [M, n] (bf16, fp16 or fp32) of fp8_quant_act's codes and scale bytes."""
+    """The numbers [M, n] (bf16, fp16 or fp32) of fp8_quant_act's codes and scale bytes, less than
+    2^36 - 2^12 of them."""
     M, n = _dims("xq", xq, 2)
     if dtype not in _FLOAT:
         raise ValueError(f"dtype: expected {' or '.join(map(str, _FLOAT))}, got {dtype}")
