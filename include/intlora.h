@@ -466,9 +466,10 @@ int intlora_gated_linear_dgu(int64_t M, int64_t f, int dtype, int act, const voi
  * (zeros); Y may be base (in place), and then rows without an adapter are not touched.  Sums are
  * binary32 in an order fixed by the sizes and by index (the same call gives the same bits); the term
  * B_a x keeps at least 16 significant bits on the way; one rounding at the end.  Rows of one adapter
- * may lie anywhere.  r in [1, 128], d and n
- * multiples of 8 and <= 2^20, L <= 4096, M < 2^31 (INTLORA_ESHAPE also for more tiles than a grid
- * holds).  Workspace (of both calls; 0 bytes for some sizes): intlora_adapters_ws_bytes. */
+ * may lie anywhere.  r in [1, 128], d and n multiples of 8 and <= 2^20, L <= 4096, M < 2^31
+ * (INTLORA_ESHAPE also for more tiles than a grid holds; the gradients, which transpose the factors,
+ * reach that first).  Workspace (of both calls; 0 bytes for some sizes, and for refused ones):
+ * intlora_adapters_ws_bytes. */
 size_t intlora_adapters_ws_bytes(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, int grads);
 int intlora_adapters_fwd(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, int dtype, const void* base,
                          const void* X, const int32_t* index, const void* A, const void* B, const float* scale, void* Y,

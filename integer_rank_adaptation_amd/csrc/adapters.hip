@@ -1505,13 +1505,14 @@ hipError_t bwd(const AdapterArgs& p, uint8_t* ws, hipStream_t st) {
 
 }  // namespace
 
-// Whether every launch holds: less than 2^32 work-items, at most 65535 blocks along y and z.  (Few tokens
-// are at most 640: their blocks always do.)
-bool adapters_fit(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r) {
+// Whether every launch of a call holds: less than 2^32 work-items, at most 65535 blocks along y and z.
+// (Few tokens are at most 640: their blocks always do.)  Transposes, pieces and parts are the gradients'
+// alone.
+bool adapters_fit(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   const int64_t most = int64_t(1) << 32, widest = d > n ? d : n, chunks = list_chunks(M, d, n);
-  const int64_t turns = ((d + 63) / 64 + (n + 63) / 64) * ((round16(r) + 63) / 64);
-  if (chunks > 65535 || most_parts(M, L, d, n) > 65535) return false;
-  if ((turns * L + 4) * 256 + (L + 1) * chunks * 1024 >= most || M * (round16(r) / 4) + 256 >= most) return false;
+  const int64_t turns = grads ? ((d + 63) / 64 + (n + 63) / 64) * ((round16(r) + 63) / 64) : 0;
+  if (chunks > 65535 || (turns * L + 4) * 256 + (L + 1) * chunks * 1024 >= most) return false;
+  if (grads && (most_parts(M, L, d, n) > 65535 || M * (round16(r) / 4) + 256 >= most)) return false;
   const int64_t downs = most_tiles(M, L, d, n, 32) * 8 * 2 * chunks;
   const int64_t ups = most_tiles(M, L, d, n, 64) * ((widest + 1023) / 1024 + 4) * chunks;
   return downs * 256 < most && ups * 256 < most;

@@ -375,7 +375,7 @@ int check_act(int act, const char* what) {
 
 constexpr int64_t kMaxAdapters = 4096;
 
-int check_adapters(const intlora::AdapterArgs& a, const char* what) {
+int check_adapters(const intlora::AdapterArgs& a, bool grads, const char* what) {
   int s = check_dtype(a.dtype, false, what);
   if (s) return s;
   if (a.out_dtype != a.dtype && a.out_dtype != INTLORA_FP32)
@@ -387,7 +387,7 @@ int check_adapters(const intlora::AdapterArgs& a, const char* what) {
       a.d % 8 != 0 || a.n % 8 != 0)
     return fail(INTLORA_ESHAPE, "%s: bad shape M=%lld d=%lld n=%lld (d, n multiples of 8, <= 2^20)", what,
                 (long long)a.M, (long long)a.d, (long long)a.n);
-  if (!intlora::adapters_fit(a.M, a.L, a.d, a.n, a.r)) return fail(INTLORA_ESHAPE, "%s: too many tiles", what);
+  if (!intlora::adapters_fit(a.M, a.L, a.d, a.n, a.r, grads)) return fail(INTLORA_ESHAPE, "%s: too many tiles", what);
   return INTLORA_OK;
 }
 
@@ -1020,7 +1020,7 @@ int intlora_gated_linear_dgu(int64_t M, int64_t f, int dtype, int act, const voi
 size_t intlora_adapters_ws_bytes(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, int grads) {
   intlora::AdapterArgs a{};
   a.M = M, a.L = L, a.d = d, a.n = n, a.r = r;
-  if (check_adapters(a, "adapters_ws_bytes")) return 0;
+  if (check_adapters(a, grads != 0, "adapters_ws_bytes")) return 0;
   ok();
   return intlora::adapters_ws_bytes(M, L, d, n, r, grads != 0);
 }
@@ -1032,7 +1032,7 @@ int intlora_adapters_fwd(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, 
   a.M = M, a.L = L, a.d = d, a.n = n, a.r = r;
   a.dtype = a.out_dtype = dtype;
   a.X = X, a.A = A, a.B = B, a.index = index, a.scale = scale, a.base = base, a.Y = Y;
-  int s = check_adapters(a, "adapters_fwd");
+  int s = check_adapters(a, false, "adapters_fwd");
   if (s) return s;
   if (M == 0) return ok();
   if ((s = check_ptrs({X, index, A, B, scale, Y}, "adapters_fwd")) || (s = check_opt(base, "base"))) return s;
@@ -1055,7 +1055,7 @@ int intlora_adapters_grad(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r,
   a.M = M, a.L = L, a.d = d, a.n = n, a.r = r;
   a.dtype = dtype, a.out_dtype = out_dtype;
   a.X = X, a.dY = dY, a.A = A, a.B = B, a.index = index, a.scale = scale, a.base = base, a.Y = dX, a.dA = dA, a.dB = dB;
-  int s = check_adapters(a, "adapters_grad");
+  int s = check_adapters(a, true, "adapters_grad");
   if (s) return s;
   if (base && !dX) return fail(INTLORA_EINVAL, "adapters_grad: base without dX");
   if (M > 0 && (s = check_ptrs({dY, X, index}, "adapters_grad"))) return s;  // without a row the gradients are zeros

@@ -117,7 +117,7 @@ struct AdapterArgs {
   void* Y;           // the output, or dX (NULL: not wanted)
   void *dA, *dB;
 };
-bool adapters_fit(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r);
+bool adapters_fit(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads);
 size_t adapters_ws_bytes(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads);
 hipError_t launch_adapters(const AdapterArgs& p, void* ws, hipStream_t st);
 hipError_t launch_adapters_grad(const AdapterArgs& p, void* ws, hipStream_t st);
