@@ -465,7 +465,8 @@ int intlora_gated_linear_dgu(int64_t M, int64_t f, int dtype, int act, const voi
  * base: M x d, the output of any layer (intlora_linear_fwd, intlora_fp8_linear_fwd, ...), or NULL
  * (zeros); Y may be base (in place), and then rows without an adapter are not touched.  Sums are
  * binary32 in an order fixed by the sizes and by index (the same call gives the same bits); the term
- * B_a x keeps at least 16 significant bits on the way; one rounding at the end.  Rows of one adapter
+ * B_a x keeps at least 16 significant bits on the way (fp16: ranks below 2^-20 of the token's largest
+ * 11, down to 2^-38); one rounding at the end.  Rows of one adapter
  * may lie anywhere.  r in [1, 128], d and n multiples of 8 and <= 2^20, L <= 4096, M < 2^31
  * (INTLORA_ESHAPE also for more tiles than a grid holds; the gradients, which transpose the factors,
  * reach that first).  Workspace (of both calls; 0 bytes for some sizes, and for refused ones):

@@ -7,7 +7,8 @@
 // k_down forms h (and dh, on A transposed), k_up the outputs (and dX, on B transposed), k_sums the
 // factors' gradients.  h stays in binary32; where it meets 16-bit weights on the matrix cores it
 // goes as a sum of two 16-bit numbers (16 or more significant bits, against the outputs' 8 or
-// 11), and in the sums over tokens, whose results may be binary32, as a sum of three (24 bits).
+// 11; of fp16 ranks below 2^-20 of the token's largest, 11 bits), and in the sums over tokens, whose
+// results may be binary32, as a sum of three (24 bits).
 #include "gemm_tile.h"
 
 namespace intlora {
@@ -503,10 +504,38 @@ __device__ __forceinline__ v4i row8(const uint16_t* __restrict__ row, int k, int
 // A token row's h, scaled, as the operand of the matrix cores: the sum of two 16-bit numbers each,
 // and what to multiply the sums with.  Lane l: token l % 16, ranks 32 c + 8 (l / 16) + 0 .. 7.
 // KT: steps of 32 of the rank.
+//
+// bf16 has binary32's range, and the two numbers hold 16 bits.  fp16 has not: a power of two brings the
+// token's largest number into [1/2, 1), hi is what fp16 holds of each and lo 2^24 times the rest, which
+// is at most 2^-12.  What lo leaves is 2^-12 of that rest, or 2^-49 where lo is subnormal itself; with
+// k = -log2 of the number that is 24 bits of it while hi is normal (k <= 14), then 37 - k, so 16 up to
+// k = 20, and never less than 11, fp16's own, down to k = 38.
 template <int TY, int KT>
 struct Low {
   v4i hi[KT], lo[KT];
   float back;
+
+  // sum over the ranks of weights w and h; ROWS: the tokens are the matrix instruction's rows
+  template <bool ROWS>
+  __device__ __forceinline__ v4f times(const v4i (&w)[KT]) const {
+    auto step = [&](const v4i& x, int c, v4f t) { return ROWS ? mfma<TY>(x, w[c], t) : mfma<TY>(w[c], x, t); };
+    v4f t = v4f{0.f, 0.f, 0.f, 0.f};
+    if (TY == T_FP16) {
+#pragma unroll
+      for (int c = 0; c < KT; ++c) t = step(lo[c], c, t);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] *= 0x1p-24f;
+#pragma unroll
+      for (int c = 0; c < KT; ++c) t = step(hi[c], c, t);
+    } else {
+#pragma unroll
+      for (int c = 0; c < KT; ++c) {
+        t = step(lo[c], c, t);
+        t = step(hi[c], c, t);
+      }
+    }
+    return t;
+  }
 
   __device__ __forceinline__ void read(const UpArgs& p, int64_t t, bool mine, float s) {
     fill(p, mine, s, [&](int k, float (&v)[8]) {
@@ -565,7 +594,7 @@ struct Low {
         if (TY == T_FP16) {
           t2 = pack2<T_FP16>(x, y);
           const f2 w = unpack2<T_FP16>(t2);
-          b = pack2<T_FP16>(finite(w.x) ? x - w.x : 0.f, finite(w.y) ? y - w.y : 0.f);
+          b = pack2<T_FP16>(finite(w.x) ? (x - w.x) * 0x1p24f : 0.f, finite(w.y) ? (y - w.y) * 0x1p24f : 0.f);
         } else {
           const float tx = top_bf16(x), ty = top_bf16(y);
           t2 = pack2<T_BF16>(tx, ty);
@@ -624,14 +653,7 @@ __global__ void __launch_bounds__(256) k_up_few(const UpArgs p) {
       __builtin_amdgcn_sched_barrier(0);
       v4f acc[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        acc[u] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < KT; ++c) {
-          acc[u] = mfma<TY>(cur.w[u][c], h.lo[c], acc[u]);
-          acc[u] = mfma<TY>(cur.w[u][c], h.hi[c], acc[u]);
-        }
-      }
+      for (int u = 0; u < 2; ++u) acc[u] = h.template times<false>(cur.w[u]);
       if (mine && col < p.d) {
         u4i y;
 #pragma unroll
@@ -675,11 +697,11 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_token(const Down of, const 
   const bool mine = id == a;
   if (a >= 0) {
     const uint16_t* W = reinterpret_cast<const uint16_t*>(p.W) + (int64_t)a * p.d * p.ld;
-    v4i w[2];
+    v4i w[2][1];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int row = n0 + 8 * (fr >> 2) + 4 * u + (fr & 3);
-      w[u] = row8<WIDE>(W + (int64_t)row * p.ld, row < p.d ? 8 * q : p.r, p.r);
+      w[u][0] = row8<WIDE>(W + (int64_t)row * p.ld, row < p.d ? 8 * q : p.r, p.r);
     }
     u4i b = u4i{0, 0, 0, 0};
     if (p.base && mine && col < p.d) b = *reinterpret_cast<const u4i*>(p.base + 2 * (t * p.d + col));
@@ -720,8 +742,7 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_token(const Down of, const 
     u4i y;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      v4f acc = mfma<TY>(w[u], h.lo[0], v4f{0.f, 0.f, 0.f, 0.f});
-      acc = mfma<TY>(w[u], h.hi[0], acc);
+      const v4f acc = h.template times<false>(w[u]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const f2 f = unpack2<TY>(b[2 * u + e]);
@@ -841,16 +862,14 @@ __global__ void __launch_bounds__(256) k_up(const UpArgs p) {
     v4f acc[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      v4f t = v4f{0.f, 0.f, 0.f, 0.f};
+      v4i w[KT];
 #pragma unroll
       for (int x = 0; x < KT; ++x) {
         const int k = 4 * x + q;
-        const v4i w = k < per ? *reinterpret_cast<const v4i*>(S + 16 * ((16 * u + fr) * per + (k ^ turned(fr, per))))
-                              : v4i{0, 0, 0, 0};
-        t = mfma<TY>(h.lo[x], w, t);
-        t = mfma<TY>(h.hi[x], w, t);
+        w[x] = k < per ? *reinterpret_cast<const v4i*>(S + 16 * ((16 * u + fr) * per + (k ^ turned(fr, per))))
+                       : v4i{0, 0, 0, 0};
       }
-      acc[u] = t;
+      acc[u] = h.template times<true>(w);
     }
     const int col = column(step) + 8 * fr;
 #pragma unroll
