@@ -426,9 +426,10 @@ int intlora_grouped_linear_dw(int64_t M, int64_t E, int64_t d, int64_t n, int dt
                               const void* X, const int64_t* offsets, void* dW, void* stream);
 
 /* The weight gradient from X as intlora_fp8_quant_act saved it (xq, sx): dW as above of dY and of
- * the numbers the codes stand for, in dY's type (exact where X had that type; a code past fp16's
- * largest number counts as that).  n a multiple of 16, M n < 2^36 - 2^12 (INTLORA_ESHAPE past that:
- * more rows go in several calls whose fp32 dW are added).  Workspace: 2 M n bytes. */
+ * the numbers the codes stand for, in dY's type (exact where X had that type, but below the type's
+ * normal range; a code past fp16's largest number counts as that).  n a multiple of 16, M n <
+ * 2^36 - 2^12 (INTLORA_ESHAPE past that: more rows go in several calls whose fp32 dW are added).
+ * Workspace: 2 M n bytes. */
 int intlora_grouped_linear_dw_fp8(int64_t M, int64_t E, int64_t d, int64_t n, int dtype, int out_dtype, const void* dY,
                                   const uint8_t* xq, const uint8_t* sx, const int64_t* offsets, void* dW, void* ws,
                                   size_t ws_bytes, void* stream);
@@ -442,7 +443,9 @@ int intlora_fp8_dequant_act(int64_t M, int64_t n, int dtype, const uint8_t* xq, 
  * rows and then the up projection's f rows of n columns, E x 2 f x n, and
  *   [G | U][t, :] = W_e X[t, :],  H[t, :] = act(G[t, :]) U[t, :]
  * in one pass: act INTLORA_SILU, g / (1 + e^-g), or INTLORA_GELU, g P(g) with the normal
- * distribution function P.  H: M x f, formed from the binary32 sums with one rounding; GU: M x 2 f,
+ * distribution function P (not its tanh form); the factor beside g counts as 0 below 2^-126.  The
+ * projections have no bias, and the gate's rows come first (a layer that keeps them behind the up's
+ * has to swap them).  H: M x f, formed from the binary32 sums with one rounding; GU: M x 2 f,
  * both projections for the backward pass, or NULL.  f and n multiples of 8.  The down projection
  * is intlora_grouped_linear_fwd on H. */
 enum { INTLORA_SILU = 0, INTLORA_GELU = 1 };
@@ -466,10 +469,11 @@ int intlora_gated_linear_dgu(int64_t M, int64_t f, int dtype, int act, const voi
  * (zeros); Y may be base (in place), and then rows without an adapter are not touched.  Sums are
  * binary32 in an order fixed by the sizes and by index (the same call gives the same bits); the term
  * B_a x keeps at least 16 significant bits on the way (fp16: ranks below 2^-20 of the token's largest
- * 11, down to 2^-38); one rounding at the end.  Rows of one adapter
- * may lie anywhere.  r in [1, 128], d and n multiples of 8 and <= 2^20, L <= 4096, M < 2^31
- * (INTLORA_ESHAPE also for more tiles than a grid holds; the gradients, which transpose the factors,
- * reach that first).  Workspace (of both calls; 0 bytes for some sizes, and for refused ones):
+ * 11, down to 2^-38); one rounding at the end.  What is not finite stays in its row (X, base) or with
+ * its adapter (A, B, scale); an infinity there may come out as NaN.  Rows of one adapter may lie
+ * anywhere.  r in [1, 128], d and n multiples of 8 and <= 2^20, L <= 4096, M < 2^31 (INTLORA_ESHAPE
+ * also for more tiles than a grid holds; the gradients, which transpose the factors, reach that
+ * first).  Workspace (of both calls; 0 bytes for some sizes, and for refused ones):
  * intlora_adapters_ws_bytes. */
 size_t intlora_adapters_ws_bytes(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, int grads);
 int intlora_adapters_fwd(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, int dtype, const void* base,

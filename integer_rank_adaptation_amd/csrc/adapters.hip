@@ -132,7 +132,9 @@ __device__ __forceinline__ void turn_tile(const ListArgs& p, int unit) {
 }
 
 // A block for each group: it counts all rows by adapter in LDS, which gives its first place and
-// tiles, and then lists its own.  Bound by latency: 8192 rows of 16 adapters 7.2 us.
+// tiles, and then lists its own.  Bound by latency for few adapters: 8192 rows of 16 7.2 us.  As every
+// block counts all rows, the work is that of rows x adapters: 8192 rows of 512 and 4096 adapters 14 and
+// 83 us, 32768 rows 30 and 192, where it is the longest kernel of the call; 641 rows of 4096 71.
 constexpr int kMaxGroups = 4096 + 1;
 
 __global__ void __launch_bounds__(1024) k_lists(const ListArgs p) {
@@ -312,7 +314,8 @@ struct DownArgs {
 // first of its adapter in the tile: it takes all of that adapter's tokens there.  Its eight waves take
 // runs of 64 columns in turn, and their sums meet in LDS, where they are added in order.  Lane l holds
 // token l % 16 and ranks 4 (l / 16) + 0 .. 3.  Rows of other adapters read as zeros and are not
-// written.  64 adapters of rank 64, n = 4096, a token each 9.0 us (3.7 TB/s; four waves a block 11.5).
+// written.  64 adapters of rank 64, n = 4096, a token each 10.3 us (34 MB, 3.3 TB/s; four waves a block
+// 12.1).
 constexpr int kDownWaves = 8;
 
 template <int TY>
@@ -611,7 +614,8 @@ struct Low {
 //
 // For few tokens: a block for each token of a tile of 16 (as k_down_few), its four waves 32 columns
 // in turn.  Bound by the factors' bytes: the next columns' weights are loaded while these are at
-// work, the first ones before h is there (64 adapters of 14336 x 64, a token each 23.4 us, 5.0 TB/s).
+// work, the first ones before h is there (64 adapters of 14336 x 64, a token each 28.5 us: 121 MB, 4.2
+// TB/s).
 template <int TY, int KT, bool WIDE>
 __global__ void __launch_bounds__(256) k_up_few(const UpArgs p) {
   const int lane = threadIdx.x & 63, fr = lane & 15, q = lane >> 4;
@@ -1181,7 +1185,11 @@ __global__ void __launch_bounds__(256) k_parts(const PartsArgs p) {
 // rows 47 and 58, 256 rows 97 and 78.  640 x 640, 256 rows, one: rank 16 8.8 and 15.7, rank 64 19 and
 // 19.  The gradients need lists in any case (2560 x 640, rank 20, us without the launches that both have:
 // 33 rows 13.0 and 14.5, 100 rows 16.8 and 15.4, 200 rows 24 and 15; 4096 x 4096, rank 64, 200 rows 57
-// and 21).
+// and 21).  At 640 rows the rule stops, and from there to about as many rows as 2 to 4 times the
+// adapters those without lists would still be faster where there are hundreds (4096 x 4096, without and
+// with lists: rank 16, 512 adapters, 641 rows 37 and 92, 1024 50 and 106, 2048 91 and 94; 2048 adapters,
+// 641 rows 39 and 154, 4096 204 and 270; rank 64, 512, 641 rows 110 and 147, 2048, 641 rows 129 and 237,
+// 2048 rows 333 and 394, 4096 rows 622 and 464).
 bool few_rows(int64_t M, int64_t L, int64_t d, int64_t n, int64_t r, bool grads) {
   if (grads) return M <= 64;
   return M <= 640 && (d + n) * (M * r - (L < M ? L : M) * (2 * r + 48)) < 3 << 23;
@@ -1208,7 +1216,9 @@ int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // Splits of the columns in k_down (and k_down_few): where its blocks are fewer than the compute units,
-// with at least two runs of 64 columns for each wave, or 1024 columns for a block.  The forward's tiles
+// with at least two runs of 64 columns for each wave, or 1024 columns for a block.  Few tokens count
+// every token's blocks, of which only those of the first of its adapter in a tile have work (one
+// adapter, 64 rows, rank 64: 256 counted, 16 at work, and so no split).  The forward's tiles
 // go for two blocks to a unit, which evens out a last tile more than units (8192 x 4096, rank
 // 64, 262 tiles: 31.7 us, in two splits 27.7); in the gradients one split saves k_split's launch.
 int down_splits(int64_t M, int64_t n, int64_t r, bool few, bool grads) {
@@ -1262,7 +1272,8 @@ hipError_t up_few(const UpArgs& a, dim3 grid, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Columns of a block: at least `want` working blocks where there are columns for them.
+// Columns of a block: at least `want` blocks where there are columns for them.  tiles: without the partly
+// filled ones that adapters add; for few tokens one each token, as in down_splits.
 int64_t up_chunk(int64_t tiles, int64_t d, int64_t want) {
   int64_t chunk = 1024;
   while (chunk > 128 && tiles * ((d + chunk - 1) / chunk) < want) chunk /= 2;
@@ -1339,7 +1350,9 @@ hipError_t sums(SumArgs a, const AdapterArgs& p, float* ws, hipStream_t st) {
 
 // One launch: one rank tile, B_a small, and no more blocks than compute units (one token, 4096 columns,
 // rank 16, us of the kernels alone: n = 640 4.7, in two launches 6.6; 2560 6.7 and 7.1; 4096 7.7 and
-// 7.1, but a call 9.8 and 13.9 with its host side; rank 64 with n = 640 would be 9.1 and 7.5).
+// 7.1, but a call 9.8 and 13.9 with its host side; rank 64 with n = 640 would be 9.1 and 7.5).  Wider rows
+// lose more than the host's side saves in a graph, where it does not count: n = 5120 9.0 and 7.4, 8192
+// 11.8 and 7.5, 14336 18.4 and 8.1.  Blocks are counted as in down_splits.
 bool in_one(int64_t M, int64_t d, int64_t n, int64_t r) {
   return r <= 16 && n <= 4096 && M * ((d + kTokenCols - 1) / kTokenCols) <= 256;
 }

@@ -436,8 +436,8 @@ def _act(act):
 
 def gated_linear(X, offsets, W, act="silu", save=False, out=None):
     """H [M, f] = act(G) * U with [G | U] = X W[e]^T for the rows of each group, X [M, n], W [E, 2f, n]
-    (bf16 or fp16; the gate's f rows first; offsets as grouped_linear, None with E = 1).  act:
-    "silu", or "gelu" by the normal distribution function.  With `save` also [G | U] as GU [M, 2f]
+    (bf16 or fp16; the gate's f rows first, no bias; offsets as grouped_linear, None with E = 1).
+    act: "silu", or "gelu" by the normal distribution function.  With `save` also [G | U] as GU [M, 2f]
     for gated_linear_dgu: (H, GU).  out: the tensor, or the pair.  Rows in no group are left as
     they are in `out`; without `out` they are not initialised."""
     M, n = _dims("X", X, 2)
